@@ -364,6 +364,149 @@ GDN_API gdn_status gdn_project_out(const gdn_config* cfg, const void* o, int32_t
                                    int32_t hidden, void* y, gdn_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * The other layer of the hybrid stack: rotary positions, a paged 4-bit
+ * key/value cache and causal attention over it ("Qwen RoPE", DS4Server issue
+ * #95, Implementation; mRoPE, Qwen3.8-27B FP8 Core AI model card; the KV cache
+ * kept apart from the recurrent state, issue #88, Scope).
+ *
+ * Rows.  q, k, v and q_out are [T, heads, D] in the io dtype with the heads of
+ *   a token contiguous and `ld` elements between tokens, so that they may be
+ *   slices of a projection's rows.  Rows and ld are 16-byte aligned,
+ *   ld >= heads * D.  Outputs do not overlap inputs unless stated.
+ *
+ * Rotary positions.  A plan, filled on the host by gdn_rope_plan_init and
+ *   passed by address (copied at the call), rotates the first rotary_dim (R)
+ *   channels of a head in the pairs (j, j + R/2), j < R/2:
+ *     x'_j = x_j cos a - x_{j+R/2} sin a,  x'_{j+R/2} = x_{j+R/2} cos a + x_j sin a,
+ *     a = positions[axis_j][t] * f_j.
+ *   num_axes (1 .. 3) axes share the pairs; sections[i] of them go to axis i
+ *   (they sum to R/2; NULL: all to axis 0, num_axes 1):
+ *     GDN_ROPE_SECTIONS     axis 0's pairs first, then axis 1's, then axis 2's;
+ *                           f_j = theta^(-2j/R)
+ *     GDN_ROPE_INTERLEAVED  pair j goes to axis j % 3 while j < 3 * sections[j % 3] and
+ *                           j % 3 < num_axes, else to axis 0; f_j = theta^(-2j/R).
+ *                           Axis 0 takes what the others leave.
+ *     GDN_ROPE_PER_AXIS     as SECTIONS, each axis with its own ladder:
+ *                           f = theta^(-i/sections[axis]), i = index within the section
+ *   inv_freq, when not NULL, gives the R/2 values f_j instead (scaled ladders);
+ *   theta is then ignored.  0 <= f_j <= 2 pi.  R is even, 0 .. 2 * GDN_ROPE_MAX_PAIRS.
+ *   Angles are exact to 2^-33 turns at any int32 position, cosine and sine
+ *   rounded to fp32, the products and sums to fp32 one by one, the result to
+ *   the io dtype.
+ *
+ * gdn_rope: out = x rotated, [T, num_heads, head_dim]; head_dim a multiple of
+ *   8 up to 256.  positions [num_axes, T] int32, any values.  inverse != 0
+ *   rotates back, which is also the gradient of the forward rotation.  out may
+ *   be x with the same ld.
+ *
+ * Cache.  pool holds num_pages pages of gdn_kv_page_bytes() bytes (16-byte
+ *   aligned); sequence n's tokens [i * page_size, (i+1) * page_size) live in
+ *   page page_table[n * pages_per_seq + i].  kv_lens[n] is the length of
+ *   sequence n with the call's own tokens: packed token t of sequence n has
+ *   the cache position kv_lens[n] - (cu_seqlens[n + 1] - t).  The same arrays
+ *   serve append and attention.  A token with a negative position (as in a
+ *   padding row, kv_lens 0) is not stored and sees no key.  A position past
+ *   the table's row, or a page id outside the pool, is an error found on the
+ *   device: it is skipped and gdn_get_device_status reports 4.
+ *   Codes: keys in groups of 64 channels, values in groups of min(D, 128), each
+ *   group with bias = bf16(min) and scale = bf16((max - min) * fl32(1/15)), and
+ *   code = clamp(rint((x - bias) / scale), 0, 15) standing for scale * code + bias
+ *   (every step in fp32; scale 0: code 0).  A group with a value, or a range,
+ *   that is not finite reads back as NaN.  The bytes of a page are the library's.
+ *
+ * gdn_kv_append: rotates q and k by plan (NULL: no rotation), writes q to
+ *   q_out and the quantised k and v into the cache.  positions as for gdn_rope,
+ *   or NULL: every axis takes the cache position.  q and q_out may be NULL
+ *   together; q_out may be q with the same ld.  Two tokens of one call must not
+ *   share a cache position (as with one page under two sequences).
+ * gdn_kv_read: what the cache holds for the call's tokens, k_out and v_out
+ *   [T, Hkv, D] dense (a token that is not stored reads as zeros).
+ * gdn_attention: o [T, Hq, D] dense, from query token t over the positions up
+ *   to its own: o = sum_p softmax(softmax_scale q . k_p) v_p, query head h
+ *   reading key/value head h / (Hq / Hkv).  A query that sees no key gets o = 0.
+ *   lse (fp32 [T, Hq], may be NULL): log of the sum of the exponentials, -inf
+ *   where nothing is seen.  One token a sequence is a decode step, a few are a
+ *   draft to verify, many a prefill chunk; sequences may mix.
+ *   Workspace: gdn_attention_workspace_size() bytes for the same (cfg, total
+ *   tokens, num_seqs), 256-byte aligned; it needs no initial contents and holds
+ *   nothing between calls, so calls that may run at the same time need one each.
+ *   kv_lens and page_table are read on the device only, so a captured call
+ *   follows their contents; cu_seqlens is fixed by the host copy.
+ *
+ * D in {64, 128, 256}, Hq % Hkv == 0, page_size a multiple of 16 up to 1024.
+ * T_tot = 0 launches nothing.  cu_seqlens as for gdn_prefill.
+ */
+#define GDN_ROPE_MAX_PAIRS 128
+typedef enum { GDN_ROPE_SECTIONS = 0, GDN_ROPE_INTERLEAVED = 1, GDN_ROPE_PER_AXIS = 2 } gdn_rope_layout;
+typedef struct {
+  int32_t rotary_dim;                /* R */
+  int32_t num_axes;
+  uint8_t axis[GDN_ROPE_MAX_PAIRS];  /* axis of pair j */
+  uint64_t turn[GDN_ROPE_MAX_PAIRS]; /* f_j / (2 pi) * 2^64 */
+} gdn_rope_plan;
+
+typedef struct {
+  int32_t num_q_heads;  /* Hq */
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* D */
+  int32_t page_size;    /* tokens a page */
+  float softmax_scale;
+  int32_t io_dtype;     /* gdn_dtype of q, k, v, q_out, k_out, v_out, o */
+} gdn_attn_config;
+
+typedef struct {
+  void* pool;                /* [num_pages] pages of gdn_kv_page_bytes() */
+  const int32_t* page_table; /* [num_seqs, pages_per_seq], device */
+  const int32_t* kv_lens;    /* [num_seqs], device */
+  int32_t num_pages;
+  int32_t pages_per_seq;
+} gdn_kv_cache;
+
+GDN_API gdn_status gdn_rope_plan_init(int32_t rotary_dim, double theta, const double* inv_freq, int32_t num_axes,
+                                      const int32_t* sections, int32_t layout, gdn_rope_plan* plan);
+GDN_API gdn_status gdn_rope(const gdn_rope_plan* plan, int32_t io_dtype, const void* x, int64_t ldx,
+                            const int32_t* positions, int32_t num_tokens, int32_t num_heads, int32_t head_dim,
+                            int32_t inverse, void* out, int64_t ldo, gdn_stream_t stream);
+GDN_API gdn_status gdn_kv_page_bytes(const gdn_attn_config* cfg, size_t* bytes);
+GDN_API gdn_status gdn_kv_append(const gdn_attn_config* cfg, const gdn_rope_plan* plan, const void* q, int64_t ldq,
+                                 const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* positions,
+                                 const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t num_seqs,
+                                 const gdn_kv_cache* cache, void* q_out, int64_t ldqo, gdn_stream_t stream);
+GDN_API gdn_status gdn_kv_read(const gdn_attn_config* cfg, const int32_t* cu_seqlens_dev,
+                               const int32_t* cu_seqlens_host, int32_t num_seqs, const gdn_kv_cache* cache,
+                               void* k_out, void* v_out, gdn_stream_t stream);
+GDN_API gdn_status gdn_attention_workspace_size(const gdn_attn_config* cfg, int64_t total_tokens, int32_t num_seqs,
+                                                size_t* bytes);
+GDN_API gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int64_t ldq,
+                                 const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t num_seqs,
+                                 const gdn_kv_cache* cache, void* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, gdn_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Projections with 4-bit weights, group scales and biases ("Q4", issue #88,
+ * Scope; affine Q4 weights, issue #95, implementation comment):
+ *   Y[m, n] = sum_k X[m, k] * w[n, k],  w[n, k] = scale[n, k / group] * code[n, k] + bias[n, k / group]
+ * group is 32, 64 or 128; K a positive multiple of 8, M, N >= 0.  X [M, K] and
+ * Y [M, N] are dense in io_dtype; sums are fp32.
+ *
+ * gdn_q4_pack: lays a weight out once for gdn_linear_q4.  codes
+ *   [N, G * group / 2] bytes (G = ceil(K / group)): channel 2i in the low half
+ *   of byte i, codes past K ignored; scales, biases [N, G] bf16.  packed:
+ *   gdn_q4_packed_bytes() bytes, 16-byte aligned.
+ * gdn_linear_q4: workspace gdn_linear_q4_workspace_size() bytes for the same
+ *   (M, N, K, group, io_dtype), 256-byte aligned (NULL when that is 0); it needs
+ *   no initial contents and holds nothing between calls, so calls that may run
+ *   at the same time need one each. */
+GDN_API gdn_status gdn_q4_packed_bytes(int32_t N, int32_t K, int32_t group, size_t* bytes);
+GDN_API gdn_status gdn_q4_pack(const void* codes, const void* scales, const void* biases, int32_t N, int32_t K,
+                               int32_t group, void* packed, gdn_stream_t stream);
+GDN_API gdn_status gdn_linear_q4_workspace_size(int32_t M, int32_t N, int32_t K, int32_t group, int32_t io_dtype,
+                                                size_t* bytes);
+GDN_API gdn_status gdn_linear_q4(int32_t io_dtype, const void* x, int32_t M, int32_t K, const void* packed, int32_t N,
+                                 int32_t group, void* y, void* workspace, size_t workspace_bytes,
+                                 gdn_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * Versioned state checkpoint of one sequence ("Persist every GDN convolution
  * and recurrent component in session checkpoints with versioned validation",
  * issue #95, Implementation; "identical ... BF16 convolution bytes, and fp32
@@ -392,8 +535,9 @@ GDN_API gdn_status gdn_state_restore(const gdn_config* cfg, const void* blob, si
  *
  * gdn_get_device_status: reads and clears the device status word, which a
  * kernel sets (never traps) when an internal wait reaches its time limit, or
- * a state slot index lies past its pool.  0 = clean.  The low byte is the
- * code (1 wait timeout, 3 slot past the pool); the bits above it, when set,
+ * a state slot index lies past its pool, or a cache position has no page.
+ * 0 = clean.  The low byte is the code (1 wait timeout, 3 slot past the pool,
+ * 4 cache position without a page); the bits above it, when set,
  * are the gdn_kernel_id of the kernel that reported it.  The first report
  * since the last read is kept.  Synchronises the stream.
  * gdn_last_error: message of the calling thread's last failed call.
@@ -439,7 +583,14 @@ typedef enum {
   GDN_K_WY_CONV = 15,     /* chunked prefill (affine chunk maps), stage 1: conv + SiLU + L2 norm of every token */
   GDN_K_WY_PREP = 16,     /* stage 2: per-(tile, value head) operands: T by tensor-core doubling, M', Q', U, P, K~ */
   GDN_K_WY_CHAIN = 17,    /* stage 3: the state carry (one M' S product per chunk) and the output rows */
-  GDN_K_COUNT = 18
+  GDN_K_ROPE = 18,        /* gdn_rope */
+  GDN_K_KV_APPEND = 19,   /* gdn_kv_append: rotation, 4-bit codes, cache write */
+  GDN_K_KV_READ = 20,     /* gdn_kv_read */
+  GDN_K_ATTENTION = 21,   /* attention over the 4-bit cache */
+  GDN_K_ATTN_COMBINE = 22, /* its partial rows joined */
+  GDN_K_Q4_PACK = 23,     /* gdn_q4_pack */
+  GDN_K_LINEAR_Q4 = 24,   /* product with 4-bit weights */
+  GDN_K_COUNT = 25
 } gdn_kernel_id;
 
 GDN_API const char* gdn_kernel_name(int32_t kernel_id);

@@ -21,7 +21,9 @@ __all__ = [
     "prefill", "prefill_noalloc", "decode_step", "decode_multi", "decode_step_indexed", "decode_multi_indexed",
     "prefill_indexed_workspace_size", "prefill_indexed", "gemm_bf16", "project_in", "project_out", "prefill_seqpar_workspace_size", "prefill_seqpar", "state_blob_size", "state_save", "state_restore", "device_status", "debug_wait_expiry", "last_error",
     "abi_version", "launch_count", "launch_count_reset", "profiler_enable", "profiler_reset", "profiler_read",
-    "kernel_name", "EXPORTS", "ZERO_INIT_STATE", "ZERO_INIT_CONV", "PREFILL_RECURRENT", "PREFILL_FUSED", "PREFILL_FACTORED", "PREFILL_AFFINE", "K", "MAX_DRAFT_TOKENS",
+    "kernel_name", "AttnConfig", "RopePlan", "Q4Weight", "make_attn_config", "rope_plan", "rope", "kv_page_bytes",
+    "kv_append", "kv_read", "attention_workspace_size", "attention", "q4_pack", "linear_q4_workspace_size", "linear_q4",
+    "EXPORTS", "ZERO_INIT_STATE", "ZERO_INIT_CONV", "PREFILL_RECURRENT", "PREFILL_FUSED", "PREFILL_FACTORED", "PREFILL_AFFINE", "K", "MAX_DRAFT_TOKENS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -44,8 +46,9 @@ STATUS = {0: "GDN_OK", -1: "GDN_E_INVAL", -2: "GDN_E_UNSUPPORTED", -3: "GDN_E_WO
 class K:
     """Kernel ids of the profiler (gdn_kernel_id)."""
     (CONV_PREFILL, CONV_STEP, CONV_HISTORY, SCHEDULE, PREFILL_RECURRENT, PREFILL_CHUNKED, DECODE, STATE_CHECKSUM,
-     SPLIT_CONV, SPLIT_PREP, SPLIT_CHAIN, SLOT_COPY, GEMM, SEQPAR, DIAG, WY_CONV, WY_PREP, WY_CHAIN) = range(18)
-    COUNT = 18
+     SPLIT_CONV, SPLIT_PREP, SPLIT_CHAIN, SLOT_COPY, GEMM, SEQPAR, DIAG, WY_CONV, WY_PREP, WY_CHAIN, ROPE, KV_APPEND,
+     KV_READ, ATTENTION, ATTN_COMBINE, Q4_PACK, LINEAR_Q4) = range(25)
+    COUNT = 25
 
 
 # Every symbol include/gdn.h declares.
@@ -57,6 +60,9 @@ EXPORTS = [
     "gdn_decode_step_indexed", "gdn_decode_multi_indexed", "gdn_prefill_indexed_workspace_size",
     "gdn_prefill_indexed", "gdn_gemm_bf16", "gdn_project_in", "gdn_project_out",
     "gdn_prefill_seqpar_workspace_size", "gdn_prefill_seqpar", "gdn_debug_wait_expiry",
+    "gdn_rope_plan_init", "gdn_rope", "gdn_kv_page_bytes", "gdn_kv_append", "gdn_kv_read",
+    "gdn_attention_workspace_size", "gdn_attention", "gdn_q4_packed_bytes", "gdn_q4_pack",
+    "gdn_linear_q4_workspace_size", "gdn_linear_q4",
 ]
 
 
@@ -76,6 +82,25 @@ class Config(ctypes.Structure):
 class Params(ctypes.Structure):
     _fields_ = [("conv_w", ctypes.c_void_p), ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
                 ("norm_w", ctypes.c_void_p)]
+
+
+ROPE_MAX_PAIRS = 128
+ROPE_LAYOUTS = {"sections": 0, "interleaved": 1, "per_axis": 2}
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
+                ("turn", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("io_dtype", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32)]
 
 
 _lib = None
@@ -107,6 +132,17 @@ def lib():
             "gdn_project_out": [P, P, I32, P, I32, P, P],
             "gdn_prefill_seqpar_workspace_size": [P, I64, I32, P],
             "gdn_prefill_seqpar": [P, P, P, P, P, P, I64, I32, U32, P, P, P, P, SZ, P, P],
+            "gdn_rope_plan_init": [I32, ctypes.c_double, P, I32, P, I32, P],
+            "gdn_rope": [P, I32, P, I64, P, I32, I32, I32, I32, P, I64, P],
+            "gdn_kv_page_bytes": [P, P],
+            "gdn_kv_append": [P, P, P, I64, P, I64, P, I64, P, P, P, I32, P, P, I64, P],
+            "gdn_kv_read": [P, P, P, I32, P, P, P, P],
+            "gdn_attention_workspace_size": [P, I64, I32, P],
+            "gdn_attention": [P, P, I64, P, P, I32, P, P, P, P, SZ, P],
+            "gdn_q4_packed_bytes": [I32, I32, I32, P],
+            "gdn_q4_pack": [P, P, P, I32, I32, I32, P, P],
+            "gdn_linear_q4_workspace_size": [I32, I32, I32, I32, I32, P],
+            "gdn_linear_q4": [I32, P, I32, I32, P, I32, I32, P, P, SZ, P],
             "gdn_state_blob_size": [P, P],
             "gdn_state_save": [P, P, P, I32, P, SZ, P],
             "gdn_state_restore": [P, P, SZ, I32, P, P, P],
@@ -305,6 +341,207 @@ def prefill_seqpar(cfg, params, qkv, z, a, b, total_tokens, segments, flags, con
                                     segments, flags, _p(conv_state), _p(state), _p(o), _p(workspace),
                                     workspace_bytes, ctypes.byref(used), _stream(stream)))
     return used.value
+
+
+# ---------------------------------------------------------------- attention side and 4-bit projections
+# These calls take tensors whose layout the C entry points cannot see, so the
+# binding checks what it can (device, type, shape, strides) before it passes
+# pointers on.  All tensors live on the current CUDA device.
+
+
+def _need(ok: bool, message: str):
+    if not ok:
+        raise GdnError(-1, message)
+
+
+def _io(dtype) -> int:
+    name = str(dtype)
+    if name in ("torch.bfloat16", "bf16"):
+        return BF16
+    if name in ("torch.float32", "f32"):
+        return F32
+    raise GdnError(-2, f"io type {name} is not bf16 or float32")
+
+
+def _device(t, stream):
+    """(current device, raw stream); t is on that device."""
+    import torch
+    _need(t.is_cuda, "tensors must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, _stream(stream)
+    return dev, torch.cuda.current_stream().cuda_stream
+
+
+def _ptr(t, dev: int, name: str, dtype: str, numel: Optional[int] = None) -> int:
+    """Pointer of a contiguous tensor of a type (and, if given, at least numel elements) on device dev."""
+    if t.get_device() != dev or str(t.dtype) != dtype or not t.is_contiguous():
+        raise GdnError(-1, f"{name} must be a contiguous {dtype} tensor on device {dev}")
+    if numel is not None and t.numel() < numel:
+        raise GdnError(-1, f"{name} has {t.numel()} elements, {numel} are needed")
+    return t.data_ptr()
+
+
+def _heads(t, dev: int, name: str, io: int, T: int, H: int, D: int):
+    """(pointer, elements between tokens) of rows [T, H, D] whose heads are contiguous within a token."""
+    if (t.get_device() != dev or tuple(t.shape) != (T, H, D)
+            or str(t.dtype) != ("torch.bfloat16" if io == BF16 else "torch.float32")):
+        raise GdnError(-1, f"{name} must be [{T}, {H}, {D}] in the io type on device {dev}, got {list(t.shape)} {t.dtype}")
+    st = t.stride()
+    if T > 0 and (st[2] != 1 or (H > 1 and st[1] != D)):
+        raise GdnError(-1, f"{name}: a token's heads must be contiguous (strides {st})")
+    return t.data_ptr(), st[0] if T > 1 else max(st[0], H * D)
+
+
+def _cu_host(cu_host) -> np.ndarray:
+    if type(cu_host) is np.ndarray and cu_host.dtype == np.int32 and cu_host.flags.c_contiguous:
+        return cu_host
+    return _host_cu(cu_host)
+
+
+def _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table) -> KvCache:
+    n = cu_h.size - 1
+    _need(n >= 1, "cu_seqlens needs two entries or more")
+    _ptr(cu_dev, dev, "cu_seqlens", "torch.int32", n + 1)
+    _need(page_table.dim() == 2 and page_table.shape[0] >= n, "page_table must be [num_seqs, pages_per_seq]")
+    _need(pool.dim() == 2 and pool.shape[1] == kv_page_bytes(cfg), "pool must be [num_pages, kv_page_bytes]")
+    return KvCache(_ptr(pool, dev, "pool", "torch.uint8"), _ptr(page_table, dev, "page_table", "torch.int32"),
+                   _ptr(kv_lens, dev, "kv_lens", "torch.int32", n), pool.shape[0], page_table.shape[1])
+
+
+def make_attn_config(num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int = 64, io_dtype="bf16",
+                     softmax_scale: Optional[float] = None) -> AttnConfig:
+    """gdn_attn_config; softmax_scale defaults to head_dim ** -0.5."""
+    return AttnConfig(num_q_heads, num_kv_heads, head_dim, page_size,
+                      head_dim ** -0.5 if softmax_scale is None else softmax_scale, _io(io_dtype))
+
+
+def rope_plan(rotary_dim: int, theta: float = 10000.0, sections=None, layout: str = "sections",
+              inv_freq=None) -> RopePlan:
+    """gdn_rope_plan_init: the rotation of the first rotary_dim channels.  sections: pairs of each axis (1 to 3 of
+    them, None = one axis); layout "sections", "interleaved" or "per_axis"; inv_freq: rotary_dim / 2 frequencies in
+    radians per position in place of theta's."""
+    _need(layout in ROPE_LAYOUTS, f"layout {layout!r} is none of {sorted(ROPE_LAYOUTS)}")
+    plan = RopePlan()
+    sec = None if sections is None else np.ascontiguousarray(sections, np.int32)
+    _need(sec is None or sec.ndim == 1, "sections is a flat list")
+    inv = None if inv_freq is None else np.ascontiguousarray(inv_freq, np.float64)
+    _need(inv is None or inv.shape == (rotary_dim // 2,), f"inv_freq must have {rotary_dim // 2} values")
+    _check(lib().gdn_rope_plan_init(rotary_dim, theta, _p(inv), 1 if sec is None else sec.size, _p(sec),
+                                    ROPE_LAYOUTS[layout], ctypes.byref(plan)))
+    return plan
+
+
+def _positions(plan, positions, dev, T: int) -> int:
+    _need(tuple(positions.shape) == (plan.num_axes, T) or (plan.num_axes == 1 and tuple(positions.shape) == (T,)),
+          f"positions must be [{plan.num_axes}, {T}], got {list(positions.shape)}")
+    return _ptr(positions, dev, "positions", "torch.int32")
+
+
+def rope(plan, x, positions, out, inverse: bool = False, stream=None):
+    """gdn_rope: out = x [T, heads, head_dim] rotated (out may be x); positions [axes, T] int32."""
+    dev, st = _device(x, stream)
+    _need(x.dim() == 3, "x must be [tokens, heads, head_dim]")
+    io, (T, H, D) = _io(x.dtype), x.shape
+    px, ldx = _heads(x, dev, "x", io, T, H, D)
+    po, ldo = _heads(out, dev, "out", io, T, H, D)
+    _check(lib().gdn_rope(ctypes.byref(plan), io, px, ldx, _positions(plan, positions, dev, T), T, H, D,
+                          1 if inverse else 0, po, ldo, st))
+
+
+def kv_page_bytes(cfg) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().gdn_kv_page_bytes(ctypes.byref(cfg), ctypes.byref(out)))
+    return out.value
+
+
+def kv_append(cfg, plan, q, k, v, positions, cu_dev, cu_host, kv_lens, pool, page_table, q_out, stream=None):
+    """gdn_kv_append: q [T, Hq, D] rotated into q_out, k and v [T, Hkv, D] into the 4-bit cache (k rotated).  plan None:
+    no rotation; positions None: the cache positions; q and q_out may be None."""
+    dev, st = _device(k, stream)
+    cu_h = _cu_host(cu_host)
+    T, io = int(cu_h[-1]), cfg.io_dtype
+    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
+    pk, ldk = _heads(k, dev, "k", io, T, cfg.num_kv_heads, cfg.head_dim)
+    pv, ldv = _heads(v, dev, "v", io, T, cfg.num_kv_heads, cfg.head_dim)
+    pq, ldq = (None, 0) if q is None else _heads(q, dev, "q", io, T, cfg.num_q_heads, cfg.head_dim)
+    po, ldo = (None, 0) if q_out is None else _heads(q_out, dev, "q_out", io, T, cfg.num_q_heads, cfg.head_dim)
+    _check(lib().gdn_kv_append(ctypes.byref(cfg), None if plan is None else ctypes.byref(plan), pq, ldq, pk, ldk, pv,
+                               ldv, None if positions is None or plan is None else _positions(plan, positions, dev, T),
+                               cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1, ctypes.byref(c), po, ldo, st))
+
+
+def kv_read(cfg, cu_dev, cu_host, kv_lens, pool, page_table, k_out, v_out, stream=None):
+    """gdn_kv_read: the cache's values for the last tokens of each sequence, k_out and v_out [T, Hkv, D]."""
+    dev, st = _device(pool, stream)
+    cu_h = _cu_host(cu_host)
+    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
+    dt = "torch.bfloat16" if cfg.io_dtype == BF16 else "torch.float32"
+    need = int(cu_h[-1]) * cfg.num_kv_heads * cfg.head_dim
+    _check(lib().gdn_kv_read(ctypes.byref(cfg), cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1, ctypes.byref(c),
+                             _ptr(k_out, dev, "k_out", dt, need), _ptr(v_out, dev, "v_out", dt, need), st))
+
+
+def attention_workspace_size(cfg, total_tokens: int, num_seqs: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().gdn_attention_workspace_size(ctypes.byref(cfg), total_tokens, num_seqs, ctypes.byref(out)))
+    return out.value
+
+
+def attention(cfg, q, cu_dev, cu_host, kv_lens, pool, page_table, o, lse=None, workspace=None, stream=None):
+    """gdn_attention: causal attention of q [T, Hq, D] over the 4-bit cache into o [T, Hq, D] (and lse [T, Hq] fp32)."""
+    dev, st = _device(q, stream)
+    cu_h = _cu_host(cu_host)
+    T, io = int(cu_h[-1]), cfg.io_dtype
+    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
+    pq, ldq = _heads(q, dev, "q", io, T, cfg.num_q_heads, cfg.head_dim)
+    po = _ptr(o, dev, "o", "torch.bfloat16" if io == BF16 else "torch.float32", T * cfg.num_q_heads * cfg.head_dim)
+    pl = None if lse is None else _ptr(lse, dev, "lse", "torch.float32", T * cfg.num_q_heads)
+    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", "torch.uint8"), workspace.numel())
+    _check(lib().gdn_attention(ctypes.byref(cfg), pq, ldq, cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1,
+                               ctypes.byref(c), po, pl, pw, nw, st))
+
+
+class Q4Weight:
+    """A weight [N, K] in 4 bits, packed for linear_q4 (see q4_pack)."""
+
+    def __init__(self, data, N: int, K: int, group: int):
+        self.data, self.N, self.K, self.group = data, N, K, group
+
+
+def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
+    """gdn_q4_pack: codes uint8 [N, ceil(K / group) * group / 2] (channel 2i in the low half of byte i), scales and
+    biases bf16 [N, ceil(K / group)]; a code c stands for scale * c + bias."""
+    import torch
+    dev, st = _device(codes, stream)
+    N = codes.shape[0]
+    size = ctypes.c_size_t()
+    _check(lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(size)))
+    G = -(-K // group)
+    _need(tuple(codes.shape) == (N, G * group // 2), f"codes must be [{N}, {G * group // 2}], got {list(codes.shape)}")
+    _need(tuple(scales.shape) == (N, G) and tuple(biases.shape) == (N, G), f"scales and biases must be [{N}, {G}]")
+    data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
+    _check(lib().gdn_q4_pack(_ptr(codes, dev, "codes", "torch.uint8"), _ptr(scales, dev, "scales", "torch.bfloat16"),
+                             _ptr(biases, dev, "biases", "torch.bfloat16"), N, K, group, data.data_ptr(), st))
+    return Q4Weight(data, N, K, group)
+
+
+def linear_q4_workspace_size(M: int, N: int, K: int, group: int, io_dtype="bf16") -> int:
+    out = ctypes.c_size_t()
+    _check(lib().gdn_linear_q4_workspace_size(M, N, K, group, _io(io_dtype), ctypes.byref(out)))
+    return out.value
+
+
+def linear_q4(x, w: Q4Weight, y, workspace=None, stream=None):
+    """gdn_linear_q4: y [M, N] = x [M, K] @ w^T for a packed 4-bit weight."""
+    dev, st = _device(x, stream)
+    _need(x.dim() == 2 and x.shape[1] == w.K, f"x must be [rows, {w.K}], got {list(x.shape)}")
+    io, M = _io(x.dtype), x.shape[0]
+    dt = str(x.dtype)
+    _need(tuple(y.shape) == (M, w.N), f"y must be [{M}, {w.N}], got {list(y.shape)}")
+    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", "torch.uint8"), workspace.numel())
+    _check(lib().gdn_linear_q4(io, _ptr(x, dev, "x", dt), M, w.K, _ptr(w.data, dev, "w", "torch.uint8"), w.N, w.group,
+                               _ptr(y, dev, "y", dt), pw, nw, st))
 
 
 def state_blob_size(cfg) -> int:

@@ -17,6 +17,7 @@
 
 #include "../../include/gdn.h"
 #include "internal.h"
+#include "kv4.cuh"
 
 namespace {
 
@@ -327,7 +328,9 @@ const char* gdn_kernel_name(int32_t id) {
                                            "split_conv",        "split_prep",      "split_chain",
                                            "slot_copy",         "gemm",            "seqpar",
                                            "diag",              "wy_conv",         "wy_prep",
-                                           "wy_chain"};
+                                           "wy_chain",          "rope",            "kv_append",
+                                           "kv_read",           "attention",       "attn_combine",
+                                           "q4_pack",           "linear_q4"};
   return (id >= 0 && id < GDN_K_COUNT) ? names[id] : "unknown";
 }
 
@@ -833,6 +836,319 @@ gdn_status gdn_project_out(const gdn_config* cfg, const void* o, int32_t num_tok
   gemm_route(g, y, hidden, hidden);
   return gemm_impl(o, num_tokens, (int32_t)hvd, w_out, hidden, 0, g, stream, "gdn_project_out");
 }
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ attention side and 4-bit projections
+namespace {
+
+gdn_status check_io_dtype(int32_t t) {
+  if (t != GDN_F32 && t != GDN_BF16) return fail(GDN_E_UNSUPPORTED, "io_dtype %d is not GDN_F32 or GDN_BF16", t);
+  return GDN_OK;
+}
+
+gdn_status check_attn_cfg(const gdn_attn_config* c) {
+  if (!c) return fail(GDN_E_INVAL, "cfg is NULL");
+  if (c->num_q_heads <= 0 || c->num_kv_heads <= 0 || c->num_q_heads % c->num_kv_heads != 0)
+    return fail(GDN_E_INVAL, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)", c->num_q_heads,
+                c->num_kv_heads);
+  if (c->num_q_heads > (1 << 12)) return fail(GDN_E_UNSUPPORTED, "num_q_heads %d too large", c->num_q_heads);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(GDN_E_UNSUPPORTED, "head_dim %d (built: 64, 128, 256)", c->head_dim);
+  if (c->page_size <= 0 || c->page_size % gdn::kKvTile != 0 || c->page_size > 1024)
+    return fail(GDN_E_INVAL, "page_size %d must be a multiple of %d up to 1024", c->page_size, gdn::kKvTile);
+  if (!std::isfinite(c->softmax_scale)) return fail(GDN_E_INVAL, "softmax_scale is not finite");
+  return check_io_dtype(c->io_dtype);
+}
+
+size_t kv_page_bytes(const gdn_attn_config* c) {
+  return (size_t)c->num_kv_heads * (c->page_size / gdn::kKvTile) * gdn::kv_tile_bytes(c->head_dim);
+}
+
+gdn_status check_cache(const gdn_attn_config* cfg, const gdn_kv_cache* c, gdn::KvCache* out) {
+  if (!c) return fail(GDN_E_INVAL, "cache is NULL");
+  gdn_status s;
+  if ((s = check_ptr(c->pool, "cache.pool")) != GDN_OK) return s;
+  if (!c->page_table || ((uintptr_t)c->page_table & 3u))
+    return fail(GDN_E_INVAL, "cache.page_table is NULL or not 4-byte aligned");
+  if (!c->kv_lens || ((uintptr_t)c->kv_lens & 3u))
+    return fail(GDN_E_INVAL, "cache.kv_lens is NULL or not 4-byte aligned");
+  if (c->num_pages <= 0 || c->pages_per_seq <= 0)
+    return fail(GDN_E_INVAL, "num_pages %d and pages_per_seq %d must be positive", c->num_pages, c->pages_per_seq);
+  if ((int64_t)c->pages_per_seq * cfg->page_size > 0x7ffffff0LL)
+    return fail(GDN_E_INVAL, "pages_per_seq %d x page_size %d passes int32", c->pages_per_seq, cfg->page_size);
+  *out = gdn::KvCache{(unsigned char*)c->pool, c->page_table, c->kv_lens, (int64_t)kv_page_bytes(cfg),
+                      c->pages_per_seq, c->num_pages, cfg->page_size, cfg->num_kv_heads};
+  return GDN_OK;
+}
+
+// rows of `heads` heads of D elements, ld elements apart
+gdn_status check_rows(const void* p, const char* name, int64_t ld, int64_t heads, int64_t D, int32_t io) {
+  gdn_status s;
+  if ((s = check_ptr(p, name)) != GDN_OK) return s;
+  if (ld < heads * D || ld % (io == GDN_BF16 ? 8 : 4) != 0 || ld > (1LL << 40))
+    return fail(GDN_E_INVAL, "%s: %lld elements between tokens (at least %lld, whole 16 bytes)", name, (long long)ld,
+                (long long)(heads * D));
+  return GDN_OK;
+}
+
+gdn_status check_plan(const gdn_rope_plan* p, int32_t head_dim) {
+  if (!p) return fail(GDN_E_INVAL, "plan is NULL");
+  if (p->rotary_dim < 0 || p->rotary_dim % 2 != 0 || p->rotary_dim > head_dim)
+    return fail(GDN_E_INVAL, "plan.rotary_dim %d (even, at most the head's %d)", p->rotary_dim, head_dim);
+  if (p->num_axes < 1 || p->num_axes > 3) return fail(GDN_E_INVAL, "plan.num_axes %d (1 to 3)", p->num_axes);
+  for (int32_t j = 0; j < p->rotary_dim / 2; ++j)
+    if (p->axis[j] >= p->num_axes) return fail(GDN_E_INVAL, "plan.axis[%d] = %d of %d", j, p->axis[j], p->num_axes);
+  return GDN_OK;
+}
+
+gdn_status check_q4(int32_t N, int32_t K, int32_t group) {
+  if (N < 0) return fail(GDN_E_INVAL, "N = %d (must be >= 0)", N);
+  if (K <= 0 || K % 8 != 0) return fail(GDN_E_INVAL, "K = %d must be a positive multiple of 8", K);
+  if (group != 32 && group != 64 && group != 128) return fail(GDN_E_UNSUPPORTED, "group %d (32, 64 or 128)", group);
+  return GDN_OK;
+}
+
+gdn_status check_ws(const void* ws, size_t have, size_t need) {
+  if (have < need || (need > 0 && !ws))
+    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes at %p, need %zu", have, ws, need);
+  if (need > 0 && ((uintptr_t)ws & 255u) != 0) return fail(GDN_E_WORKSPACE, "workspace is not 256-byte aligned");
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_rope_plan_init(int32_t rotary_dim, double theta, const double* inv_freq, int32_t num_axes,
+                              const int32_t* sections, int32_t layout, gdn_rope_plan* plan) {
+  if (!plan) return fail(GDN_E_INVAL, "plan is NULL");
+  if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > 2 * GDN_ROPE_MAX_PAIRS)
+    return fail(GDN_E_INVAL, "rotary_dim %d (even, at most %d)", rotary_dim, 2 * GDN_ROPE_MAX_PAIRS);
+  if (num_axes < 1 || num_axes > 3 || (num_axes > 1 && !sections))
+    return fail(GDN_E_INVAL, "num_axes %d (1 to 3, with sections from 2 on)", num_axes);
+  if (layout < GDN_ROPE_SECTIONS || layout > GDN_ROPE_PER_AXIS) return fail(GDN_E_INVAL, "layout %d", layout);
+  if (!inv_freq && !(theta >= 1.0 && std::isfinite(theta)))
+    return fail(GDN_E_INVAL, "theta %g must be finite and at least 1", theta);
+  const int32_t half = rotary_dim / 2;
+  int32_t sec[3] = {half, 0, 0};
+  int64_t sum = 0;
+  for (int32_t i = 0; i < num_axes && sections; ++i) {
+    if (sections[i] < 0) return fail(GDN_E_INVAL, "sections[%d] = %d", i, sections[i]);
+    sum += sec[i] = sections[i];
+  }
+  if (sections && sum != half) return fail(GDN_E_INVAL, "sections sum to %lld, not %d", (long long)sum, half);
+  gdn_rope_plan out;
+  memset(&out, 0, sizeof(out));
+  out.rotary_dim = rotary_dim;
+  out.num_axes = num_axes;
+  int32_t begin = 0, ax = 0;  // SECTIONS, PER_AXIS: the section that holds pair j
+  for (int32_t j = 0; j < half; ++j) {
+    while (j >= begin + sec[ax]) begin += sec[ax++];
+    long double e;  // f_j = theta^-e
+    if (layout == GDN_ROPE_INTERLEAVED) {
+      const int32_t a = j % 3;
+      out.axis[j] = (uint8_t)(a < num_axes && j < 3 * sec[a] ? a : 0);
+      e = (long double)j / half;
+    } else {
+      out.axis[j] = (uint8_t)ax;
+      e = layout == GDN_ROPE_PER_AXIS ? (long double)(j - begin) / sec[ax] : (long double)j / half;
+    }
+    const long double f = inv_freq ? (long double)inv_freq[j] : powl((long double)theta, -e);
+    if (!(f >= 0.0L && f <= 6.28318530717958647692L))
+      return fail(GDN_E_INVAL, "frequency %g of pair %d outside [0, 2 pi]", (double)f, j);
+    const long double turn = floorl(f / 6.283185307179586476925286766559L * 18446744073709551616.0L + 0.5L);
+    out.turn[j] = turn >= 18446744073709551616.0L ? 0 : (uint64_t)turn;  // a whole turn is none
+  }
+  *plan = out;
+  return GDN_OK;
+}
+
+gdn_status gdn_rope(const gdn_rope_plan* plan, int32_t io_dtype, const void* x, int64_t ldx, const int32_t* positions,
+                    int32_t num_tokens, int32_t num_heads, int32_t head_dim, int32_t inverse, void* out, int64_t ldo,
+                    gdn_stream_t stream) {
+  gdn_status s;
+  if ((s = check_io_dtype(io_dtype)) != GDN_OK) return s;
+  if (head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256)
+    return fail(GDN_E_UNSUPPORTED, "head_dim %d (a multiple of 8 up to 256)", head_dim);
+  if (num_tokens < 0 || num_heads <= 0 || num_heads > (1 << 20))
+    return fail(GDN_E_INVAL, "num_tokens %d, num_heads %d", num_tokens, num_heads);
+  if ((s = check_plan(plan, head_dim)) != GDN_OK) return s;
+  if (num_tokens > 0) {
+    if ((s = check_rows(x, "x", ldx, num_heads, head_dim, io_dtype)) != GDN_OK ||
+        (s = check_rows(out, "out", ldo, num_heads, head_dim, io_dtype)) != GDN_OK)
+      return s;
+    if (!positions || ((uintptr_t)positions & 3u)) return fail(GDN_E_INVAL, "positions is NULL or not 4-byte aligned");
+    if (out == x && ldo != ldx) return fail(GDN_E_INVAL, "out is x with another row pitch");
+  }
+  if ((s = check_device()) != GDN_OK) return s;
+  if (num_tokens == 0) return GDN_OK;
+  cudaError_t e = gdn::launch_rope(*plan, io_dtype == GDN_BF16, x, ldx, positions, num_tokens, num_heads, head_dim,
+                                   inverse != 0, out, ldo, (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_rope launch");
+}
+
+gdn_status gdn_kv_page_bytes(const gdn_attn_config* cfg, size_t* bytes) {
+  gdn_status s;
+  if ((s = check_attn_cfg(cfg)) != GDN_OK) return s;
+  if (!bytes) return fail(GDN_E_INVAL, "bytes is NULL");
+  *bytes = kv_page_bytes(cfg);
+  return GDN_OK;
+}
+
+gdn_status gdn_kv_append(const gdn_attn_config* cfg, const gdn_rope_plan* plan, const void* q, int64_t ldq,
+                         const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* positions,
+                         const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host, int32_t num_seqs,
+                         const gdn_kv_cache* cache, void* q_out, int64_t ldqo, gdn_stream_t stream) {
+  gdn_status s;
+  gdn::KvCache c;
+  gdn_rope_plan none;
+  if ((s = check_attn_cfg(cfg)) != GDN_OK) return s;
+  if (!plan) {
+    none.rotary_dim = 0;
+    none.num_axes = 1;
+    plan = &none;
+  } else if ((s = check_plan(plan, cfg->head_dim)) != GDN_OK) {
+    return s;
+  }
+  int64_t total = 0;
+  int32_t max_len = 0;
+  if ((s = check_cu(cu_seqlens_dev, cu_seqlens_host, num_seqs, &total, &max_len)) != GDN_OK) return s;
+  if ((s = check_cache(cfg, cache, &c)) != GDN_OK) return s;
+  if ((q == nullptr) != (q_out == nullptr)) return fail(GDN_E_INVAL, "q and q_out are NULL together or not at all");
+  if ((uintptr_t)positions & 3u) return fail(GDN_E_INVAL, "positions is not 4-byte aligned");
+  const int32_t io = cfg->io_dtype, D = cfg->head_dim;
+  if (total > 0) {
+    if ((s = check_rows(k, "k", ldk, cfg->num_kv_heads, D, io)) != GDN_OK ||
+        (s = check_rows(v, "v", ldv, cfg->num_kv_heads, D, io)) != GDN_OK)
+      return s;
+    if (q && ((s = check_rows(q, "q", ldq, cfg->num_q_heads, D, io)) != GDN_OK ||
+              (s = check_rows(q_out, "q_out", ldqo, cfg->num_q_heads, D, io)) != GDN_OK))
+      return s;
+    if (q && q_out == q && ldqo != ldq) return fail(GDN_E_INVAL, "q_out is q with another row pitch");
+  }
+  int dev = 0;
+  if ((s = check_device(&dev)) != GDN_OK) return s;
+  if (total == 0) return GDN_OK;
+  cudaError_t e = gdn::launch_kv_append(*plan, io == GDN_BF16, D, cfg->num_q_heads, q, ldq, k, ldk, v, ldv, positions,
+                                        cu_seqlens_dev, (int32_t)total, num_seqs, c, q_out, ldqo, g_status_ptr[dev],
+                                        (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_append launch");
+}
+
+gdn_status gdn_kv_read(const gdn_attn_config* cfg, const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                       int32_t num_seqs, const gdn_kv_cache* cache, void* k_out, void* v_out, gdn_stream_t stream) {
+  gdn_status s;
+  gdn::KvCache c;
+  if ((s = check_attn_cfg(cfg)) != GDN_OK) return s;
+  int64_t total = 0;
+  int32_t max_len = 0;
+  if ((s = check_cu(cu_seqlens_dev, cu_seqlens_host, num_seqs, &total, &max_len)) != GDN_OK) return s;
+  if ((s = check_cache(cfg, cache, &c)) != GDN_OK) return s;
+  if (total > 0 && ((s = check_ptr(k_out, "k_out")) != GDN_OK || (s = check_ptr(v_out, "v_out")) != GDN_OK)) return s;
+  int dev = 0;
+  if ((s = check_device(&dev)) != GDN_OK) return s;
+  if (total == 0) return GDN_OK;
+  cudaError_t e = gdn::launch_kv_read(cfg->io_dtype == GDN_BF16, cfg->head_dim, cu_seqlens_dev, (int32_t)total,
+                                      num_seqs, c, k_out, v_out, g_status_ptr[dev], (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_read launch");
+}
+
+gdn_status gdn_attention_workspace_size(const gdn_attn_config* cfg, int64_t total_tokens, int32_t num_seqs,
+                                        size_t* bytes) {
+  gdn_status s;
+  if ((s = check_attn_cfg(cfg)) != GDN_OK) return s;
+  if (!bytes) return fail(GDN_E_INVAL, "bytes is NULL");
+  if (total_tokens < 0 || total_tokens > 0x7fffffffLL || num_seqs <= 0 || num_seqs > kMaxSeqs)
+    return fail(GDN_E_INVAL, "bad sizes");
+  *bytes = gdn::attention_ws_bytes((int32_t)total_tokens, num_seqs, cfg->num_q_heads, cfg->num_kv_heads,
+                                   cfg->head_dim);
+  return GDN_OK;
+}
+
+gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int64_t ldq, const int32_t* cu_seqlens_dev,
+                         const int32_t* cu_seqlens_host, int32_t num_seqs, const gdn_kv_cache* cache, void* o,
+                         float* lse, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  gdn_status s;
+  gdn::KvCache c;
+  if ((s = check_attn_cfg(cfg)) != GDN_OK) return s;
+  int64_t total = 0;
+  int32_t max_len = 0;
+  if ((s = check_cu(cu_seqlens_dev, cu_seqlens_host, num_seqs, &total, &max_len)) != GDN_OK) return s;
+  if ((s = check_cache(cfg, cache, &c)) != GDN_OK) return s;
+  if (total > 0 && ((s = check_rows(q, "q", ldq, cfg->num_q_heads, cfg->head_dim, cfg->io_dtype)) != GDN_OK ||
+                    (s = check_ptr(o, "o")) != GDN_OK))
+    return s;
+  if ((uintptr_t)lse & 3u) return fail(GDN_E_INVAL, "lse is not 4-byte aligned");
+  const size_t need = gdn::attention_ws_bytes((int32_t)total, num_seqs, cfg->num_q_heads, cfg->num_kv_heads,
+                                              cfg->head_dim);
+  if ((s = check_ws(workspace, workspace_bytes, need)) != GDN_OK) return s;
+  int dev = 0;
+  if ((s = check_device(&dev)) != GDN_OK) return s;
+  if (total == 0) return GDN_OK;
+  const gdn::AttnProblem p{q, o, lse, ldq, cu_seqlens_dev, (int32_t)total, num_seqs, cfg->num_q_heads, cfg->head_dim,
+                           max_len, cfg->softmax_scale, cfg->io_dtype == GDN_BF16};
+  cudaError_t e = gdn::launch_attention(p, c, workspace, g_status_ptr[dev], (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attention launch");
+}
+
+gdn_status gdn_q4_packed_bytes(int32_t N, int32_t K, int32_t group, size_t* bytes) {
+  gdn_status s;
+  if ((s = check_q4(N, K, group)) != GDN_OK) return s;
+  if (!bytes) return fail(GDN_E_INVAL, "bytes is NULL");
+  *bytes = gdn::q4_layout(N, K, group).total_bytes;
+  return GDN_OK;
+}
+
+gdn_status gdn_q4_pack(const void* codes, const void* scales, const void* biases, int32_t N, int32_t K, int32_t group,
+                       void* packed, gdn_stream_t stream) {
+  gdn_status s;
+  if ((s = check_q4(N, K, group)) != GDN_OK) return s;
+  if (N > 0) {
+    if (!codes || !scales || !biases || ((uintptr_t)scales & 1u) || ((uintptr_t)biases & 1u))
+      return fail(GDN_E_INVAL, "codes, scales or biases is NULL or misaligned");
+    if ((s = check_ptr(packed, "packed")) != GDN_OK) return s;
+  }
+  if ((s = check_device()) != GDN_OK) return s;
+  if (N == 0) return GDN_OK;
+  cudaError_t e = gdn::launch_q4_pack(codes, scales, biases, N, K, group, packed, (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_q4_pack launch");
+}
+
+gdn_status gdn_linear_q4_workspace_size(int32_t M, int32_t N, int32_t K, int32_t group, int32_t io_dtype,
+                                        size_t* bytes) {
+  gdn_status s;
+  if ((s = check_q4(N, K, group)) != GDN_OK || (s = check_io_dtype(io_dtype)) != GDN_OK) return s;
+  if (M < 0) return fail(GDN_E_INVAL, "M = %d (must be >= 0)", M);
+  if (!bytes) return fail(GDN_E_INVAL, "bytes is NULL");
+  *bytes = gdn::linear_q4_ws_bytes(M, N, K, group, io_dtype == GDN_BF16);
+  return GDN_OK;
+}
+
+gdn_status gdn_linear_q4(int32_t io_dtype, const void* x, int32_t M, int32_t K, const void* packed, int32_t N,
+                         int32_t group, void* y, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  gdn_status s;
+  if ((s = check_q4(N, K, group)) != GDN_OK || (s = check_io_dtype(io_dtype)) != GDN_OK) return s;
+  if (M < 0) return fail(GDN_E_INVAL, "M = %d (must be >= 0)", M);
+  if (M > 0 && N > 0) {
+    if ((s = check_ptr(x, "x")) != GDN_OK || (s = check_ptr(packed, "packed")) != GDN_OK) return s;
+    if (!y || ((uintptr_t)y & (io_dtype == GDN_BF16 ? 1u : 3u)))
+      return fail(GDN_E_INVAL, "y is NULL or not aligned to its element size");
+  }
+  if ((s = check_ws(workspace, workspace_bytes, gdn::linear_q4_ws_bytes(M, N, K, group, io_dtype == GDN_BF16))) !=
+      GDN_OK)
+    return s;
+  int dev = 0;
+  if ((s = check_device(&dev)) != GDN_OK) return s;
+  if (M == 0 || N == 0) return GDN_OK;
+  cudaError_t e = gdn::launch_linear_q4(io_dtype == GDN_BF16, x, M, K, packed, N, group, y, workspace,
+                                        g_status_ptr[dev], (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_linear_q4 launch");
+}
+
+}  // extern "C"
+
+extern "C" {
 
 gdn_status gdn_state_blob_size(const gdn_config* cfg, size_t* bytes) {
   gdn::Dims d;

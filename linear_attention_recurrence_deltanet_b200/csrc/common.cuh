@@ -19,6 +19,7 @@ enum : int32_t {
   kStatusOk = 0,
   kStatusWaitTimeout = 1,   // a bounded wait gave up
   kStatusBadSlot = 3,       // a state slot index past the end of the pool (the row was skipped)
+  kStatusBadPage = 4,       // a cache position without a page inside the pool (the token was skipped)
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int32_t code) {

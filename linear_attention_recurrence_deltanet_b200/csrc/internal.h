@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/gdn.h"
 #include "common.cuh"
 
 namespace gdn {
@@ -164,6 +165,44 @@ cudaError_t launch_prefill_wy(const Dims& d, int chunk_size, const float* conv_w
                               const int32_t* tile_off, const int4* tile_map, int32_t N, int64_t total_tokens,
                               int64_t total_tiles, bool zero_state, bool zero_conv, const void* conv_state,
                               float* state, void* o, void* ws, int32_t* status, cudaStream_t stream);
+
+// rope.cu: rotary positions, and the 4-bit paged cache's writer and reader (kv4.cuh)
+struct KvCache;
+cudaError_t launch_rope(const gdn_rope_plan& plan, bool bf16, const void* x, int64_t ldx, const int32_t* pos, int32_t T,
+                        int32_t H, int32_t D, bool inverse, void* out, int64_t ldo, cudaStream_t stream);
+cudaError_t launch_kv_append(const gdn_rope_plan& plan, bool bf16, int32_t D, int32_t Hq, const void* q, int64_t ldq,
+                             const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* pos,
+                             const int32_t* cu, int32_t T, int32_t N, const KvCache& cache, void* q_out, int64_t ldqo,
+                             int32_t* status, cudaStream_t stream);
+cudaError_t launch_kv_read(bool bf16, int32_t D, const int32_t* cu, int32_t T, int32_t N, const KvCache& cache,
+                           void* k_out, void* v_out, int32_t* status, cudaStream_t stream);
+
+// attention.cu: causal attention over the 4-bit paged cache
+struct AttnProblem {
+  const void* q;
+  void* o;
+  float* lse;         // may be NULL
+  int64_t ldq;        // elements between tokens of q
+  const int32_t* cu;  // [N + 1], device
+  int32_t T, N, Hq, D, max_q;
+  float scale;
+  bool bf16;
+};
+size_t attention_ws_bytes(int32_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
+cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
+                             cudaStream_t stream);
+
+// linear_q4.cu: Y = X W^T with 4-bit weights, group scales and biases
+struct Q4Layout {
+  int32_t tiles, blocks, groups;  // 16-row tiles, 64-column blocks of codes, groups of a row
+  size_t scale_off, total_bytes;
+};
+Q4Layout q4_layout(int32_t N, int32_t K, int32_t group);
+cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* biases, int32_t N, int32_t K,
+                           int32_t group, void* packed, cudaStream_t stream);
+size_t linear_q4_ws_bytes(int32_t M, int32_t N, int32_t K, int32_t group, bool bf16);
+cudaError_t launch_linear_q4(bool bf16, const void* x, int32_t M, int32_t K, const void* packed, int32_t N,
+                             int32_t group, void* y, void* ws, int32_t* status, cudaStream_t stream);
 
 // diag.cu: a kernel whose bounded wait always runs out (tests the status path)
 cudaError_t launch_wait_expiry(uint64_t limit_ns, int32_t* status, cudaStream_t stream);

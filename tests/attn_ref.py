@@ -1,0 +1,189 @@
+"""Plain float64 references of the attention-side operators and the 4-bit projection (CPU torch, no kernels)."""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+U = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}  # half a step, relative
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def frequencies(rot, theta, sections, layout):
+    """(f_j, axis_j), straight from the definition."""
+    half = rot // 2
+    sec = list(sections) if sections is not None else [half]
+    f, ax = [], []
+    for j in range(half):
+        if layout == "interleaved":
+            a = j % 3
+            a = a if a < len(sec) and j < 3 * sec[a] else 0
+            e = j / half
+        else:
+            a = next(i for i in range(len(sec)) if j < sum(sec[:i + 1]))
+            e = (j - sum(sec[:a])) / sec[a] if layout == "per_axis" else j / half
+        f.append(theta ** -e)
+        ax.append(a)
+    return np.array(f), np.array(ax, int)
+
+
+def cos_sin(positions, f, ax):
+    """fp32 cosine and sine [T, half] of float64 angles."""
+    ang = np.asarray(positions, np.float64)[ax].T * f
+    return torch.from_numpy(np.cos(ang)).float(), torch.from_numpy(np.sin(ang)).float()
+
+
+def rotate64(x, cs):
+    """The rotation in float64 with the given fp32 cosines and sines."""
+    c, s = (t.double().unsqueeze(1) for t in cs)
+    h = c.shape[-1]
+    x = x.double()
+    a, b = x[..., :h], x[..., h:2 * h]
+    return torch.cat((a * c - b * s, b * c + a * s, x[..., 2 * h:]), -1)
+
+
+def rotate32(x, cs):
+    """The rotation with every product and sum rounded to fp32."""
+    c, s = (t.unsqueeze(1) for t in cs)
+    h = c.shape[-1]
+    x = x.float()
+    a, b = x[..., :h], x[..., h:2 * h]
+    return torch.cat((a * c - b * s, b * c + a * s, x[..., 2 * h:]), -1)
+
+
+def quantise(x, group):
+    """(codes, scale, bias, values) of fp32 x [..., D], as the header defines them; scale and bias as float64."""
+    y = x.float().unflatten(-1, (-1, group))
+    lo, hi = y.amin(-1, keepdim=True), y.amax(-1, keepdim=True)
+    s = ((hi - lo) * torch.tensor(1.0 / 15.0, dtype=torch.float32)).bfloat16().float()
+    b = lo.bfloat16().float()
+    c = torch.where(s > 0, ((y - b) / s).round().clamp(0, 15), torch.zeros_like(y))
+    bad = ~(torch.isfinite(hi - lo) & torch.isfinite(b))
+    s, b = s.masked_fill(bad, math.nan), b.masked_fill(bad, math.nan)
+    v = s.double() * c.double() + b.double()
+    return c.flatten(-2), s.squeeze(-1).double(), b.squeeze(-1).double(), v.flatten(-2)
+
+
+def v_group(D):
+    return min(D, 128)
+
+
+def attention64(q, k, v, scale, new):
+    """One sequence: q [new, Hq, D], k and v [len, Hkv, D] float64 (the cache's values) -> o, lse."""
+    n, hq, d = q.shape
+    length, hkv, _ = k.shape
+    o, lse = torch.zeros(n, hq, d, dtype=torch.float64), torch.full((n, hq), -math.inf, dtype=torch.float64)
+    for i in range(n):
+        seen = length - new + i + 1
+        if seen <= 0:
+            continue
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            s = (k[:seen, kh] @ q[i, h].double()) * scale
+            lse[i, h] = torch.logsumexp(s, 0)
+            o[i, h] = torch.softmax(s, 0) @ v[:seen, kh]
+    return o, lse
+
+
+def attention_bound(q, k_parts, v_parts, o, scale, new, io):
+    """What rounding allows: (|o error|, |lse error|) per query and head.
+
+    Scores: products of the io type and small integers are exact, sums lose at most 2^-23 of the running magnitude a
+    step; a warp's chain of a score has fewer than 8 steps that see the whole sum, so 2^-20 of the sum of magnitudes
+    covers them (offset codes: up to 144 steps of the scale for bf16, 8 for fp32).  A score off by e changes p by a
+    factor within e^{+-2e}.  Probabilities enter the value product in parts that keep 16 bits (bf16 io) or 24, values
+    as codes around 8; sums as for scores.  The output rounds once."""
+    n, hq, d = q.shape
+    (_, ks, kb, _), (_, vs, vb, _) = k_parts, v_parts
+    length, hkv = ks.shape[:2]
+    top = 144.0 if io == "bf16" else 8.0
+    kb_m = kb.abs() if io == "bf16" else (kb + 8 * ks).abs()
+    k_mag = (top * ks + kb_m).repeat_interleave(64, -1)
+    v_mag = (8 * vs + (vb + 8 * vs).abs()).amax(-1)  # [length, hkv]
+    eo, el = torch.zeros(n, hq, dtype=torch.float64), torch.zeros(n, hq, dtype=torch.float64)
+    for i in range(n):
+        seen = length - new + i + 1
+        if seen <= 0:
+            continue
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            ds = abs(scale) * 2.0 ** -20 * (k_mag[:seen, kh] @ q[i, h].double().abs()).max()
+            el[i, h] = ds
+            eo[i, h] = (2 * ds + (2.0 ** -16 if io == "bf16" else 2.0 ** -20) + 2.0 ** -20) * v_mag[:seen, kh].max()
+    return U[io] * o.abs() + eo.unsqueeze(-1), el
+
+
+class Case:
+    """A packed batch over a shuffled paged cache, on the GPU, with its float64 twin on the CPU."""
+
+    def __init__(self, new, ctx, hq, hkv, d, page, io, seed=0, spare=2, fill=0xFF, outlier=True):
+        import linear_attention_recurrence_deltanet_b200 as gdn
+        g = torch.Generator().manual_seed(seed)
+        self.new, self.lens = list(new), [a + b for a, b in zip(new, ctx)]
+        self.hq, self.hkv, self.d, self.page, self.io = hq, hkv, d, page, io
+        self.N, self.T = len(new), sum(new)
+        self.cfg = gdn.make_attn_config(hq, hkv, d, page_size=page, io_dtype=io)
+        self.scale = d ** -0.5
+        self.cu = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+        need = [-(-n // page) for n in self.lens]
+        self.width, self.pages = max(need + [1]), sum(need) + spare
+        order = torch.randperm(self.pages, generator=g).tolist()
+        self.table = torch.full((self.N, self.width), -7, dtype=torch.int32)  # ids past a sequence's end are never read
+        for n, m in enumerate(need):
+            for j in range(m):
+                self.table[n, j] = order.pop()
+        self.spare = order
+        self.q = torch.randn(self.T, hq, d, generator=g).to(DT[io])
+        self.k = [torch.randn(n, hkv, d, generator=g) for n in self.lens]
+        self.v = [torch.randn(n, hkv, d, generator=g).to(DT[io]) for n in self.lens]
+        for t in self.k:
+            if outlier and t.numel():
+                t[..., 3::29] *= 5.0
+        self.k = [t.to(DT[io]) for t in self.k]
+        # every byte of the pool outside the stored tokens is poison: as bf16 scales, NaN
+        self.pool = torch.full((self.pages, gdn.kv_page_bytes(self.cfg)), fill, dtype=torch.uint8, device="cuda")
+        self.fill_value = fill
+        self.d_table, self.d_lens = self.table.cuda(), torch.tensor(self.lens, dtype=torch.int32).cuda()
+        self.d_cu, self.d_q = torch.from_numpy(self.cu).cuda(), self.q.cuda()
+        self.gdn = gdn
+
+    def fill(self):
+        """The whole context into the cache, unrotated, in one append."""
+        cu = np.concatenate(([0], np.cumsum(self.lens))).astype(np.int32)
+        k, v = torch.cat(self.k).cuda(), torch.cat(self.v).cuda()
+        self.gdn.kv_append(self.cfg, None, None, k, v, None, torch.from_numpy(cu).cuda(), cu, self.d_lens, self.pool,
+                           self.d_table, None)
+        return self
+
+    def outputs(self):
+        o = torch.full((self.T, self.hq, self.d), 7.0, dtype=DT[self.io], device="cuda")
+        lse = torch.full((self.T, self.hq), 7.0, device="cuda")
+        ws = torch.full((max(256, self.gdn.attention_workspace_size(self.cfg, self.T, self.N)),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        return o, lse, ws
+
+    def attention(self, stream=None):
+        o, lse, ws = self.outputs()
+        self.gdn.attention(self.cfg, self.d_q, self.d_cu, self.cu, self.d_lens, self.pool, self.d_table, o, lse, ws,
+                           stream=stream)
+        return o, lse
+
+    def check(self, o, lse, skip=()):
+        o, lse = o.cpu(), lse.cpu()
+        assert torch.isfinite(o).all()
+        for n in range(self.N):
+            a, b = int(self.cu[n]), int(self.cu[n + 1])
+            if a == b or n in skip:
+                continue
+            kp, vp = quantise(self.k[n], 64), quantise(self.v[n], v_group(self.d))
+            ref, rl = attention64(self.q[a:b], kp[3], vp[3], self.scale, b - a)
+            eo, el = attention_bound(self.q[a:b], kp, vp, ref, self.scale, b - a, self.io)
+            off = (o[a:b].double() - ref).abs() - eo
+            assert off.max() <= 0, f"sequence {n}: o past its bound by {off.max():.3g}"
+            seen = torch.isfinite(rl)
+            assert torch.equal(torch.isfinite(lse[a:b]), seen) and (lse[a:b][~seen] == -math.inf).all()
+            dl = (lse[a:b].double() - rl).abs()[seen] - el[seen] - 2.0 ** -21 * (1 + rl.abs()[seen])
+            assert dl.numel() == 0 or dl.max() <= 0, f"sequence {n}: lse past its bound by {dl.max():.3g}"
+            assert (o[a:b][~seen] == 0).all()

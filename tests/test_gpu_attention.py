@@ -1,0 +1,438 @@
+"""Rotary positions, the 4-bit paged cache and attention over it, through the public calls against float64."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_recurrence_deltanet_b200 as gdn
+from attn_ref import DT, U, Case, cos_sin, frequencies, quantise, rotate32, rotate64, v_group
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    gdn.lib()
+    yield
+    assert gdn.device_status() == 0
+
+
+# --------------------------------------------------------------------------------------------------------- rope
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,D,rot,sections,layout", [
+    (1, 1, 64, 64, None, "sections"), (5, 24, 128, 64, None, "sections"), (33, 3, 128, 128, [24, 20, 20], "interleaved"),
+    (7, 5, 72, 72, [12, 12, 12], "per_axis"), (6, 2, 80, 60, [10, 20], "per_axis"), (9, 2, 256, 256, [64, 32, 32], "sections"),
+    (3, 7, 128, 36, [8, 5, 5], "interleaved"), (4, 2, 8, 2, None, "sections"), (2, 2, 64, 0, None, "sections"),
+    (2500, 2, 64, 64, [16, 8, 8], "interleaved"),
+])
+def test_rope_forward_and_inverse(io, T, H, D, rot, sections, layout):
+    g = torch.Generator().manual_seed(T * 7 + D)
+    axes = len(sections) if sections else 1
+    x = torch.randn(T, H, D, generator=g).to(DT[io])
+    pos = torch.randint(-5, 262144, (axes, T), generator=g, dtype=torch.int32)
+    pos[:, 0] = 2 ** 31 - 1
+    plan = gdn.rope_plan(rot, 1e7, sections=sections, layout=layout)
+    f, ax = frequencies(rot, 1e7, sections, layout)
+    cs = cos_sin(pos.numpy(), f, ax) if rot else (torch.zeros(T, 0), torch.zeros(T, 0))
+    # positions near 2^31 in float64: angle error 2^31 * 2^-53, far below an fp32 step of the cosine
+    wide = torch.full((T, H + 2, D), 3.0, dtype=DT[io], device="cuda")
+    wide[:, 1:H + 1] = x.cuda()
+    out = torch.full((T, H, D), 9.0, dtype=DT[io], device="cuda")
+    gdn.rope(plan, wide[:, 1:H + 1], pos.cuda(), out)
+    ref = rotate64(x, cs)
+    # three fp32 roundings of the products and the sum, a step of cosine and sine, one final rounding
+    pair = x.double().abs()
+    mag = torch.cat((pair[..., :rot // 2] + pair[..., rot // 2:rot],) * 2 + (pair[..., rot:],), -1)
+    tol = U[io] * ref.abs() + 6 * 2.0 ** -24 * mag
+    assert ((out.cpu().double() - ref).abs() <= tol).all()
+    assert torch.equal(out.cpu()[..., rot:], x[..., rot:])
+    # in place, inverse: rotates back within the two roundings
+    gdn.rope(plan, out, pos.cuda(), out, inverse=True)
+    back = rotate64(x, cs)
+    tol2 = 2 * U[io] * mag + 12 * 2.0 ** -24 * mag
+    assert ((out.cpu().double() - x.double()).abs() <= tol2 + U[io] * back.abs().max() * 0).all()
+
+
+def test_rope_inverse_is_the_gradient():
+    """sum(w * rope(x)) has the gradient rope^-1(w), by the formula and by differences."""
+    T, H, D, rot = 3, 2, 64, 64
+    g = torch.Generator().manual_seed(3)
+    x, w = torch.randn(T, H, D, generator=g).cuda(), torch.randn(T, H, D, generator=g).cuda()
+    pos = torch.tensor([[0, 3, 100], [5, 2, 77]], dtype=torch.int32).cuda()
+    plan = gdn.rope_plan(rot, 1e4, sections=[20, 12], layout="interleaved")
+    grad = torch.empty_like(w)
+    gdn.rope(plan, w, pos, grad, inverse=True)
+    y0, y1 = torch.empty_like(x), torch.empty_like(x)
+    for i in ((0, 0, 0), (1, 1, 37), (2, 0, 63)):
+        e = torch.zeros_like(x)
+        e[i] = 0.5
+        gdn.rope(plan, x + e, pos, y1)
+        gdn.rope(plan, x - e, pos, y0)
+        num = ((w.double() * (y1.double() - y0.double())).sum()).item()
+        # linear in x: the difference is exact up to 128 rounded terms
+        assert abs(num - grad[i].item()) <= 128 * 6 * 2.0 ** -24 * 4
+
+
+def test_rope_custom_frequencies_and_strided_out():
+    T, H, D = 6, 2, 64
+    f = np.linspace(1.0, 0.01, 16)
+    plan = gdn.rope_plan(32, inv_freq=f)
+    x = torch.randn(T, H, D, generator=torch.Generator().manual_seed(1))
+    pos = torch.arange(T, dtype=torch.int32)
+    buf = torch.full((T, H + 1, D), 5.0, device="cuda")
+    gdn.rope(plan, x.cuda(), pos.cuda(), buf[:, 1:])
+    ref = rotate64(x, cos_sin(pos.view(1, -1).numpy(), f, np.zeros(16, int)))
+    assert ((buf[:, 1:].cpu().double() - ref).abs() <= 8 * 2.0 ** -24 * (1 + ref.abs()) * 4).all()
+    assert (buf[:, 0] == 5.0).all()
+
+
+# ------------------------------------------------------------------------------------------------- append, read
+APPEND = [
+    # new tokens, context, Hq, Hkv, D, page, rot, sections, layout
+    ([1], [0], 4, 1, 64, 16, 32, None, "sections"),
+    ([1, 1, 1, 1], [0, 15, 16, 200], 24, 2, 128, 64, 64, None, "sections"),
+    ([5, 0, 33, 1], [11, 3, 0, 47], 6, 2, 128, 48, 128, [24, 20, 20], "interleaved"),
+    ([17, 70], [0, 31], 6, 3, 64, 32, 60, [10, 10, 10], "per_axis"),
+    ([40, 3], [1, 16], 2, 2, 256, 16, 256, None, "sections"),
+    ([9], [4], 2, 1, 256, 32, 36, [9, 9], "sections"),
+    ([3000], [100], 3, 1, 64, 128, 64, None, "sections"),
+]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("new,ctx,hq,hkv,d,page,rot,sections,layout", APPEND)
+def test_append_then_read(io, new, ctx, hq, hkv, d, page, rot, sections, layout):
+    c = Case(new, ctx, hq, hkv, d, page, io, seed=len(new) + d)
+    axes = len(sections) if sections else 1
+    g = torch.Generator().manual_seed(9)
+    T = c.T
+    rows = torch.randn(T, hq + 2 * hkv, d, generator=g)
+    rows[:, hq:hq + hkv, 2::31] *= 6.0
+    rows = rows.to(DT[io])
+    pos = torch.randint(0, 70000, (axes, T), generator=g, dtype=torch.int32)
+    plan = gdn.rope_plan(rot, 1e6, sections=sections, layout=layout)
+    dev = rows.cuda()
+    q, k, v = dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:]  # slices of a projection's rows
+    q_out = torch.full((T, hq, d), 4.0, dtype=DT[io], device="cuda")
+    before = c.pool.clone()
+    gdn.kv_append(c.cfg, plan, q, k, v, pos.cuda(), c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, q_out)
+    k_out, v_out = (torch.full((T, hkv, d), 4.0, dtype=DT[io], device="cuda") for _ in range(2))
+    gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, k_out, v_out)
+    f, ax = frequencies(rot, 1e6, sections, layout)
+    cs = cos_sin(pos.numpy(), f, ax)
+    cpu = rows
+    ref = rotate64(cpu[:, :hq], cs)
+    a = cpu[:, :hq].double().abs()
+    mag = torch.cat((a[..., :rot // 2] + a[..., rot // 2:rot],) * 2 + (a[..., rot:],), -1)
+    assert ((q_out.cpu().double() - ref).abs() <= U[io] * ref.abs() + 6 * 2.0 ** -24 * mag).all()
+    # values: every step is exactly rounded, so they are the definition's bits
+    _, _, _, vv = quantise(cpu[:, hq + hkv:], v_group(d))
+    assert torch.equal(v_out.cpu(), vv.to(DT[io]))
+    # keys: the same, but for cosines whose fp32 rounding sits on a border of the float64 ones
+    kr = rotate32(cpu[:, hq:hq + hkv], cs)
+    _, ks, _, kv = quantise(kr, 64)
+    step = ks.repeat_interleave(64, -1)
+    far = (k_out.cpu().double() - kv.to(DT[io]).double()).abs()
+    assert (far <= 1.02 * step + 2 * U[io] * kv.abs() + 2.0 ** -7 * kv.abs()).all()
+    assert (far > 0).double().mean() <= 1e-3
+    # nothing else in the pool changed: clear what the call's tokens occupy in both copies
+    mask = touched(c)
+    assert torch.equal(c.pool[~mask], before[~mask])
+    # appending again is idempotent
+    again = c.pool.clone()
+    gdn.kv_append(c.cfg, plan, q, k, v, pos.cuda(), c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, q_out)
+    assert torch.equal(again, c.pool)
+
+
+def touched(c):
+    """Bytes of the pool that the call's tokens own, from the documented page layout."""
+    d, gk, gv = c.d, c.d // 64, c.d // v_group(c.d)
+    tile = 16 * (d + 4 * (gk + gv))
+    m = torch.zeros(c.pool.shape, dtype=torch.bool)
+    for n in range(c.N):
+        for p in range(c.lens[n] - c.new[n], c.lens[n]):
+            pg, r = int(c.table[n, p // c.page]), p % 16
+            vr = (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3)
+            for h in range(c.hkv):
+                base = (h * (c.page // 16) + p % c.page // 16) * tile
+                for b in range(d // 64):
+                    m[pg, base + b * 512 + r * 32:base + b * 512 + r * 32 + 32] = True
+                    o = base + 16 * d // 2 + b * 512 + vr * 32
+                    m[pg, o:o + 32] = True
+                for s in range(gk + gv):
+                    o = base + 16 * d + s * 64 + r * 4
+                    m[pg, o:o + 4] = True
+    return m.cuda()
+
+
+def test_append_in_place_queries_and_cache_positions():
+    """q_out may be q; positions None rotates by the cache position."""
+    c = Case([3, 2], [10, 0], 4, 2, 128, 16, "f32", seed=5)
+    plan = gdn.rope_plan(128, 1e4)
+    k, v = torch.randn(5, 2, 128).cuda(), torch.randn(5, 2, 128).cuda()
+    q = c.d_q.clone()
+    gdn.kv_append(c.cfg, plan, q, k, v, None, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, q)
+    f, ax = frequencies(128, 1e4, None, "sections")
+    ref = rotate64(c.q, cos_sin(np.array([[10, 11, 12, 0, 1]]), f, ax))
+    assert ((q.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 12 * 2.0 ** -24 * 5).all()
+
+
+def test_append_constant_extreme_and_non_finite_groups():
+    c = Case([8], [0], 1, 1, 128, 16, "f32", seed=6)
+    k = torch.randn(8, 1, 128)
+    k[0] = 0.0
+    k[1] = 2.5
+    k[2, 0, 5] = math.inf
+    k[3, 0, 70] = math.nan
+    k[4] *= 1e30
+    k[5] *= 1e-40  # subnormals
+    k[6, 0, 0], k[6, 0, 1] = 3e38, -3e38  # a range past fp32
+    k[7, 0, :64] = -math.inf
+    v = k.flip(-1).contiguous()
+    gdn.kv_append(c.cfg, None, None, k.cuda(), v.cuda(), None, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, None)
+    ko, vo = torch.empty(8, 1, 128, device="cuda"), torch.empty(8, 1, 128, device="cuda")
+    gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, ko, vo)
+    for got, x, gr in ((ko.cpu(), k, 64), (vo.cpu(), v, 128)):
+        want = quantise(x, gr)[3].float()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(), want.nan_to_num())
+    assert torch.isnan(ko[2, 0, :64]).all() and torch.isfinite(ko[2, 0, 64:]).all()
+
+
+def test_append_padding_rows_and_bad_pages():
+    c = Case([1, 1, 1], [4, 0, 8], 2, 1, 64, 16, "bf16", seed=8)
+    c.d_lens[1] = 0  # a padding row: nothing to store
+    k, v = torch.randn(3, 1, 64).bfloat16().cuda(), torch.randn(3, 1, 64).bfloat16().cuda()
+    before = c.pool.clone()
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    gdn.kv_append(c.cfg, None, None, k, v, None, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, None)
+    assert gdn.device_status() == 0
+    page1 = int(c.table[1, 0])
+    assert torch.equal(c.pool[page1], before[page1])
+    gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, ko, vo)
+    assert (ko[1] == 0).all() and (vo[1] == 0).all() and (ko[0] != 0).any()
+    assert gdn.device_status() == 0
+    # a page id outside the pool, and a length past the table's row: skipped and reported
+    for bad in ("id", "len"):
+        t, lens = c.d_table.clone(), c.d_lens.clone()
+        if bad == "id":
+            t[2, 0] = c.pages
+        else:
+            lens[2] = c.width * c.page + 1
+        before = c.pool.clone()
+        gdn.kv_append(c.cfg, None, None, k, v, None, c.d_cu, c.cu, lens, c.pool, t, None)
+        assert gdn.device_status() & 0xFF == 4
+        page2 = int(c.table[2, 0])
+        assert torch.equal(c.pool[page2], before[page2])
+        gdn.kv_read(c.cfg, c.d_cu, c.cu, lens, c.pool, t, ko, vo)
+        assert gdn.device_status() & 0xFF == 4 and (ko[2] == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------------- attention
+ATTN = [
+    # new, ctx, Hq, Hkv, D, page
+    ([1], [0], 1, 1, 64, 16),
+    ([1], [1], 8, 1, 128, 16),
+    ([1, 1, 1, 1, 1], [0, 14, 15, 16, 63], 24, 2, 128, 64),
+    ([1, 1], [777, 130], 16, 2, 256, 32),
+    ([1], [2500], 24, 2, 128, 64),
+    ([1, 1, 1], [1300, 5, 90], 32, 8, 128, 48),
+    ([1, 1], [300, 40], 12, 12, 64, 128),
+    ([1, 1], [300, 700], 40, 2, 64, 16),
+    ([4, 4, 2], [100, 0, 333], 16, 2, 256, 16),
+    ([3, 4], [29, 61], 6, 2, 128, 64),
+    ([4], [1000], 24, 2, 128, 64),
+    ([0, 7, 0, 1], [3, 20, 0, 0], 6, 3, 64, 32),
+    ([50, 1, 19], [0, 200, 64], 6, 1, 128, 64),
+    ([130], [70], 4, 2, 64, 16),
+    ([37], [150], 6, 2, 256, 64),
+    ([129, 65], [0, 31], 3, 1, 128, 48),
+    ([300], [212], 2, 1, 128, 64),
+    ([1] * 70, list(range(0, 140, 2)), 2, 1, 64, 16),
+]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("new,ctx,hq,hkv,d,page", ATTN)
+def test_attention_against_float64(io, new, ctx, hq, hkv, d, page):
+    c = Case(new, ctx, hq, hkv, d, page, io, seed=hq + d + len(new)).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    o2, lse2 = c.attention()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)  # bit-identical on repetition
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_rows_that_see_nothing(io):
+    """kv_lens 0 (padding) and fewer cached tokens than queries: the rows before the cache see nothing."""
+    c = Case([1, 4, 40], [0, 0, 0], 6, 2, 128, 16, io, seed=2).fill()
+    c.d_lens[0], c.d_lens[1], c.d_lens[2] = 0, 2, 25
+    c.lens = [0, 2, 25]
+    c.k, c.v = [t[:n] for t, n in zip(c.k, c.lens)], [t[:n] for t, n in zip(c.v, c.lens)]
+    o, lse = c.attention()
+    c.check(o, lse)
+    assert (o[:3] == 0).all() and (lse[:3] == -math.inf).all() and (o[5:20] == 0).all()
+    assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_bad_pages_are_reported_and_skipped(new):
+    c = Case([new, new], [100, 60], 6, 2, 128, 16, "bf16", seed=4).fill()
+    t = c.d_table.clone()
+    t[0, 2] = -1
+    t[0, 3] = c.pages + 5
+    o, lse, ws = c.outputs()
+    gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, t, o, lse, ws)
+    assert gdn.device_status() & 0xFF == 4
+    # the other sequence is unaffected; this one attends to what is left
+    c.check(o, lse, skip=(0,))
+    keep = [j for j in range(c.lens[0]) if j // 16 not in (2, 3)]
+    kp, vp = quantise(c.k[0], 64)[3], quantise(c.v[0], 128)[3]
+    s = torch.einsum("hd,thd->ht", c.q[0].double(), kp[:c.lens[0] - new + 1].repeat_interleave(3, 1)) * c.scale
+    p = torch.zeros_like(s)
+    keep = [j for j in keep if j < s.shape[1]]
+    p[:, keep] = torch.softmax(s[:, keep], -1)
+    ref = torch.einsum("ht,thd->hd", p, vp[:s.shape[1]].repeat_interleave(3, 1))
+    assert ((o[0].cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -9).all()
+    # a length past the table's row counts the row's tokens
+    lens = c.d_lens.clone()
+    lens[1] = c.width * c.page + 3
+    gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, lens, c.pool, c.d_table, o, lse, ws)
+    assert gdn.device_status() & 0xFF == 4
+
+
+@pytest.mark.parametrize("new", [1, 33])
+def test_attention_non_finite_tokens_reach_only_their_readers(new):
+    """A NaN in a token's value reaches the sequences that see it and no other; masked places are not read."""
+    c = Case([new, new], [40, 40], 4, 2, 64, 16, "bf16", seed=14)
+    c.v[0][3, 0, 5] = math.nan
+    c.fill()
+    o, lse = c.attention()
+    assert torch.isnan(o[:new, :2]).all() and torch.isfinite(o[:new, 2:]).all()
+    o[:new] = 0
+    c.check(o, lse, skip=(0,))
+
+
+def test_attention_large_scores_and_shifts():
+    """Scores around +-1e4 and equal scores: the softmax neither overflows nor loses its sum."""
+    c = Case([1, 1], [90, 90], 2, 2, 64, 16, "f32", seed=15, outlier=False)
+    c.q[0] *= 3e3
+    c.q[1] = 0.0
+    c.d_q = c.q.cuda()
+    c.fill()
+    o, lse = c.attention()
+    kp, vp = quantise(c.k[1], 64), quantise(c.v[1], 64)
+    assert ((o[1].cpu().double() - vp[3].mean(0)).abs() <= 2.0 ** -18 * 8).all()
+    assert ((lse[1].cpu().double() - math.log(91)).abs() <= 2.0 ** -20).all()
+    ref, rl = __import__("attn_ref").attention64(c.q[:1], *(quantise(t[0], 64)[3] for t in (c.k, c.v)), c.scale, 1)
+    assert ((lse[0].cpu().double() - rl[0]).abs() <= 2.0 ** -19 * rl[0].abs()).all()
+    assert torch.isfinite(o).all()
+
+
+def test_attention_strided_queries_no_lse_and_scale():
+    c = Case([2, 5], [30, 9], 6, 2, 128, 16, "bf16", seed=16).fill()
+    o, lse = c.attention()
+    wide = torch.full((c.T, 9, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:8] = c.d_q
+    o2, _, ws = c.outputs()
+    gdn.attention(c.cfg, wide[:, 2:8], c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, o2, None, ws)
+    assert torch.equal(o, o2)
+    cfg = gdn.make_attn_config(6, 2, 128, page_size=16, softmax_scale=0.0)
+    gdn.attention(cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, o2, lse, ws)
+    seen = torch.tensor([31, 32, 10, 11, 12, 13, 14], dtype=torch.float64)
+    assert ((lse.cpu().double() - seen.log().unsqueeze(1)).abs() <= 2.0 ** -20).all()
+
+
+def test_attention_pool_past_two_gigabytes():
+    """Page offsets past 2^31 bytes."""
+    d, page, hkv = 128, 64, 2
+    cfg = gdn.make_attn_config(4, hkv, d, page_size=page)
+    pages = (5 << 30) // gdn.kv_page_bytes(cfg)
+    c = Case([1], [300], 4, hkv, d, page, "bf16", seed=17)
+    pool = torch.empty(pages, gdn.kv_page_bytes(cfg), dtype=torch.uint8, device="cuda")
+    c.pool, c.pages = pool, pages
+    for j in range(c.width):
+        c.table[0, j] = pages - 1 - 3 * j if j % 2 else 2 * j
+    c.d_table = c.table.cuda()
+    c.fill()
+    c.check(*c.attention())
+
+
+def test_attention_streams_and_concurrent_calls():
+    cases = [Case([1] * 8, [900 + 13 * i for i in range(8)], 24, 2, 128, 64, "bf16", seed=s).fill() for s in (1, 2)]
+    want = [c.attention() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(5):
+        outs = []
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                outs.append(c.attention())
+        torch.cuda.synchronize()
+        got.append(outs)
+    for outs in got:
+        for (o, l), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_decode_step_captured_and_replayed_with_growing_lengths():
+    """One graph holds append and attention; kv_lens moves on the device between replays."""
+    N, hq, hkv, d, page, steps = 3, 6, 2, 128, 16, 20
+    ctx = [0, 14, 45]
+    c = Case([1] * N, [x + steps for x in ctx], hq, hkv, d, page, "bf16", seed=21)
+    plan = gdn.rope_plan(64, 1e4)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    pre = np.concatenate(([0], np.cumsum(ctx))).astype(np.int32)
+    kc = torch.cat([t[:n] for t, n in zip(c.k, ctx)]).cuda()
+    vc = torch.cat([t[:n] for t, n in zip(c.v, ctx)]).cuda()
+    gdn.kv_append(c.cfg, plan, None, kc, vc, None, torch.from_numpy(pre).cuda(), pre, lens, c.pool, c.d_table, None)
+    q, k, v = (torch.zeros(N, h, d, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+    q_rot = torch.empty_like(q)
+    o, lse, ws = c.outputs()
+
+    def step():
+        lens.add_(1)
+        gdn.kv_append(c.cfg, plan, q, k, v, None, c.d_cu, c.cu, lens, c.pool, c.d_table, q_rot)
+        gdn.attention(c.cfg, q_rot, c.d_cu, c.cu, lens, c.pool, c.d_table, o, lse, ws)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    g = torch.Generator().manual_seed(1)
+    f, ax = frequencies(64, 1e4, None, "sections")
+    for i in range(steps):
+        qi = torch.randn(N, hq, d, generator=g).bfloat16()
+        q.copy_(qi.cuda())
+        k.copy_(torch.stack([t[n + i] for t, n in zip(c.k, ctx)]).cuda())
+        v.copy_(torch.stack([t[n + i] for t, n in zip(c.v, ctx)]).cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        if i in (0, 1, 2, steps - 1):
+            for n in range(N):
+                L = ctx[n] + i + 1
+                cs = cos_sin(np.arange(L)[None], f, ax)
+                kq = quantise(rotate32(c.k[n][:L], cs), 64)
+                vq = quantise(c.v[n][:L], 128)
+                one = cos_sin(np.array([[L - 1]]), f, ax)
+                qr = rotate32(qi[n:n + 1], one).bfloat16()
+                from attn_ref import attention64, attention_bound
+                ref, _ = attention64(qr, kq[3], vq[3], c.scale, 1)
+                eo, _ = attention_bound(qr, kq, vq, ref, c.scale, 1, "bf16")
+                assert ((o[n:n + 1].cpu().double() - ref).abs() <= eo + 2.0 ** -10).all(), (i, n)
+    assert gdn.device_status() == 0
+
+
+def test_outputs_past_the_last_token_are_left_alone():
+    c = Case([1, 2], [20, 3], 6, 2, 128, 16, "bf16", seed=22).fill()
+    o, lse, ws = c.outputs()
+    big_o = torch.full((c.T + 5, 6, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    big_l = torch.full((c.T + 5, 6), 7.0, device="cuda")
+    gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, big_o, big_l, ws)
+    c.check(big_o[:c.T], big_l[:c.T])
+    assert (big_o[c.T:] == 7.0).all() and (big_l[c.T:] == 7.0).all()

@@ -1,0 +1,159 @@
+"""The product with 4-bit weights through the public calls against float64, and a layer's decode step together."""
+
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_recurrence_deltanet_b200 as gdn
+from attn_ref import DT, U, Case, attention64, quantise, v_group
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    gdn.lib()
+    yield
+    assert gdn.device_status() == 0
+
+
+def weight(N, K, group, seed):
+    """(code [N, K], scale, bias [N, G], packed) with codes past K set, so that reading them would show."""
+    g = torch.Generator().manual_seed(seed)
+    G = -(-K // group)
+    code = torch.randint(0, 16, (N, G * group), generator=g, dtype=torch.uint8)
+    scale = ((0.5 + torch.rand(N, G, generator=g)) * 0.05).bfloat16()
+    bias = (scale.float() * (-7.5 + torch.randn(N, G, generator=g))).bfloat16()
+    packed = gdn.q4_pack((code[:, 0::2] | (code[:, 1::2] << 4)).cuda(), scale.cuda(), bias.cuda(), K, group)
+    return code[:, :K].double(), scale.double(), bias.double(), packed
+
+
+def product(x, code, scale, bias, group):
+    """(y, magnitude of what the sums saw for bf16 io, the same for fp32) in float64."""
+    K = code.shape[1]
+    s, b = (t.repeat_interleave(group, 1)[:, :K] for t in (scale, bias))
+    x = x.double()
+    return x @ (s * code + b).t(), x.abs() @ (144 * s + b.abs()).t(), x.abs() @ (8 * s + (b + 8 * s).abs()).t()
+
+
+def run(x, w, fill=9.0):
+    M, io = x.shape[0], "bf16" if x.dtype == torch.bfloat16 else "f32"
+    y = torch.full((M, w.N), fill, dtype=x.dtype, device="cuda")
+    ws = torch.full((max(256, gdn.linear_q4_workspace_size(M, w.N, w.K, w.group, io)),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    gdn.linear_q4(x, w, y, ws)
+    return y
+
+
+SHAPES = [(1, 16, 64), (1, 1, 8), (1, 5120, 640), (2, 33, 200), (3, 100, 5120), (5, 1000, 128), (7, 17, 72),
+          (8, 256, 1024), (9, 47, 328), (16, 512, 2048), (17, 130, 264), (31, 64, 512), (33, 200, 1000), (64, 320, 768),
+          (65, 70, 136), (100, 257, 512), (200, 129, 640), (300, 520, 1032)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_q4_against_float64(io, group, M, N, K):
+    code, scale, bias, w = weight(N, K, group, M + N + K)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(DT[io])
+    y = run(x.cuda(), w)
+    ref, mag_b, mag_f = product(x, code, scale, bias, group)
+    # exact products, sums that lose at most 2^-20 of the magnitudes (see attention_bound); a long prefill rounds the
+    # weights to bf16 first (half a step each); one final rounding
+    if io == "f32":
+        tol = U[io] * ref.abs() + 2.0 ** -20 * mag_f
+    else:
+        s, b = (t.repeat_interleave(group, 1)[:, :K] for t in (scale, bias))
+        tol = U[io] * ref.abs() + 2.0 ** -20 * mag_b
+        if M > 64:
+            tol += U[io] * (x.double().abs() @ (s * code + b).abs().t())
+    off = (y.cpu().double() - ref).abs() - tol
+    assert off.max() <= 0, off.max()
+    assert torch.equal(y, run(x.cuda(), w, fill=-3.0))
+
+
+def test_linear_q4_zero_rows_and_outputs():
+    _, _, _, w = weight(64, 128, 64, 1)
+    x = torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda")
+    gdn.linear_q4(x, w, torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_linear_q4_ignores_rows_past_the_last_and_reads_no_padding():
+    """Rows of y past M stay; K not a multiple of the group: the tail of x is not read past K."""
+    code, scale, bias, w = weight(50, 72, 64, 2)
+    flat = torch.full((3 * 72 + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(3, 72, generator=torch.Generator().manual_seed(1)).bfloat16()
+    flat[:216] = x.flatten().cuda()
+    y = torch.full((5, 50), 6.0, dtype=torch.bfloat16, device="cuda")
+    gdn.linear_q4(flat[:216].view(3, 72), w, y[:3], torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    assert torch.isfinite(y).all() and (y[3:] == 6.0).all()
+
+
+def test_linear_q4_non_finite_rows_stay_apart():
+    code, scale, bias, w = weight(40, 256, 32, 3)
+    x = torch.randn(6, 256, generator=torch.Generator().manual_seed(1)).bfloat16()
+    clean = run(x.cuda(), w)
+    x[2, 7] = float("inf")
+    y = run(x.cuda(), w)
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[2]).any()
+
+
+def test_linear_q4_captured_on_a_side_stream():
+    _, _, _, w = weight(300, 512, 64, 4)
+    x = torch.randn(4, 512, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    want = run(x, w)
+    y = torch.empty_like(want)
+    ws = torch.empty(max(256, gdn.linear_q4_workspace_size(4, 300, 512, 64)), dtype=torch.uint8, device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        gdn.linear_q4(x, w, y, ws)
+    for _ in range(3):
+        y.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_layer_decode_steps_together():
+    """linear_q4 (q, k, v rows) -> kv_append -> attention -> linear_q4, three steps of two sequences, against the same
+    steps in float64 from each stage's own rounded inputs."""
+    hidden, hq, hkv, d, page, N = 192, 6, 2, 64, 16, 2
+    rows = (hq + 2 * hkv) * d
+    ci, si, bi, w_in = weight(rows, hidden, 64, 5)
+    co, so, bo, w_out = weight(hidden, hq * d, 128, 6)
+    cfg = gdn.make_attn_config(hq, hkv, d, page_size=page)
+    plan = gdn.rope_plan(32, 1e4)
+    table = torch.tensor([[1], [3]], dtype=torch.int32).cuda()
+    pool = torch.full((4, gdn.kv_page_bytes(cfg)), 0xFF, dtype=torch.uint8, device="cuda")
+    cu = np.array([0, 1, 2], np.int32)
+    cu_d, lens = torch.from_numpy(cu).cuda(), torch.zeros(2, dtype=torch.int32, device="cuda")
+    kept_k, kept_v = [[], []], [[], []]
+    g = torch.Generator().manual_seed(2)
+    for step in range(3):
+        x = torch.randn(N, hidden, generator=g).bfloat16()
+        qkv = run(x.cuda(), w_in)
+        ref, mag, _ = product(x, ci, si, bi, 64)
+        assert ((qkv.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag).all()
+        r = qkv.view(N, hq + 2 * hkv, d)
+        lens += 1
+        q_rot = torch.empty(N, hq, d, dtype=torch.bfloat16, device="cuda")
+        gdn.kv_append(cfg, plan, r[:, :hq], r[:, hq:hq + hkv], r[:, hq + hkv:], None, cu_d, cu, lens, pool, table, q_rot)
+        ko, vo = (torch.empty(N, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        gdn.kv_read(cfg, cu_d, cu, lens, pool, table, ko, vo)
+        o = torch.empty(N, hq, d, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(max(256, gdn.attention_workspace_size(cfg, N, N)), dtype=torch.uint8, device="cuda")
+        gdn.attention(cfg, q_rot, cu_d, cu, lens, pool, table, o, None, ws)
+        y = run(o.view(N, hq * d), w_out)
+        for n in range(N):
+            # the cache's values are read back rounded to bf16: half a step of each
+            kept_k[n].append(ko[n].cpu().double())
+            kept_v[n].append(vo[n].cpu().double())
+            k, v = torch.stack(kept_k[n]), torch.stack(kept_v[n])
+            want, _ = attention64(q_rot[n:n + 1].cpu(), k, v, d ** -0.5, 1)
+            ds = 2.0 ** -8 * (q_rot[n].cpu().double().abs().sum(-1).max() * k.abs().max() * d ** -0.5)
+            tol = 2.0 ** -8 * want.abs() + (2 * ds + 2.0 ** -8 + 2.0 ** -12) * v.abs().max()
+            assert ((o[n:n + 1].cpu().double() - want).abs() <= tol).all()
+        ref, mag, _ = product(o.view(N, -1).cpu(), co, so, bo, 128)
+        assert ((y.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag).all()
