@@ -2,95 +2,691 @@
 // sequence of `len` cached tokens, of which the last `new` are the queries' own,
 //   o = sum_t p_t v_t,  p = softmax over t <= len - new + i of scale q . k_t.
 //
-// One warp per (token, query head): a key a lane for the scores of 32 keys, then
-// D / 32 channels a lane for their values.
+// The codes go to the tensor cores as they are, as small integers, and the
+// scales and biases of their groups are applied outside the products:
+//   q . k_t = sum_g s_tg (q_g . c_tg) + b_tg sum(q_g),
+//   o = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (b_t + 8 s_t),
+// so that nothing is rounded but p_t s_t, which goes in two bf16 parts (three
+// for fp32 io, whose queries go in three as well).  A 4-bit code becomes a bf16
+// by masking it into the low mantissa bits of 128.
+//
+// Split.  The query rows of a (sequence, key/value head) are cut into tiles of
+// 16 (query token, query head) rows, 8 where no sequence has more.  The 16-token
+// cache tiles of all (sequence, head, row tile) groups, end to end, are cut into
+// equal quotas, one a block, so that ragged lengths fill the SMs evenly; the
+// four warps of a block take every fourth tile of its piece and join at the
+// piece's end.  A group that crosses blocks leaves unnormalised partial rows in
+// the workspace for attn_combine_kernel.
+#include <algorithm>
+
 #include "../../include/gdn.h"
 #include "internal.h"
 #include "kv4.cuh"
+#include "tc.cuh"
 
 namespace gdn {
 namespace {
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attention_kernel(AttnProblem a, KvCache cache, int32_t* status) {
-  __shared__ float s_q[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-  if (row >= (int64_t)a.T * a.Hq) return;
-  const int t = (int)(row / a.Hq), hq = (int)(row - (int64_t)t * a.Hq), h = hq / (a.Hq / cache.Hkv);
-  const int n = seq_of(a.cu, a.N, t), len = cache.lens[n];
-  const int seen = len - (a.cu[n + 1] - t) + 1;  // keys this query sees
-  for (int c = lane; c < D; c += 32) s_q[warp][c] = to_f(((const T*)a.q)[t * a.ldq + (int64_t)hq * D + c]);
-  __syncwarp();
-  constexpr int CL = D / 32;
-  float m = -INFINITY, l = 0.0f, o[CL];
-#pragma unroll
-  for (int i = 0; i < CL; ++i) o[i] = 0.0f;
-  for (int j0 = 0; j0 < seen; j0 += 32) {
-    const int j = j0 + lane;
-    const int64_t at = j < seen ? kv_tile_at(cache, D, n, j, h) : -1;
-    if (j < seen && at < 0) set_status(status, kStatusBadPage | (GDN_K_ATTENTION << 8));
-    float s = -INFINITY;
-    if (at >= 0) {
-      const unsigned char* tile = cache.pool + at;
-      const uint32_t* sc = reinterpret_cast<const uint32_t*>(tile + kv_scale_off(D)) + j % kKvTile;
-      s = 0.0f;
-      for (int c = 0; c < D; c += 8) {
-        float k[8];
-        dequantise8(*reinterpret_cast<const uint32_t*>(tile + (c / 64) * 512 + (j % kKvTile) * 32 + (c % 64) / 2),
-                    sc[(c / kKGroup) * kKvTile], k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(s_q[warp][c + i], k[i], s);
-      }
-      s *= a.scale;
-    }
-    float mx = s;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float p = at >= 0 ? expf(s - mn) : 0.0f, r = expf(m - mn);
-    l = l * r + warp_sum(p);
-#pragma unroll
-    for (int i = 0; i < CL; ++i) o[i] *= r;
-    m = mn;
-    for (int u = 0; u < 32; ++u) {
-      const int64_t au = __shfl_sync(0xffffffffu, at, u);
-      const float pu = __shfl_sync(0xffffffffu, p, u);
-      if (au < 0) continue;
-      const unsigned char* tile = cache.pool + au;
-      const int ju = (j0 + u) % kKvTile, c = lane * CL;
-      const uint32_t sw = reinterpret_cast<const uint32_t*>(tile + kv_scale_off(D))[(D / kKGroup + c / v_group(D)) * kKvTile + ju];
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + kv_v_off(D) + (c / 64) * 512 + v_row(ju) * 32 + (c % 64) / 8 * 4);
-      float v[8];
-      dequantise8(w >> (4 * (c % 8)), sw, v);
-#pragma unroll
-      for (int i = 0; i < CL; ++i) o[i] = fmaf(pu, v[i], o[i]);
-    }
-  }
-  const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-#pragma unroll
-  for (int i = 0; i < CL; ++i) ((T*)a.o)[row * D + lane * CL + i] = from_f<T>(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m + logf(l);
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kMinTiles = 8;  // the least quota: two tiles a warp
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;  // how far (powers of two) a score may pass the running maximum before it moves
+
+constexpr int stages(int D) { return D == 64 ? 8 : D == 128 ? 6 : 4; }
+constexpr int blocks_per_sm(int D) { return D == 256 ? 2 : 3; }
+// queries in shared memory where a warp's copy would take over half of its registers
+constexpr bool q_in_smem(int D, int TQ) { return D * TQ > 128; }
+constexpr int smem_bytes(int D, int TQ) {
+  return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
-template <typename T>
-void attention_d(const AttnProblem& p, const KvCache& c, int grid, int32_t* status, cudaStream_t st) {
-  if (p.D == 64) attention_kernel<T, 64><<<grid, 128, 0, st>>>(p, c, status);
-  else if (p.D == 128) attention_kernel<T, 128><<<grid, 128, 0, st>>>(p, c, status);
-  else attention_kernel<T, 256><<<grid, 128, 0, st>>>(p, c, status);
+// Partial rows of the blocks: slot 2b holds block b's part of a group that starts in an earlier block, slot 2b + 1
+// that of a group that starts in b and leaves it.
+struct Workspace {
+  float* o;     // [2 * blocks][16][D]
+  float2* ml;   // [2 * blocks][16]: running maximum (log2 units) and sum
+  int4* split;  // [blocks]: (sequence, head, row tile, last block) of the group that starts in b and leaves it, or last -1
+};
+
+struct Args {
+  AttnProblem p;
+  KvCache cache;
+  Workspace ws;
+  int32_t G;  // blocks
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8
+__device__ __forceinline__ uint32_t code128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t code8(uint32_t w) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(code128(w)), "r"(0x43084308u));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// rows of a sequence's query tile, the keys they see, and the cache tiles that covers
+struct Rows {
+  int32_t rows;   // new * (Hq / Hkv)
+  int32_t first;  // keys that query token 0 sees: len - new + 1
+  int32_t cap;    // positions that the page table's row covers
+};
+__device__ __forceinline__ Rows rows_of(const Args& a, int n) {
+  const int nw = a.p.cu[n + 1] - a.p.cu[n];
+  return Rows{nw * (a.p.Hq / a.cache.Hkv), a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
+}
+template <int RT>
+__device__ __forceinline__ int tiles_of(const Args& a, const Rows& r, int rt) {
+  const int last = min(r.rows, (rt + 1) * RT) - 1;  // the tile's last row sees most
+  const int seen = min(r.first + last / (a.p.Hq / a.cache.Hkv), r.cap);
+  return max(1, (seen + kKvTile - 1) / kKvTile);  // at least one: somebody writes the rows
+}
+template <int RT>
+__device__ __forceinline__ int64_t units_of(const Args& a, int n) {
+  const Rows r = rows_of(a, n);
+  int64_t u = 0;
+  for (int rt = 0; rt * RT < r.rows; ++rt) u += tiles_of<RT>(a, r, rt);
+  return u * a.cache.Hkv;
+}
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp) {  // inclusive, over the block's threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += s_warp[w];
+  return v;
+}
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const __grid_constant__ Args a) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int TQ = F32 ? 3 : 1;          // bf16 parts of a query
+  constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, NM = D / 16;
+  constexpr int S = stages(D), TB = kv_tile_bytes(D);
+  constexpr bool QS = q_in_smem(D, TQ);
+  constexpr int NR = RT / 8;               // rows a thread holds: r, and r + 8 with 16-row tiles
+  static_assert(!F32 || RT == 16, "fp32 io runs 16-row tiles");
+
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t s_full[kWarps][S];
+  __shared__ int64_t s_warp[kWarps];
+  __shared__ int64_t s_found[2];           // sequence that holds the block's first unit, units before it
+  __shared__ float2 s_ml[kWarps][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  unsigned char* ring = smem + warp * (S * TB);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + kWarps * S * TB);
+  const AttnProblem& p = a.p;
+  const int Gq = p.Hq / a.cache.Hkv;
+
+  if (threadIdx.x < kWarps * S) tc::mbar_init(&s_full[threadIdx.x / S][threadIdx.x % S], 1);
+  tc::mbar_init_fence();
+
+  // the block's quota of the units, and the sequence it starts in
+  int64_t total = 0;
+  for (int n0 = 0; n0 < p.N; n0 += kThreads) {
+    const int n = n0 + threadIdx.x;
+    const int64_t s = block_scan(n < p.N ? units_of<RT>(a, n) : 0, s_warp);
+    __syncthreads();
+    if (threadIdx.x == kThreads - 1) s_found[0] = s;
+    __syncthreads();
+    total += s_found[0];
+  }
+  const int64_t quota = max((int64_t)kMinTiles, (total + a.G - 1) / a.G);
+  int64_t u = quota * blockIdx.x;
+  const int64_t u_end = min(total, u + quota);
+  if (u >= u_end) {
+    if (threadIdx.x == 0) a.ws.split[blockIdx.x] = make_int4(0, 0, 0, -1);
+    return;
+  }
+  int64_t before = 0;
+  for (int n0 = 0; n0 < p.N; n0 += kThreads) {
+    const int n = n0 + threadIdx.x;
+    const int64_t own = n < p.N ? units_of<RT>(a, n) : 0;
+    const int64_t s = before + block_scan(own, s_warp);
+    __syncthreads();
+    if (n < p.N && s - own <= u && u < s) s_found[0] = n, s_found[1] = s - own;
+    if (threadIdx.x == kThreads - 1) s_warp[0] = s;
+    __syncthreads();
+    before = s_warp[0];
+    __syncthreads();
+    if (before > u) break;
+  }
+  int n = (int)s_found[0];
+  int64_t at = u - s_found[1];  // units of sequence n before u
+
+  // (head, row tile) of sequence n and the tile within it; group: its index over all sequences
+  const float c_log2 = p.scale * kLog2e;
+  Rows rw = rows_of(a, n);
+  int h = 0, rt = 0;
+  {
+    const int64_t per_head = units_of<RT>(a, n) / a.cache.Hkv;
+    h = (int)(at / per_head);
+    at -= h * per_head;
+    while (at >= tiles_of<RT>(a, rw, rt)) at -= tiles_of<RT>(a, rw, rt), ++rt;
+  }
+  uint32_t phase = 0;  // bit s: parity of the ring's stage s
+  bool dead = false;
+
+  while (true) {
+    const int tiles = tiles_of<RT>(a, rw, rt);
+    const int t_begin = (int)at, t_end = (int)min((int64_t)tiles, at + (u_end - u));
+    // rows of this thread: keys seen by each (0 for a row that is none)
+    int lim[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int row = rt * RT + r + 8 * i;
+      lim[i] = row < rw.rows ? max(0, min(rw.first + row / Gq, rw.cap)) : 0;
+      if (row < rw.rows && rw.first + row / Gq > rw.cap) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
+    }
+    const int row_last = min(rw.rows, (rt + 1) * RT) - 1;
+    // every row of the group sees the tiles before this one whole
+    const int whole = row_last - rt * RT + 1 == RT ? min(rw.first + rt * RT / Gq, rw.cap) / kKvTile : 0;
+    const int seen_tiles = (max(0, min(rw.first + row_last / Gq, rw.cap)) + kKvTile - 1) / kKvTile;
+
+    // queries as A fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64, paired (c, c + 4) as the codes are
+    uint32_t qf[QS ? 1 : NM][4];
+    float qsum[NR][GK];
+    if constexpr (QS) __syncthreads();  // the last piece's reads of s_q
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = rt * RT + r + 8 * i;
+      const bool on = i < NR && row < rw.rows;
+      const T* src = (const T*)p.q + (int64_t)(p.cu[n] + (on ? row / Gq : 0)) * p.ldq + (int64_t)(h * Gq + (on ? row % Gq : 0)) * D;
+#pragma unroll
+      for (int g = 0; g < GK; ++g) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+        if (on) {
+          float y[8];
+          load8(src + g * 64 + q * 16, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = y[e];
+          load8(src + g * 64 + q * 16 + 8, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[8 + e] = y[e];
+        }
+        if (i < NR) {
+          float s = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s += x[e];
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          qsum[i < NR ? i : 0][g] = s;
+        }
+#pragma unroll
+        for (int term = 0; term < TQ; ++term) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int e = 8 * (m >> 1) + 2 * (m & 1);
+            const uint32_t f0 = bf16x2(x[e], x[e + 4]), f1 = bf16x2(x[e + 1], x[e + 5]);
+            if constexpr (F32) {
+              x[e] -= lo_bf16(f0), x[e + 4] -= hi_bf16(f0), x[e + 1] -= lo_bf16(f1), x[e + 5] -= hi_bf16(f1);
+            }
+            if constexpr (QS) {
+              if (g % kWarps == warp) {
+                uint32_t* d = reinterpret_cast<uint32_t*>(s_q + ((g * 4 + m) * TQ + term) * 32 + lane);
+                d[i] = f0, d[2 + i] = f1;
+              }
+            } else {
+              qf[g * 4 + m][i] = f0, qf[g * 4 + m][2 + i] = f1;
+            }
+          }
+        }
+      }
+    }
+    if constexpr (QS) __syncthreads();
+
+    float o[CB][8][4];
+    float mx[NR], l[NR], ob[NR][GV];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      mx[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < GV; ++g) ob[i][g] = 0.0f;
+    }
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[cb][j][e] = 0.0f;
+
+    // this warp's tiles: t_begin + warp + 4 j.  Every 32 of them, lane j looks up the place of the j-th.
+    const int stop = min(t_end, seen_tiles);
+    const int count = !dead && t_begin + warp < stop ? (stop - t_begin - warp + kWarps - 1) / kWarps : 0;
+    int64_t place = -1;
+    auto look_up = [&](int j0) {
+      const int t = t_begin + warp + kWarps * (j0 + lane);
+      place = -1;
+      if (j0 + lane < count) {
+        place = kv_tile_at(a.cache, D, n, t * kKvTile, h);
+        if (place < 0) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
+      }
+    };
+    auto fetch = [&](int64_t from, int s) {  // lane 0
+      tc::mbar_expect_tx(&s_full[warp][s], TB);
+      tc::bulk_load(ring + s * TB, a.cache.pool + from, TB, &s_full[warp][s]);
+    };
+    // tile j uses stage j % S; a tile without a page is skipped on both sides
+    look_up(0);
+    int64_t next_place = place;  // places of tiles j0 .. j0 + 31 of the fetch side
+    for (int j = 0; j < S - 1; ++j) {
+      const int64_t f = __shfl_sync(0xffffffffu, next_place, j);
+      if (lane == 0 && j < count && f >= 0) fetch(f, j % S);
+    }
+    int s_use = 0, s_fetch = S - 1;
+    uint32_t valid = __ballot_sync(0xffffffffu, next_place >= 0);  // of the 32 tiles around the use side
+    uint32_t valid_next = valid;
+    for (int j = 0; j < count && !dead; ++j) {
+      const int jf = j + S - 1;
+      if (jf % 32 == 0) {
+        look_up(jf);
+        next_place = place;
+        valid_next = __ballot_sync(0xffffffffu, next_place >= 0);
+      }
+      if (j % 32 == 0 && j > 0) valid = valid_next;
+      {
+        const int64_t f = __shfl_sync(0xffffffffu, next_place, jf % 32);
+        if (lane == 0 && jf < count && f >= 0) fetch(f, s_fetch);
+        s_fetch = s_fetch + 1 == S ? 0 : s_fetch + 1;
+      }
+      const bool here = (valid >> (j % 32)) & 1u;
+      if (here) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_full[warp][s_use], (phase >> s_use) & 1u, kWaitNs))) {
+          set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));
+          dead = true;
+          break;
+        }
+        phase ^= 1u << s_use;
+        const unsigned char* tile = ring + s_use * TB;
+        const int t = t_begin + warp + kWarps * j;
+
+        // scores of the tile's 16 tokens: two 8-token products, tokens 2q and 2q + 1 of each in this thread
+        float s[2][2 * NR];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2 * NR; ++e) s[i][e] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < GK; ++g) {
+          float acc[2][4] = {};
+          uint2 kw[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            kw[i] = *reinterpret_cast<const uint2*>(tile + g * 512 + (8 * i + r) * 32 + q * 8);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int sh = 8 * (m & 1);
+            uint32_t b0[2], b1[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
+              b0[i] = F32 ? code8(w >> sh) : code128(w >> sh);
+              b1[i] = F32 ? code8(w >> (sh + 4)) : code128(w >> (sh + 4));
+            }
+#pragma unroll
+            for (int term = 0; term < TQ; ++term) {
+              uint4 f;
+              if constexpr (QS) f = s_q[((g * 4 + m) * TQ + term) * 32 + lane];
+              else f = make_uint4(qf[g * 4 + m][0], qf[g * 4 + m][1], qf[g * 4 + m][2], qf[g * 4 + m][3]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) mma(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint2 sw = *reinterpret_cast<const uint2*>(tile + kv_scale_off(D) + g * 64 + (8 * i + 2 * q) * 4);
+            const float s0 = lo_bf16(sw.x), s1 = lo_bf16(sw.y);
+            const float z0 = fmaf(F32 ? 8.0f : -128.0f, s0, hi_bf16(sw.x));
+            const float z1 = fmaf(F32 ? 8.0f : -128.0f, s1, hi_bf16(sw.y));
+#pragma unroll
+            for (int k = 0; k < NR; ++k) {
+              s[i][2 * k] = fmaf(s0, acc[i][2 * k], fmaf(z0, qsum[k][g], s[i][2 * k]));
+              s[i][2 * k + 1] = fmaf(s1, acc[i][2 * k + 1], fmaf(z1, qsum[k][g], s[i][2 * k + 1]));
+            }
+          }
+        }
+        // online softmax in powers of two.  The running maximum moves only when a score passes it by kSlack, which is
+        // rare after the first tiles; until then exponentials are at most 2^kSlack.
+        const bool masked = t >= whole;
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2 * NR; ++e) {
+            s[i][e] *= c_log2;
+            if (masked && t * kKvTile + 8 * i + 2 * q + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
+            over |= s[i][e] > mx[e >> 1] + kSlack;
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int k = 0; k < NR; ++k) {
+            float m = fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m, mx[k]);
+            const float f = m == mx[k] ? 1.0f : exp2f(mx[k] - m);
+            mx[k] = m;
+            l[k] *= f;
+#pragma unroll
+            for (int g = 0; g < GV; ++g) ob[k][g] *= f;
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+              for (int jj = 0; jj < 8; ++jj) {
+                o[cb][jj][2 * k] *= f, o[cb][jj][2 * k + 1] *= f;
+                if constexpr (NR == 1) o[cb][jj][2] *= f, o[cb][jj][3] *= f;  // the same row's low part
+              }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          const float m = mx[k] == -INFINITY ? 0.0f : mx[k];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float pe = exp2f(s[i][2 * k + e] - m);
+              s[i][2 * k + e] = pe;
+              l[k] += pe;
+            }
+        }
+        // values: p_t s_t against the codes around 8
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv) {
+          uint32_t ph[4], pl[4], pt[4];  // A fragments: (row r, row r + 8) x (tokens 2q.., tokens 2q + 8..)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint2 sw = *reinterpret_cast<const uint2*>(tile + kv_scale_off(D) + (GK + gv) * 64 + (8 * i + 2 * q) * 4);
+            const float s0 = lo_bf16(sw.x), s1 = lo_bf16(sw.y);
+            const float z0 = fmaf(8.0f, s0, hi_bf16(sw.x)), z1 = fmaf(8.0f, s1, hi_bf16(sw.y));
+#pragma unroll
+            for (int k = 0; k < NR; ++k) {
+              float x0 = s[i][2 * k] * s0, x1 = s[i][2 * k + 1] * s1;
+              float y0 = s[i][2 * k] * z0, y1 = s[i][2 * k + 1] * z1;
+              if (masked) {  // what a row does not see may hold anything
+                const int tok = t * kKvTile + 8 * i + 2 * q;
+                if (tok >= lim[k]) x0 = y0 = 0.0f;
+                if (tok + 1 >= lim[k]) x1 = y1 = 0.0f;
+              }
+              ob[k][gv] += y0 + y1;
+              const uint32_t hi = bf16x2(x0, x1);
+              x0 -= lo_bf16(hi), x1 -= hi_bf16(hi);
+              const uint32_t lo = bf16x2(x0, x1);
+              if constexpr (NR == 1) {  // rows 8 .. 15 of the product carry the low parts of rows 0 .. 7
+                ph[2 * i] = hi, ph[2 * i + 1] = lo;
+              } else {
+                ph[2 * i + k] = hi, pl[2 * i + k] = lo;
+              }
+              if constexpr (F32) pt[2 * i + k] = bf16x2(x0 - lo_bf16(lo), x1 - hi_bf16(lo));
+            }
+          }
+#pragma unroll
+          for (int cb = gv * (CB / GV); cb < (gv + 1) * (CB / GV); ++cb) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = *reinterpret_cast<const uint32_t*>(tile + kv_v_off(D) + cb * 512 + ((e >> 1) * 8 + (e & 1) * 4 + q) * 32 + r * 4);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t sel = half ? 0x7632 : 0x5410;
+              const uint32_t w01 = __byte_perm(w[0], w[1], sel), w23 = __byte_perm(w[2], w[3], sel);
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                const uint32_t b0 = code8(w01 >> (4 * jj)), b1 = code8(w23 >> (4 * jj));
+                float(&c)[4] = o[cb][half * 4 + jj];
+                mma(c, ph[0], ph[1], ph[2], ph[3], b0, b1);
+                if constexpr (NR == 2) mma(c, pl[0], pl[1], pl[2], pl[3], b0, b1);
+                if constexpr (F32) mma(c, pt[0], pt[1], pt[2], pt[3], b0, b1);
+              }
+            }
+          }
+        }
+        __syncwarp();  // the stage is read before lane 0 refills it
+      }
+      s_use = s_use + 1 == S ? 0 : s_use + 1;
+    }
+    // a wait that ran out: the copies still in flight land before the ring is used for the join
+    if (dead) {
+      for (int s = 0; s < S; ++s) tc::mbar_wait(&s_full[warp][s], (phase >> s) & 1u, kWaitNs / 100);
+    }
+
+    // the join: every warp's rows (unnormalised, bias added) into its ring, then all threads over rows and channels
+    float* mine = reinterpret_cast<float*>(ring);
+    constexpr int LD = D + 4;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      float sl = l[k];
+      sl += __shfl_xor_sync(0xffffffffu, sl, 1);
+      sl += __shfl_xor_sync(0xffffffffu, sl, 2);
+#pragma unroll
+      for (int g = 0; g < GV; ++g) {
+        ob[k][g] += __shfl_xor_sync(0xffffffffu, ob[k][g], 1);
+        ob[k][g] += __shfl_xor_sync(0xffffffffu, ob[k][g], 2);
+      }
+      if (q == 0) s_ml[warp][r + 8 * k] = make_float2(mx[k], sl);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)  // channels 16q + 8e + (0 .. 7)
+#pragma unroll
+          for (int jj = 0; jj < 8; jj += 4) {
+            float4 v;
+            float* f = &v.x;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              f[x] = o[cb][jj + x][2 * k + e] + ob[k][cb * GV / CB];
+              if constexpr (NR == 1) f[x] += o[cb][jj + x][2 + e];
+            }
+            *reinterpret_cast<float4*>(mine + (r + 8 * k) * LD + cb * 64 + 16 * q + 8 * e + jj) = v;
+          }
+    }
+    __syncthreads();
+    const bool from_start = t_begin == 0, to_end = t_end == tiles;
+    const int rows_here = row_last - rt * RT + 1;
+    const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+    for (int x = threadIdx.x; x < rows_here * (D / 4); x += kThreads) {
+      const int row = x / (D / 4), c = (x - row * (D / 4)) * 4;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][row].x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sl = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w][row];
+        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+        const float f = exp2f(ml.x - m);
+        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * (S * TB)) + row * LD + c);
+        v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y), v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
+        sl = fmaf(f, ml.y, sl);
+      }
+      if (from_start && to_end) {
+        const int gr = rt * RT + row, tok = p.cu[n] + gr / Gq;
+        const int64_t out = (int64_t)tok * p.Hq + h * Gq + gr % Gq;
+        const float inv = sl == 0.0f ? 0.0f : 1.0f / sl;
+        T* d = (T*)p.o + out * D + c;
+        if constexpr (F32) {
+          *reinterpret_cast<float4*>(d) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        } else {
+          *reinterpret_cast<uint2*>(d) = make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
+        }
+        if (c == 0 && p.lse) p.lse[out] = sl == 0.0f ? -INFINITY : (m + log2f(sl)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(a.ws.o + ((int64_t)slot * 16 + row) * D + c) = v;
+        if (c == 0) a.ws.ml[slot * 16 + row] = make_float2(m, sl);
+      }
+    }
+    if (threadIdx.x == 0 && (from_start || u + tiles - t_begin >= u_end))  // the quota's last group writes last
+      a.ws.split[blockIdx.x] =
+          make_int4(n, h, rt, from_start && !to_end ? (int)((u - t_begin + tiles - 1) / quota) : -1);
+    u += t_end - t_begin;
+    if (u >= u_end) break;
+    tc::fence_async_all();  // the join's writes to the ring, before the next piece's copies into it
+    __syncthreads();
+    at = 0;
+    if ((rt + 1) * RT < rw.rows) {
+      ++rt;
+    } else {
+      rt = 0;
+      if (++h == a.cache.Hkv) {
+        h = 0;
+        do ++n; while (p.cu[n + 1] == p.cu[n]);  // a sequence without queries has no units
+        rw = rows_of(a, n);
+      }
+    }
+  }
+}
+
+// One block per (split group, row): joins the partial rows that the group's blocks have left.  Block x takes the x-th
+// of the blocks that started a group and did not finish it.
+constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32;
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ Args a) {
+  __shared__ float s_o[kCombineWarps][D];
+  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
+  __shared__ int s_count[kCombineWarps], s_first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
+  if (threadIdx.x == 0) s_first = -1;
+  int seen = 0;
+  for (int b0 = 0; b0 < a.G; b0 += kCombineThreads) {
+    const int b = b0 + threadIdx.x;
+    const bool is = b < a.G && a.ws.split[b].w >= 0;
+    const uint32_t ball = __ballot_sync(0xffffffffu, is);
+    __syncthreads();
+    if (lane == 0) s_count[warp] = __popc(ball);
+    __syncthreads();
+    int before = seen;
+    for (int w = 0; w < kCombineWarps; ++w) {
+      if (w < warp) before += s_count[w];
+      seen += s_count[w];
+    }
+    if (is && before + __popc(ball & ((1u << lane) - 1u)) == (int)blockIdx.x) s_first = b;
+  }
+  __syncthreads();
+  const int first = s_first;
+  if (first < 0) return;
+  const int4 sp = a.ws.split[first];
+  const Rows rw = rows_of(a, sp.x);
+  const int gr = sp.z * RT + row;
+  if (gr >= rw.rows) return;
+  const int Gq = a.p.Hq / a.cache.Hkv, parts = sp.w - first + 1;
+  auto slot_of_part = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * 16 + row; };
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < parts; i += kCombineThreads) m = fmaxf(m, a.ws.ml[slot_of_part(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_m[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) m = fmaxf(m, s_m[w]);
+  constexpr int CL = D / 32;
+  float v[CL], l = 0.0f;
+#pragma unroll
+  for (int x = 0; x < CL; ++x) v[x] = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < parts; i += kCombineWarps) {
+    const int64_t slot = slot_of_part(i);
+    const float2 ml = a.ws.ml[slot];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // nothing seen
+    const float f = exp2f(ml.x - m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int x = 0; x < CL; ++x) v[x] = fmaf(f, a.ws.o[slot * D + x * 32 + lane], v[x]);
+  }
+#pragma unroll
+  for (int x = 0; x < CL; ++x) s_o[warp][x * 32 + lane] = v[x];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  float sl = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) sl += s_l[w];
+  const int64_t out = (int64_t)(a.p.cu[sp.x] + gr / Gq) * a.p.Hq + sp.y * Gq + gr % Gq;
+  for (int c = threadIdx.x; c < D; c += kCombineThreads) {
+    float y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) y += s_o[w][c];
+    ((T*)a.p.o)[out * D + c] = from_f<T>(sl == 0.0f ? 0.0f : y / sl);
+  }
+  if (threadIdx.x == 0 && a.p.lse) a.p.lse[out] = sl == 0.0f ? -INFINITY : (m + log2f(sl)) * kLn2;
+}
+
+constexpr int kSms = 148;
+int grid_of(int D) { return kSms * blocks_per_sm(D); }
+
+struct WsLayout {
+  size_t o, ml, split, total;
+};
+WsLayout ws_layout(int D) {
+  const size_t g = (size_t)grid_of(D);
+  WsLayout w;
+  w.o = 0;
+  w.ml = w.o + g * 2 * 16 * D * sizeof(float);
+  w.split = w.ml + g * 2 * 16 * sizeof(float2);
+  w.total = (w.split + g * sizeof(int4) + 255) / 256 * 256;
+  return w;
+}
+
+template <typename T, int D, int RT>
+cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
+  const WsLayout w = ws_layout(D);
+  unsigned char* b = (unsigned char*)ws;
+  const Args a{p, cache, Workspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)}, grid_of(D), status};
+  constexpr int bytes = smem_bytes(D, sizeof(T) == 4 ? 3 : 1);
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  {
+    LaunchScope scope(GDN_K_ATTENTION, stream);
+    attn_kernel<T, D, RT><<<a.G, kThreads, bytes, stream>>>(a);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // as many split groups as there are groups, or blocks; rows of the longest sequence's tile
+  const int Gq = p.Hq / cache.Hkv;
+  const int64_t groups = ((int64_t)p.T * Gq / RT + p.N) * cache.Hkv;
+  const int rows = (int)std::min<int64_t>(RT, (int64_t)p.max_q * Gq);
+  LaunchScope scope(GDN_K_ATTN_COMBINE, stream);
+  attn_combine_kernel<T, D, RT><<<dim3((unsigned)std::min<int64_t>(groups, a.G), rows), kCombineThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_d(const AttnProblem& p, const KvCache& c, void* ws, int32_t* status, cudaStream_t st) {
+  if (!p.bf16) return run<float, D, 16>(p, c, ws, status, st);
+  // 8-row tiles leave the other half of the products' rows to the low parts of the probabilities
+  if ((int64_t)p.max_q * (p.Hq / c.Hkv) <= 8) return run<__nv_bfloat16, D, 8>(p, c, ws, status, st);
+  return run<__nv_bfloat16, D, 16>(p, c, ws, status, st);
 }
 
 }  // namespace
 
-size_t attention_ws_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t attention_ws_bytes(int32_t, int32_t, int32_t, int32_t, int32_t D) { return ws_layout(D).total; }
 
-cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void*, int32_t* status, cudaStream_t stream) {
-  const int grid = (int)(((int64_t)p.T * p.Hq + 3) / 4);
-  LaunchScope scope(GDN_K_ATTENTION, stream);
-  if (p.bf16) attention_d<__nv_bfloat16>(p, cache, grid, status, stream);
-  else attention_d<float>(p, cache, grid, status, stream);
-  return cudaGetLastError();
+cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
+                             cudaStream_t stream) {
+  if (p.D == 64) return run_d<64>(p, cache, ws, status, stream);
+  if (p.D == 128) return run_d<128>(p, cache, ws, status, stream);
+  return run_d<256>(p, cache, ws, status, stream);
 }
 
 }  // namespace gdn
