@@ -590,7 +590,8 @@ typedef enum {
   GDN_K_ATTN_COMBINE = 22, /* its partial rows joined */
   GDN_K_Q4_PACK = 23,     /* gdn_q4_pack */
   GDN_K_LINEAR_Q4 = 24,   /* product with 4-bit weights */
-  GDN_K_COUNT = 25
+  GDN_K_X_HALF = 25,      /* gdn_linear_q4, many rows: x as the products' operand */
+  GDN_K_COUNT = 26
 } gdn_kernel_id;
 
 GDN_API const char* gdn_kernel_name(int32_t kernel_id);

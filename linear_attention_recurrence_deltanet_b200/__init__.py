@@ -47,7 +47,7 @@ class K:
     """Kernel ids of the profiler (gdn_kernel_id)."""
     (CONV_PREFILL, CONV_STEP, CONV_HISTORY, SCHEDULE, PREFILL_RECURRENT, PREFILL_CHUNKED, DECODE, STATE_CHECKSUM,
      SPLIT_CONV, SPLIT_PREP, SPLIT_CHAIN, SLOT_COPY, GEMM, SEQPAR, DIAG, WY_CONV, WY_PREP, WY_CHAIN, ROPE, KV_APPEND,
-     KV_READ, ATTENTION, ATTN_COMBINE, Q4_PACK, LINEAR_Q4) = range(25)
+     KV_READ, ATTENTION, ATTN_COMBINE, Q4_PACK, LINEAR_Q4, X_HALF) = range(26)
     COUNT = 25
 
 

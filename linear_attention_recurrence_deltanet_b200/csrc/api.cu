@@ -330,7 +330,8 @@ const char* gdn_kernel_name(int32_t id) {
                                            "diag",              "wy_conv",         "wy_prep",
                                            "wy_chain",          "rope",            "kv_append",
                                            "kv_read",           "attention",       "attn_combine",
-                                           "q4_pack",           "linear_q4"};
+                                           "q4_pack",           "linear_q4",
+                                           "x_half"};
   return (id >= 0 && id < GDN_K_COUNT) ? names[id] : "unknown";
 }
 

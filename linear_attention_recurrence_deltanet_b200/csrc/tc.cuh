@@ -180,6 +180,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, uint64_t
   }
 }
 
+// The same with the limit in SM clock cycles, whose counter is read in a few cycles (for loops that wait every few
+// hundred).
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* m, uint32_t parity, int64_t limit) {
+  if (mbar_try_wait(m, parity)) return true;
+  const int64_t t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(m, parity)) return true;
+    if (clock64() - t0 > limit) return false;
+  }
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
 }

@@ -260,8 +260,8 @@ def test_linear_refusals():
 
 def test_packed_bytes_cover_whole_tiles():
     size = ctypes.c_size_t()
-    for N, K, group, want in ((16, 64, 64, 512 + 256), (17, 72, 64, 2 * 2 * 512 + 2 * 256), (0, 64, 32, 0),
-                              (16, 640, 128, 10 * 512 + 2 * 256)):
+    for N, K, group, want in ((16, 64, 64, 512 + 64 + 64), (17, 72, 64, 2 * (2 * 512 + 2 * 64 + 64)), (0, 64, 32, 0),
+                              (16, 640, 128, 10 * 512 + 5 * 64 + 64)):
         gdn.lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(size))
         assert size.value == want, (N, K, group)
 

@@ -59,15 +59,18 @@ def test_linear_q4_against_float64(io, group, M, N, K):
     x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(DT[io])
     y = run(x.cuda(), w)
     ref, mag_b, mag_f = product(x, code, scale, bias, group)
-    # exact products, sums that lose at most 2^-20 of the magnitudes (see attention_bound); a long prefill rounds the
-    # weights to bf16 first (half a step each); one final rounding
+    # exact products, sums that lose at most 2^-20 of the magnitudes (see attention_bound); more than 16 rows of bf16 round
+    # the weights to fp16 first (half a step, 2^-11 each) and x, scaled to below 2^11 by its row's largest, to steps of
+    # 2^-24 at least: 2^-25 / 2^10 of that largest; one final rounding
     if io == "f32":
         tol = U[io] * ref.abs() + 2.0 ** -20 * mag_f
     else:
         s, b = (t.repeat_interleave(group, 1)[:, :K] for t in (scale, bias))
         tol = U[io] * ref.abs() + 2.0 ** -20 * mag_b
-        if M > 64:
-            tol += U[io] * (x.double().abs() @ (s * code + b).abs().t())
+        if M > 16:
+            w64 = (s * code + b).abs().t()
+            tol += 2.0 ** -11 * (x.double().abs() @ w64)
+            tol += 2.0 ** -35 * x.double().abs().amax(1, keepdim=True) * w64.sum(0)
     off = (y.cpu().double() - ref).abs() - tol
     assert off.max() <= 0, off.max()
     assert torch.equal(y, run(x.cuda(), w, fill=-3.0))
