@@ -194,7 +194,8 @@ cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* w
 
 // linear_q4.cu: Y = X W^T with 4-bit weights, group scales and biases
 struct Q4Layout {
-  int32_t tiles, blocks, groups;  // 16-row tiles, 64-column blocks of codes, groups of a row
+  int32_t tiles, blocks, groups;  // 128-row tiles, 64-column blocks of codes, groups of a row
+  int32_t row_groups;             // groups laid out a row
   size_t scale_off, row_off, total_bytes;
 };
 Q4Layout q4_layout(int32_t N, int32_t K, int32_t group);

@@ -4,16 +4,16 @@
 // comment).  Per group
 //   y = sum_g scale_ng (x_g . code_ng) + bias_ng sum(x_g).
 //
-// Packed weights (gdn_q4_pack), zero-filled to whole tiles:
-//   codes   [N / 16 tiles][K / 64 blocks][32 lanes] 16 bytes: lane 4r + q holds the
-//           words of channels 16q .. 16q+7 and 16q+8 .. 16q+15 of row r, then of
-//           row r + 8, of its block -- a warp's fragment of the tile in one
-//           16-byte load a lane.  A word holds channel 2i in its nibble i and
-//           channel 2i + 1 in its nibble 4 + i, so that masking the word gives
-//           pairs of neighbouring channels.
-//   scales  [N / 16 tiles][groups][16 rows] words, scale low, bias high
-//   rows    [N / 16 tiles][16] floats: the power of two that brings the row's
-//           largest weight below 2^11
+// Packed weights (gdn_q4_pack), zero-filled to whole tiles of 128 rows and blocks
+// of 64 channels, so that both kernels stream them with a few large copies:
+//   codes   [tiles][blocks][8 strips of 16 rows][32 lanes] 16 bytes: lane 4r + q
+//           holds the words of channels 16q .. 16q+7 and 16q+8 .. 16q+15 of row r,
+//           then of row r + 8 -- a warp's fragment of the strip in one 16-byte load
+//           a lane.  A word holds channel 2i in its nibble i and channel 2i + 1 in
+//           its nibble 4 + i, so that masking the word gives pairs of neighbours.
+//   scales  [tiles][groups of whole blocks][128 rows] words, scale low, bias high
+//   rows    [tiles][128] floats: the power of two that brings the row's largest
+//           weight below 2^11
 #include <algorithm>
 
 #include "../../include/gdn.h"
@@ -25,7 +25,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kTile = 16, kBlock = 64;
+constexpr int kTile = 128, kStrip = 16, kStrips = 8, kBlock = 64;
+constexpr int kBlockBytes = kTile * kBlock / 2, kGroupBytes = kTile * 4;  // of a tile's codes, of its scale words
 
 __global__ void q4_pack_kernel(const unsigned char* __restrict__ codes, const unsigned short* __restrict__ scales,
                                const unsigned short* __restrict__ biases, int N, int K, int group, int64_t row_bytes,
@@ -34,9 +35,9 @@ __global__ void q4_pack_kernel(const unsigned char* __restrict__ codes, const un
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) {
     uint32_t w = 0;
     if (i < scale_words) {
-      const int64_t blk = i / 128;
-      const int in = (int)(i - blk * 128), lane = in / 4, part = in & 3;
-      const int64_t n = blk / L.blocks * kTile + lane / 4 + (part >> 1) * 8;
+      const int64_t blk = i / (kBlockBytes / 4);
+      const int in = (int)(i % (kBlockBytes / 4)), lane = in / 4 & 31, part = in & 3;
+      const int64_t n = blk / L.blocks * kTile + in / 128 * kStrip + lane / 4 + (part >> 1) * 8;
       const int64_t k0 = blk % L.blocks * kBlock + (lane & 3) * 16 + (part & 1) * 8;
       if (n < N)
         for (int b = 0; b < 4; ++b)
@@ -46,8 +47,8 @@ __global__ void q4_pack_kernel(const unsigned char* __restrict__ codes, const un
             w |= (byte & 15u) << (4 * b) | odd << (16 + 4 * b);
           }
     } else {
-      const int64_t j = i - scale_words, n = j / 16 / L.groups * kTile + j % 16, g = j / 16 % L.groups;
-      if (n < N)
+      const int64_t j = i - scale_words, n = j / kTile / L.row_groups * kTile + j % kTile, g = j / kTile % L.row_groups;
+      if (n < N && g < L.groups)
         w = (uint32_t)scales[n * L.groups + g] | ((uint32_t)biases[n * L.groups + g] << 16);
     }
     out[i] = w;
@@ -83,23 +84,19 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// The weight stream: each warp copies chunks of B blocks of its 16 rows, and their groups' scale words, into a ring of
-// its own, so that the copies run ahead of the products whatever the other warps do.
-template <int B, int S>
-struct Ring {
-  static constexpr int kSlot = B * 512 + 64 * 2 * B;  // groups of 32: two a block
-  unsigned char* smem;
-  uint64_t* full;  // [S]
-  int head = 0;    // chunks asked for
-  __device__ __forceinline__ void fetch(const unsigned char* packed, const Q4Layout& L, int lg, int64_t tile, int block) {
-    const int nb = min(B, L.blocks - block), g0 = (block * kBlock) >> lg;
-    const int ng = min(L.groups, (((block + nb) * kBlock - 1) >> lg) + 1) - g0;
-    unsigned char* d = smem + (head % S) * kSlot;
-    uint64_t* m = full + head % S;
-    tc::mbar_expect_tx(m, nb * 512 + ng * 64);
-    tc::bulk_load(d, packed + (tile * L.blocks + block) * 512, nb * 512, m);
-    tc::bulk_load(d + B * 512, packed + L.scale_off + (tile * L.groups + g0) * 64, ng * 64, m);
-    ++head;
+// The weight stream: one lane copies `nb` blocks of a tile and their groups' scale words into a slot, kScaleAt bytes
+// apart, both completing on `full`.
+struct Stream {
+  const unsigned char *codes, *scales;  // of the tile
+  int lg;
+  __device__ __forceinline__ Stream(const unsigned char* packed, const Q4Layout& L, int tile, int lg_group)
+      : codes(packed + (int64_t)tile * L.blocks * kBlockBytes),
+        scales(packed + L.scale_off + (int64_t)tile * L.row_groups * kGroupBytes), lg(lg_group) {}
+  __device__ __forceinline__ void fetch(unsigned char* slot, int scale_at, int block, int nb, uint64_t* full) const {
+    const int g0 = (block * kBlock) >> lg, ng = (((block + nb) * kBlock - 1) >> lg) + 1 - g0;
+    tc::mbar_expect_tx(full, nb * kBlockBytes + ng * kGroupBytes);
+    tc::bulk_load(slot, codes + (int64_t)block * kBlockBytes, nb * kBlockBytes, full);
+    tc::bulk_load(slot + scale_at, scales + (int64_t)g0 * kGroupBytes, ng * kGroupBytes, full);
   }
 };
 constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
@@ -111,9 +108,11 @@ constexpr int kSms = 148;
 // in fp32, so nothing but the sums is rounded.  bf16 io takes 128 + code (one
 // mask a pair), fp32 io code - 8 and three bf16 parts of x.
 //
-// A block takes 16 weight rows; its warps, and those of the `S` blocks of its
-// cluster, deal the groups of K out and join in shared memory.  The weight
-// stream bounds it: a warp keeps 2 KB of codes in flight ahead of the products.
+// A block takes 128 weight rows; its eight warps, and those of the S blocks of its
+// cluster, deal the 64-channel blocks of K out.  A warp streams its blocks (4 KB
+// of codes and their scales) through a ring of its own and multiplies all 128
+// rows with the x it holds in registers; the warps join in shared memory.  The
+// weight stream bounds it.
 constexpr int kSmallWarps = 8, kSmallThreads = kSmallWarps * 32;
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -132,7 +131,17 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {  // channels 
   return r;
 }
 
-constexpr int kSmallB = 2, kSmallS = 4;  // blocks of a chunk, chunks of a warp's ring
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {  // C = 0
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+constexpr int kSmallSlots = 2, kSmallSlot = kBlockBytes + 2 * kGroupBytes;  // groups of 32: two a block
+constexpr int kSmallSmem = kSmallWarps * kSmallSlots * kSmallSlot;           // 80 KB: two blocks an SM
+constexpr int kRedLd = kTile + 4;                                            // floats between columns of the join
 
 template <typename T, int MT, int G>
 __global__ void __launch_bounds__(kSmallThreads, 2)
@@ -140,165 +149,172 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                         int N, T* __restrict__ y, int S, int32_t* status) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int P = F32 ? 3 : 1;                 // bf16 parts of x
-  constexpr int NB = G == 128 ? 2 : 1;           // 64-channel blocks that are scaled together
   constexpr int SUB = G == 32 ? 2 : 1;           // groups of a block
   constexpr int LG = G == 32 ? 5 : G == 64 ? 6 : 7;
-  using R = Ring<kSmallB, kSmallS>;
-  extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ uint64_t s_full[kSmallWarps][kSmallS];
-  __shared__ float s_part[kSmallWarps][MT * 4][32];
-  __shared__ float s_sum[MT * 128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-  const int rank = (int)blockIdx.x % S, m0 = (int)blockIdx.y * MT * 8;
-  const int first = (int)blockIdx.x / S, stride = (int)gridDim.x / S;  // row tiles of this cluster
-  const int chunks = (L.blocks + kSmallB - 1) / kSmallB, step = S * kSmallWarps, w0 = rank * kSmallWarps + warp;
+  static_assert(kSmallWarps * MT * 8 * kRedLd * 4 <= kSmallSmem, "the join uses the rings");
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t s_full[kSmallWarps][kSmallSlots];
+  __shared__ float s_sum[MT * 8 * kTile];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3, m0 = (int)blockIdx.y * MT * 8;
+  const int rank = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
+  const int step = S * kSmallWarps, first = rank * kSmallWarps + warp;  // this warp's blocks
 
-  if (threadIdx.x < kSmallWarps * kSmallS) tc::mbar_init(&s_full[threadIdx.x / kSmallS][threadIdx.x % kSmallS], 1);
+  if (threadIdx.x < kSmallWarps * kSmallSlots) tc::mbar_init(&s_full[threadIdx.x / kSmallSlots][threadIdx.x % kSmallSlots], 1);
   tc::mbar_init_fence();
   __syncthreads();
-  R ring{ring_smem + warp * kSmallS * R::kSlot, s_full[warp]};
-  int ft = first, fc = w0;  // the next chunk to ask for
-  auto fetch = [&]() {
-    if (fc < chunks && ft < L.tiles) {
-      if (lane == 0) ring.fetch(packed, L, LG, ft, fc * kSmallB);
-      fc += step;
-      if (fc >= chunks) fc = w0, ft += stride;
-    }
-  };
-  for (int i = 0; i < kSmallS; ++i) fetch();
-  int used = 0;
-  bool dead = false;
+  unsigned char* ring = smem + warp * kSmallSlots * kSmallSlot;
+  const Stream stream(packed, L, tile, LG);
+  if (lane == 0)
+    for (int i = 0, b = first; i < kSmallSlots && b < L.blocks; ++i, b += step)
+      stream.fetch(ring + i * kSmallSlot, kBlockBytes, b, 1, &s_full[warp][i]);
 
-  for (int tile = first; tile < L.tiles; tile += stride) {
-  float acc[MT][4];
+  float acc[kStrips][MT][4];
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int i = 0; i < kStrips; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.0f;
+  const T* xp[MT];  // this lane's channels of block 0
+  int kmax[MT];     // channels from there on that are there
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + t * 8 + r;
+    kmax[t] = m < M ? K - q * 16 : 0;
+    xp[t] = x + (int64_t)(m < M ? m : 0) * K + q * 16;
+  }
 
-  for (int c = w0; c < chunks && !dead; c += step) {
-    if (!__all_sync(0xffffffffu, tc::mbar_wait_cycles(ring.full + used % kSmallS, (used / kSmallS) & 1, kWaitCycles))) {
-      set_status(status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
-      dead = true;
-      break;
-    }
-    const unsigned char* slot = ring.smem + (used % kSmallS) * R::kSlot;
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + kSmallB * 512);
+  int slot_i = 0;
+  uint32_t phase = 0;
+  for (int b = first; b < L.blocks; b += step) {
+    // x as B fragments, and its sums over the groups as the product with ones
+    uint32_t f[MT][P][8];
+    float xs[SUB][MT][4];
 #pragma unroll
-    for (int i = 0; i < kSmallB / NB; ++i) {
-      const int u = c * (kSmallB / NB) + i;
-      if (u * NB >= L.blocks) break;
-      float p[SUB][MT][4], xs[SUB][MT][4];
+    for (int t = 0; t < MT; ++t) {
+      const T* src = xp[t] + (int64_t)b * kBlock;
+      const int left = kmax[t] - b * kBlock;
 #pragma unroll
-      for (int g = 0; g < SUB; ++g)
+      for (int h = 0; h < (F32 ? 4 : 2); ++h) {
+        const uint4 v = (F32 ? 4 : 8) * h < left ? ld16(src + (F32 ? 4 : 8) * h) : make_uint4(0, 0, 0, 0);
+        if constexpr (!F32) {
+          f[t][0][4 * h] = v.x, f[t][0][4 * h + 1] = v.y, f[t][0][4 * h + 2] = v.z, f[t][0][4 * h + 3] = v.w;
+        } else {
+          float e[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+          for (int pt = 0; pt < P; ++pt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[g][t][e] = xs[g][t][e] = 0.0f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (u * NB + b >= L.blocks) break;
-        const uint4 cw = *reinterpret_cast<const uint4*>(slot + (i * NB + b) * 512 + lane * 16);
-        uint32_t a[8][2];  // pairs of the lane's 16 channels, rows r and r + 8
-        const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          a[j][0] = code_pair<F32>(w[j >> 2], j & 3);
-          a[j][1] = code_pair<F32>(w[2 + (j >> 2)], j & 3);
-        }
-        const int k = (u * NB + b) * kBlock + q * 16;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const int m = m0 + t * 8 + r;
-          const T* src = x + (int64_t)m * K + k;
-          uint32_t f[P][8];
-          if constexpr (!F32) {
-            uint4 v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              v[h] = m < M && k + 8 * h < K ? ld16(src + 8 * h) : make_uint4(0, 0, 0, 0);
-            f[0][0] = v[0].x, f[0][1] = v[0].y, f[0][2] = v[0].z, f[0][3] = v[0].w;
-            f[0][4] = v[1].x, f[0][5] = v[1].y, f[0][6] = v[1].z, f[0][7] = v[1].w;
-          } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint4 v = m < M && k + 4 * h < K ? ld16(src + 4 * h) : make_uint4(0, 0, 0, 0);
-              float e[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
-#pragma unroll
-              for (int part = 0; part < P; ++part)
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                  const uint32_t z = bf16x2(e[2 * d], e[2 * d + 1]);
-                  f[part][2 * h + d] = z;
-                  e[2 * d] -= lo_bf16(z), e[2 * d + 1] -= hi_bf16(z);
-                }
+            for (int d = 0; d < 2; ++d) {
+              const uint32_t z = bf16x2(e[2 * d], e[2 * d + 1]);
+              f[t][pt][2 * h + d] = z;
+              e[2 * d] -= lo_bf16(z), e[2 * d + 1] -= hi_bf16(z);
             }
-          }
-#pragma unroll
-          for (int part = 0; part < P; ++part)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int g = 0; g < SUB; ++g) {
-                // groups of 32: lanes q < 2 hold the first, q >= 2 the second
-                const bool on = SUB == 1 || (q >> 1) == g;
-                const uint32_t b0 = on ? f[part][2 * j] : 0u, b1 = on ? f[part][2 * j + 1] : 0u;
-                mma(p[g][t], a[2 * j][0], a[2 * j][1], a[2 * j + 1][0], a[2 * j + 1][1], b0, b1);
-                mma(xs[g][t], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, b0, b1);
-              }
         }
       }
 #pragma unroll
+      for (int g = 0; g < SUB; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xs[g][t][e] = 0.0f;
+#pragma unroll
+      for (int pt = 0; pt < P; ++pt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < SUB; ++g) {  // groups of 32: lanes q < 2 hold the first, q >= 2 the second
+            const bool on = SUB == 1 || (q >> 1) == g;
+            mma(xs[g][t], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, on ? f[t][pt][2 * j] : 0u,
+                on ? f[t][pt][2 * j + 1] : 0u);
+          }
+    }
+    if (!tc::mbar_wait_warp(&s_full[warp][slot_i], phase, kWaitCycles)) {
+      set_status(status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
+      break;
+    }
+    const unsigned char* slot = ring + slot_i * kSmallSlot;
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + kBlockBytes) + r;
+#pragma unroll
+    for (int i = 0; i < kStrips; ++i) {
+      const uint4 cw = *reinterpret_cast<const uint4*>(slot + i * 512 + lane * 16);
+      const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+      uint32_t a[8][2];  // pairs of the lane's 16 channels, rows r and r + 8
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[j][0] = code_pair<F32>(w[j >> 2], j & 3);
+        a[j][1] = code_pair<F32>(w[2 + (j >> 2)], j & 3);
+      }
+#pragma unroll
       for (int g = 0; g < SUB; ++g) {
-        if (u * SUB + g >= L.groups) break;
+        float p[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int pt = 0; pt < P; ++pt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool on = SUB == 1 || (q >> 1) == g;
+              const uint32_t f0 = on ? f[t][pt][2 * j] : 0u, f1 = on ? f[t][pt][2 * j + 1] : 0u;
+              if (pt == 0 && j == 0) mma0(p[t], a[0][0], a[0][1], a[1][0], a[1][1], f0, f1);
+              else mma(p[t], a[2 * j][0], a[2 * j][1], a[2 * j + 1][0], a[2 * j + 1][1], f0, f1);
+            }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t w = sc[(i * SUB + g) * 16 + r + 8 * h];
-          const float s = lo_bf16(w), z = fmaf(F32 ? 8.0f : -128.0f, s, hi_bf16(w));
+          const uint32_t sw = sc[g * kTile + i * kStrip + 8 * h];
+          const float s = lo_bf16(sw), z = fmaf(F32 ? 8.0f : -128.0f, s, hi_bf16(sw));
 #pragma unroll
           for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              acc[t][2 * h + e] = fmaf(s, p[g][t][2 * h + e], fmaf(z, xs[g][t][e], acc[t][2 * h + e]));
+              acc[i][t][2 * h + e] = fmaf(s, p[t][2 * h + e], fmaf(z, xs[g][t][e], acc[i][t][2 * h + e]));
         }
       }
     }
-    ++used;
     __syncwarp();  // the slot is read before lane 0 refills it
-    fetch();
+    const int nb = b + kSmallSlots * step;
+    if (lane == 0 && nb < L.blocks) stream.fetch(ring + slot_i * kSmallSlot, kBlockBytes, nb, 1, &s_full[warp][slot_i]);
+    if (++slot_i == kSmallSlots) slot_i = 0, phase ^= 1;
   }
-
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s_part[warp][t * 4 + e][lane] = acc[t][e];
+  // (after a wait that ran out) every copy has landed before the rings take the sums
+  for (int i = 0; i < kSmallSlots; ++i) {
+    const int mine = first < L.blocks ? (L.blocks - first + step - 1) / step : 0, uses = (mine - i + kSmallSlots - 1) / kSmallSlots;
+    if (uses > 0) tc::mbar_wait_warp(&s_full[warp][i], (uses & 1) ^ 1, kWaitCycles / 100);
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 128; i += kSmallThreads) {
+
+  float* red = reinterpret_cast<float*>(smem);  // [warp][column of x][row]
+#pragma unroll
+  for (int i = 0; i < kStrips; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(warp * MT * 8 + t * 8 + 2 * q + (e & 1)) * kRedLd + i * kStrip + r + 8 * (e >> 1)] = acc[i][t][e];
+  __syncthreads();
+  auto put = [&](int i, float v) {
+    const int n = tile * kTile + i % kTile, m = m0 + i / kTile;
+    if (n < N && m < M) y[(int64_t)m * N + n] = from_f<T>(v);
+  };
+  for (int i = threadIdx.x; i < MT * 8 * kTile; i += kSmallThreads) {
+    if (m0 + i / kTile >= M) break;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) v += s_part[w][i >> 5][i & 31];
-    s_sum[i] = v;
+    for (int w = 0; w < kSmallWarps; ++w) v += red[(w * MT * 8 + i / kTile) * kRedLd + i % kTile];
+    if (S == 1) put(i, v);
+    else s_sum[i] = v;
   }
-  if (S > 1) tc::cluster_sync();
-  else __syncthreads();
-  if (rank == 0) {
-    for (int i = threadIdx.x; i < MT * 128; i += kSmallThreads) {
-      const int n_in = i & 15, m_in = i >> 4;  // neighbouring threads write neighbouring outputs
-      const int at = ((m_in >> 3) * 4 + (n_in >> 3) * 2 + (m_in & 1)) * 32 + (n_in & 7) * 4 + ((m_in & 7) >> 1);
-      float v = s_sum[at];
+  if (S == 1) return;
+  tc::cluster_sync();
+  if (rank == 0)
+    for (int i = threadIdx.x; i < MT * 8 * kTile; i += kSmallThreads) {
+      if (m0 + i / kTile >= M) break;
+      float v = s_sum[i];
       for (int o = 1; o < S; ++o) {
         float f;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(tc::mapa_shared(tc::smem_u32(&s_sum[at]), o)));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(tc::mapa_shared(tc::smem_u32(&s_sum[i]), o)));
         v += f;
       }
-      const int n = tile * kTile + n_in, m = m0 + m_in;
-      if (n < N && m < M) y[(int64_t)m * N + n] = from_f<T>(v);
+      put(i, v);
     }
-  }
-  if (S > 1) tc::cluster_sync();  // the leader has read the others' sums
-  }
-  if (dead && lane == 0)  // the copies still in flight land before the block exits
-    for (int j = used; j < ring.head; ++j) tc::mbar_wait_cycles(ring.full + j % kSmallS, (j / kSmallS) & 1, kWaitCycles / 100);
+  tc::cluster_sync();  // the leader has read the others' sums
 }
 
 // ------------------------------------------------------------------ many rows
@@ -311,32 +327,42 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 // as the tiles that the products read.
 //
 // Warp 0 loads x, warp 1 issues the products, warps 2-5 write the accumulator
-// out, warps 6-13 expand.  Two accumulators, so that one tile's output overlaps
-// the next one's products.  With fewer tiles than SMs a cluster of S blocks
-// splits K and joins in the leader's shared memory.
-constexpr int kBM = 128, kExpandWarps = 8, kBigThreads = (6 + kExpandWarps) * 32;
-constexpr int kBigB = 4, kBigS = 3;  // blocks of a chunk, chunks of a warp's ring
-using BigRing = Ring<kBigB, kBigS>;
-constexpr int kWStage = kBM * kBlock * 2, kMaxRing = 8;
-constexpr int kCodeRing = kExpandWarps * kBigS * BigRing::kSlot;  // 60 KB
-constexpr int kBigRing = 147456, kBigSmem = kBigRing + kCodeRing + 1024;  // 144 KB: three stages at 256 rows of x
+// out, warp 6 loads codes and scales, warps 7-30 expand: three groups of
+// eight, a warp each 16-row strip, take the blocks in turn, since a block's way
+// through a warp takes longer than its products.
+// Two accumulators, so that one tile's output overlaps the next one's products.
+// Rounds of whole tiles, then the remaining tiles in S slices of K each: their
+// sums go to the workspace, and the block that comes last adds them in the order
+// of the slices.
+constexpr int kGroups = 3, kExpandWarps = kGroups * kStrips, kBigThreads = (7 + kExpandWarps) * 32;
+constexpr int kBigB = kGroups, kMaxSlots = 4;  // blocks of a chunk, chunks ahead
+constexpr int kChunk = kBigB * kBlockBytes + 2 * kBigB * kGroupBytes;
+constexpr int kWStage = kTile * kBlock * 2, kMaxRing = 8;
+constexpr int kBigRing = 229376, kBigSmem = kBigRing + 1024;  // chunks and stages: 224 KB
 static_assert(kBigSmem + 2048 <= 232448, "shared memory of a block");
+// chunks: many where tiles of x leave room (and weights come from memory), few beside four stages of 256 rows
+__host__ __device__ constexpr int big_slots(int tn) { return tn <= 128 ? kMaxSlots : 2; }
 
 struct BigArgs {
   const unsigned char* packed;
   Q4Layout L;
   const unsigned char* xh;  // [blocks][mp][128 bytes]
   const float* xf;          // [mp]: power of two of each row
+  float* part;              // [blocks of the last round][tn][128] sums of a slice
+  int32_t* count;           // [tiles of the last round] slices written, 0 at the start
   __nv_bfloat16* y;
-  int32_t M, N, mp, tn, lg_group, S;
+  int32_t M, N, mp, tn, lg_group, full, S;  // rounds of whole tiles; slices of a tile of the last round
   int32_t* status;
 };
 
 // one block a row of x: fp16 scaled to below 2^11, into the layout of the products' operand
 __global__ void __launch_bounds__(256) x_half_kernel(const __nv_bfloat16* __restrict__ x, int M, int K, int blocks, int mp,
-                                                     unsigned char* __restrict__ xh, float* __restrict__ xf) {
+                                                     unsigned char* __restrict__ xh, float* __restrict__ xf,
+                                                     int32_t* __restrict__ count, int counts) {
   __shared__ uint32_t s_top[8];
   const int m = blockIdx.x;
+  if (m == 0)
+    for (int i = threadIdx.x; i < counts; i += 256) count[i] = 0;
   const int chunks = blocks * 8;
   const __nv_bfloat16* row = x + (int64_t)m * K;
   uint32_t top = 0;  // largest finite magnitude, as bits
@@ -391,29 +417,65 @@ __device__ __forceinline__ uint4 expand(uint32_t w, __half2 s, __half2 b) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A named barrier of n threads: whether any of them passed true.  One warp of a group polls an mbarrier and the others
+// wait here: an arrival at any mbarrier wakes every warp that polls one, and with 20 of them polling their tries took
+// more issue slots than the expansion (2048 rows: 232 us).
+__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+// a group's wait for up to two mbarriers
+__device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* m0, uint32_t p0, uint64_t* m1, uint32_t p1) {
+  bool ok = true;
+  if (polls) ok = tc::mbar_wait_warp(m0, p0, kWaitCycles) && (!m1 || tc::mbar_wait_warp(m1, p1, kWaitCycles));
+  return !bar_or(id, n, !ok);
+}
+
 __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid_constant__ BigArgs a) {
   using namespace tc;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full_c[kExpandWarps][kBigS], full_x[kMaxRing], full_w[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
+  unsigned char* sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (an offset, so that the accesses stay shared ones)
+  __shared__ uint64_t full_c[kMaxSlots], free_c[kMaxSlots];
+  __shared__ uint64_t full[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tslot;
+  __shared__ int s_last;
   bool bad = false;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int xbytes = a.tn * 128, stage_bytes = kWStage + xbytes;
-  const int stages = min(kMaxRing, kBigRing / stage_bytes);
-  const int mt = a.mp / a.tn, nt = (a.N + kBM - 1) / kBM;
-  const int rank = a.S > 1 ? (int)cluster_ctarank() : 0;
-  const int tiles = mt * nt, first = (int)blockIdx.x / a.S, stride = (int)gridDim.x / a.S;
-  auto slice = [&](int i) { return i == a.S ? a.L.blocks : (int)((int64_t)a.L.blocks * i / a.S) & ~1; };  // whole groups
-  const int kb0 = slice(rank), nk = slice(rank + 1) - kb0;
+  const int slots = big_slots(a.tn), stages = min(kMaxRing, (kBigRing - slots * kChunk) / stage_bytes);
+  unsigned char* chunks = sm + stages * stage_bytes;
+  const int mt = a.mp / a.tn, tiles = mt * a.L.tiles;
+  // this block's pieces: whole tiles, then a slice of one
+  struct Piece {
+    int tile, k0, k1;
+  };
+  auto piece = [&](int i, Piece& p) {
+    if (i < a.full) {
+      p = Piece{i * (int)gridDim.x + (int)blockIdx.x, 0, a.L.blocks};
+      return true;
+    }
+    const int t = a.full * (int)gridDim.x + (int)blockIdx.x / a.S, j = (int)blockIdx.x % a.S;
+    if (i > a.full || t >= tiles) return false;
+    auto slice = [&](int v) { return v == a.S ? a.L.blocks : (int)((int64_t)a.L.blocks * v / a.S) & ~1; };  // whole groups
+    p = Piece{t, slice(j), slice(j + 1)};
+    return true;
+  };
+  Piece p;
 
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(&full_x[s], 1);
-      mbar_init(&full_w[s], kExpandWarps);
+      mbar_init(&full[s], 2);  // x, and the warps that expand its weights
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kExpandWarps * kBigS; ++s) mbar_init(&full_c[s / kBigS][s % kBigS], 1);
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(&full_c[s], 1);
+      mbar_init(&free_c[s], kGroups);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 4);
@@ -426,152 +488,176 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
   const uint32_t tbase = tslot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // x_half_kernel's output
-      int i = 0, last[kMaxRing];
-      for (int s = 0; s < kMaxRing; ++s) last[s] = -1;
-      for (int t = first; t < tiles && !bad; t += stride) {
-        const int m0 = (t % mt) * a.tn;
-        for (int kb = 0; kb < nk; ++kb, ++i) {
-          const int s = i % stages;
-          if (i >= stages && !mbar_wait_cycles(&empty[s], ((i / stages) & 1) ^ 1, kWaitCycles)) {
-            bad = true;
-            break;
-          }
-          mbar_expect_tx(&full_x[s], xbytes);
-          bulk_load(sm + s * stage_bytes + kWStage, a.xh + ((int64_t)(kb0 + kb) * a.mp + m0) * 128, xbytes, &full_x[s]);
-          last[s] = i;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // x_half_kernel's output
+    int i = 0, s = 0;
+    uint32_t phase = 1;
+    for (int j = 0; piece(j, p) && !bad; ++j) {
+      const unsigned char* src = a.xh + ((int64_t)p.k0 * a.mp + (p.tile % mt) * a.tn) * 128;
+      for (int kb = p.k0; kb < p.k1; ++kb, ++i, src += (int64_t)a.mp * 128) {
+        if (i >= stages && !mbar_wait_warp(&empty[s], phase, kWaitCycles)) {
+          bad = true;
+          break;
         }
+        if (elect_one()) {
+          mbar_expect_tx(&full[s], xbytes);
+          bulk_load(sm + s * stage_bytes + kWStage, src, xbytes, &full[s]);
+        }
+        __syncwarp();
+        if (++s == stages) s = 0, phase ^= 1;
       }
-      if (bad)  // let the copies already issued land before the block exits
-        for (int s = 0; s < stages; ++s)
-          if (last[s] >= 0) mbar_wait_cycles(&full_x[s], (last[s] / stages) & 1, kWaitCycles);
     }
+    if (bad)  // let the copies already issued land before the block exits
+      for (int j = max(0, i - stages); j < i; ++j) mbar_wait_warp(&full[j % stages], (j / stages) & 1, kWaitCycles / 100);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc_f16(kBM, a.tn, false, false);
-      int i = 0, j = 0;
-      for (int t = first; t < tiles && !bad; t += stride, ++j) {
-        const int ab = j & 1;
-        if (j >= 2 && !mbar_wait_cycles(&acc_empty[ab], ((j >> 1) & 1) ^ 1, kWaitCycles)) {
+    const uint32_t id = idesc_f16(kTile, a.tn, false, false);
+    const uint64_t dw = desc_kmaj(smem_u32(sm), kTile, 0), dx = desc_kmaj(smem_u32(sm) + kWStage, a.tn, 0);
+    const int stage16 = stage_bytes >> 4;  // addresses count in 16 bytes
+    int s = 0;
+    uint32_t phase = 0;
+    for (int j = 0; piece(j, p) && !bad; ++j) {
+      const int ab = j & 1;
+      if (j >= 2 && !mbar_wait_warp(&acc_empty[ab], ((j >> 1) & 1) ^ 1, kWaitCycles)) {
+        bad = true;
+        break;
+      }
+      fence_after();
+      const uint32_t d = tbase + 256 * ab;
+      for (int kb = p.k0; kb < p.k1; ++kb) {
+        if (!mbar_wait_warp(&full[s], phase, kWaitCycles)) {
           bad = true;
           break;
         }
         fence_after();
-        const uint32_t d = tbase + 256 * ab;
-        for (int kb = 0; kb < nk; ++kb, ++i) {
-          const int s = i % stages;
-          if (!mbar_wait_cycles(&full_x[s], (i / stages) & 1, kWaitCycles) || !mbar_wait_cycles(&full_w[s], (i / stages) & 1, kWaitCycles)) {
-            bad = true;
-            break;
-          }
-          fence_after();
-          const uint32_t w = smem_u32(sm + s * stage_bytes), x = w + kWStage;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk)
-            mma_f16(d, desc_kmaj(w, kBM, kk), desc_kmaj(x, a.tn, kk), id, (kb > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBlock / 16; ++kk)  // 32 bytes further in each row
+            mma_f16(d, dw + (uint32_t)(s * stage16 + 2 * kk), dx + (uint32_t)(s * stage16 + 2 * kk), id, (kb > p.k0 || kk > 0) ? 1u : 0u);
           mma_commit(&empty[s]);
+          if (kb + 1 == p.k1) mma_commit(&acc_full[ab]);
         }
-        if (!bad) mma_commit(&acc_full[ab]);
+        __syncwarp();
+        if (++s == stages) s = 0, phase ^= 1;
       }
-      // every product issued has finished before TMEM is released
-      mma_commit(&drain);
-      mbar_wait_cycles(&drain, 0, kWaitCycles);
     }
-  } else if (warp >= 6) {
-    const int strip = warp - 6, r = lane >> 2, q = lane & 3;
-    const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off);
-    BigRing ring{sm + kBigRing + strip * kBigS * BigRing::kSlot, full_c[strip]};
-    // a strip behind the last row of weights has no chunks: its rows are zeros
-    int ft = first, fb = 0;  // the next chunk to ask for
-    auto fetch = [&]() {
-      while (ft < tiles) {
-        const int tile = (ft / mt) * (kBM / kTile) + strip, block = kb0 + fb;
-        if ((fb += kBigB) >= nk) fb = 0, ft += stride;
-        if (tile >= a.L.tiles) continue;
-        if (lane == 0) ring.fetch(a.packed, a.L, a.lg_group, tile, block);
-        return;
+    // every product issued has finished before TMEM is released
+    if (elect_one()) mma_commit(&drain);
+    __syncwarp();
+    mbar_wait_warp(&drain, 0, kWaitCycles);
+  } else if (warp == 6) {
+    int i = 0, c = 0;
+    uint32_t phase = 1;
+    for (int j = 0; piece(j, p) && !bad; ++j) {
+      const Stream stream(a.packed, a.L, p.tile / mt, a.lg_group);
+      for (int k0 = p.k0; k0 < p.k1; k0 += kBigB, ++i) {
+        if (i >= slots && !mbar_wait_warp(&free_c[c], phase, kWaitCycles)) {
+          bad = true;
+          break;
+        }
+        if (elect_one()) stream.fetch(chunks + c * kChunk, kBigB * kBlockBytes, k0, min(kBigB, p.k1 - k0), &full_c[c]);
+        __syncwarp();
+        if (++c == slots) c = 0, phase ^= 1;
       }
-    };
-    for (int i = 0; i < kBigS; ++i) fetch();
-    int s = 0, used = 0;
-    uint32_t round = 0;
-    for (int t = first; t < tiles && !bad; t += stride) {
-      const int tile = (t / mt) * (kBM / kTile) + strip;
-      const bool on = tile < a.L.tiles;
+    }
+    if (bad)  // let the copies already issued land before the block exits
+      for (int j = max(0, i - slots); j < i; ++j) mbar_wait_warp(&full_c[j % slots], (j / slots) & 1, kWaitCycles / 100);
+  } else if (warp >= 7) {
+    const int strip = (warp - 7) & 7, grp = (warp - 7) >> 3, r = lane >> 2, q = lane & 3;
+    const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off) + strip * kStrip + r;
+    const unsigned char* code_at = chunks + grp * kBlockBytes + strip * 512 + lane * 16;
+    const unsigned char* scale_at = chunks + kBigB * kBlockBytes + (strip * kStrip + r) * 4;
+    unsigned char* row = sm + strip * 2048 + r * 128;
+    const int c0 = ((2 * q) ^ r) << 4, c1 = ((2 * q + 1) ^ r) << 4;
+    int s = 0, c = 0;                    // stage of the next chunk's first block; chunk slot
+    uint32_t round = 0, slot_phase = 0;  // rounds of the stages; phase of the slot
+    for (int j = 0; piece(j, p) && !bad; ++j) {
       float inv[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) inv[h] = on ? __ldg(row_inv + tile * kTile + r + 8 * h) : 0.0f;
-      for (int k0 = 0; k0 < nk && !bad; k0 += kBigB) {
-        const unsigned char* slot = ring.smem + (used % kBigS) * BigRing::kSlot;
-        if (on) {
-          const bool ok = mbar_wait_cycles(ring.full + used % kBigS, (used / kBigS) & 1, kWaitCycles);
-          if (__any_sync(0xffffffffu, !ok)) {
-            bad = true;
-            break;
-          }
+      for (int h = 0; h < 2; ++h) inv[h] = __ldg(row_inv + (p.tile / mt) * kTile + 8 * h);
+      for (int k0 = p.k0; k0 < p.k1; k0 += kBigB) {
+        const bool here = k0 + grp < p.k1;
+        int se = s + grp;
+        uint32_t re = round;
+        if (se >= stages) se -= stages, ++re;
+        if (!group_wait(2 + grp, 32 * kStrips, strip == 0, &full_c[c], slot_phase, here && re > 0 ? &empty[se] : nullptr,
+                        (re & 1) ^ 1)) {
+          bad = true;
+          break;
         }
-        const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + kBigB * 512) - (((kb0 + k0) * kBlock) >> a.lg_group) * 16;
-#pragma unroll
-        for (int e = 0; e < kBigB; ++e) {
-          if (k0 + e >= nk) break;
-          uint4 c = make_uint4(0, 0, 0, 0);
+        if (here) {
+          const uint4 w = *reinterpret_cast<const uint4*>(code_at + c * kChunk);
+          const int g = (((k0 + grp) * kBlock + q * 16) >> a.lg_group) - ((k0 * kBlock) >> a.lg_group);
+          const unsigned char* sc = scale_at + c * kChunk + g * kGroupBytes;
           __half2 sh[2], bh[2];
-          if (on) {
-            c = *reinterpret_cast<const uint4*>(slot + e * 512 + lane * 16);
-            const int g = min(((kb0 + k0 + e) * kBlock + q * 16) >> a.lg_group, a.L.groups - 1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = sc[g * 16 + r + 8 * h];
-              sh[h] = __float2half2_rn(lo_bf16(w) * inv[h]);
-              bh[h] = __float2half2_rn(hi_bf16(w) * inv[h]);
-            }
-          } else {
-            sh[0] = sh[1] = bh[0] = bh[1] = __float2half2_rn(0.0f);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(sc + 32 * h);
+            sh[h] = __float2half2_rn(lo_bf16(v) * inv[h]);
+            bh[h] = __float2half2_rn(hi_bf16(v) * inv[h]);
           }
-          if (round > 0) {
-            const bool ok = mbar_wait_cycles(&empty[s], (round & 1) ^ 1, kWaitCycles);
-            if (__any_sync(0xffffffffu, !ok)) {
-              bad = true;
-              break;
-            }
-          }
-          unsigned char* row = sm + s * stage_bytes + strip * 2048 + r * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * q) ^ r) << 4)) = expand(c.x, sh[0], bh[0]);
-          *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ r) << 4)) = expand(c.y, sh[0], bh[0]);
-          *reinterpret_cast<uint4*>(row + 1024 + (((2 * q) ^ r) << 4)) = expand(c.z, sh[1], bh[1]);
-          *reinterpret_cast<uint4*>(row + 1024 + (((2 * q + 1) ^ r) << 4)) = expand(c.w, sh[1], bh[1]);
+          unsigned char* d = row + se * stage_bytes;
+          *reinterpret_cast<uint4*>(d + c0) = expand(w.x, sh[0], bh[0]);
+          *reinterpret_cast<uint4*>(d + c1) = expand(w.y, sh[0], bh[0]);
+          *reinterpret_cast<uint4*>(d + 1024 + c0) = expand(w.z, sh[1], bh[1]);
+          *reinterpret_cast<uint4*>(d + 1024 + c1) = expand(w.w, sh[1], bh[1]);
           fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full_w[s]);
-          if (++s == stages) s = 0, ++round;
         }
-        if (on && !bad) {
-          ++used;
-          __syncwarp();  // the slot is read before lane 0 refills it
-          fetch();
+        asm volatile("bar.sync %0, %1;" ::"r"(2 + grp), "n"(32 * kStrips) : "memory");
+        if (strip == 0 && lane == 0) {
+          if (here) mbar_arrive(&full[se]);
+          mbar_arrive(&free_c[c]);
         }
+        s += min(kBigB, p.k1 - k0);
+        if (s >= stages) s -= stages, ++round;
+        if (++c == slots) c = 0, slot_phase ^= 1;
       }
     }
-    if (bad && lane == 0)  // the copies still in flight land before the block exits
-      for (int j = used; j < ring.head; ++j) mbar_wait_cycles(ring.full + j % kBigS, (j / kBigS) & 1, kWaitCycles / 100);
-  } else if (a.S == 1) {  // warp w reads TMEM lanes 32 (w % 4) .. + 31: weight rows 32 q + lane
+  } else {  // warp w reads TMEM lanes 32 (w % 4) .. + 31: weight rows 32 q + lane
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int q = warp & 3;
+    const int q = warp & 3, row = 32 * q + lane;
     const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off);
-    int j = 0;
-    for (int t = first; t < tiles; t += stride, ++j) {
-      const int ab = j & 1, m0 = (t % mt) * a.tn, n = (t / mt) * kBM + 32 * q + lane;
+    for (int j = 0; piece(j, p); ++j) {
+      const int ab = j & 1, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
+      const bool split = p.k1 - p.k0 < a.L.blocks;
       const float wf = n < a.N ? 1.0f / __ldg(row_inv + n) : 0.0f;
-      const bool ok = mbar_wait_cycles(&acc_full[ab], (j >> 1) & 1, kWaitCycles);
-      if (__any_sync(0xffffffffu, !ok)) {  // the whole warp leaves together (the TMEM loads are warp-wide)
+      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0)) {  // the four warps leave together
         bad = true;
         break;
       }
       fence_after();
       const uint32_t src = tbase + 256 * ab + ((uint32_t)(32 * q) << 16);
+      if (split) {  // always a block's last piece: no other waits for the accumulator
+        float* mine = a.part + (int64_t)blockIdx.x * a.tn * kTile + row;
 #pragma unroll 1
-      for (int c = 0; c < a.tn; c += 16) {
+        for (int c = 0; c < a.tn; c += 16) {
+          float v[16];
+          tmem_ld16(src + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * kTile, v[e]);
+        }
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (tid == 64) s_last = atomicAdd(a.count + blockIdx.x / a.S, 1) == a.S - 1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!s_last) break;
+        __threadfence();
+        const float* parts = a.part + (int64_t)(blockIdx.x / a.S) * a.S * a.tn * kTile + row;
+#pragma unroll 1
+        for (int c = 0; c < a.tn && m0 + c < a.M; c += 16) {
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __ldcg(parts + (c + e) * kTile);
+          for (int o = 1; o < a.S; ++o)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += __ldcg(parts + ((int64_t)o * a.tn + c + e) * kTile);
+          if (n < a.N)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (m0 + c + e < a.M) a.y[(int64_t)(m0 + c + e) * a.N + n] = __float2bfloat16_rn(v[e] * wf * a.xf[m0 + c + e]);
+        }
+        break;
+      }
+#pragma unroll 1
+      for (int c = 0; c < a.tn && m0 + c < a.M; c += 16) {
         float v[16];
         tmem_ld16(src + c, v);
         if (n < a.N)
@@ -582,51 +668,6 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
-    }
-  }
-  if (a.S > 1) {  // one tile a cluster: the others' sums, [tn][128] floats each, go to the leader's ring
-    const int q = warp & 3, row = 32 * q + lane;
-    const bool epi = warp >= 2 && warp < 6;
-    if (epi) {
-      const bool ok = mbar_wait_cycles(&acc_full[0], 0, kWaitCycles);
-      if (__any_sync(0xffffffffu, !ok)) bad = true;
-      fence_after();
-    }
-    fence_before();
-    __syncwarp();
-    cluster_sync();  // every product of the cluster is done: the leader's ring is free
-    fence_after();
-    const uint32_t src = tbase + ((uint32_t)(32 * q) << 16);
-    if (epi && rank > 0 && !bad) {
-      const uint32_t slot = mapa_shared(smem_u32(sm), 0) + (uint32_t)(((rank - 1) * a.tn) * kBM + row) * 4;
-#pragma unroll 1
-      for (int c = 0; c < a.tn; c += 16) {
-        float v[16];
-        tmem_ld16(src + c, v);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(slot + (uint32_t)(c + e) * kBM * 4), "f"(v[e]) : "memory");
-      }
-    }
-    fence_before();
-    __syncwarp();
-    cluster_sync();
-    fence_after();
-    if (epi && rank == 0 && !bad) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      const int m0 = (first % mt) * a.tn, n = (first / mt) * kBM + row;
-      const float wf = n < a.N ? 1.0f / __ldg(reinterpret_cast<const float*>(a.packed + a.L.row_off) + n) : 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < a.tn; c += 16) {
-        float v[16];
-        tmem_ld16(src + c, v);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          for (int o = 0; o < a.S - 1; ++o) v[e] += reinterpret_cast<const float*>(sm)[(o * a.tn + c + e) * kBM + row];
-          if (n < a.N && m0 + c + e < a.M)
-            a.y[(int64_t)(m0 + c + e) * a.N + n] = __float2bfloat16_rn(v[e] * wf * a.xf[m0 + c + e]);
-        }
-      }
     }
   }
   if (sync_tc_any(bad) && tid == 0) set_status(a.status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
@@ -640,8 +681,9 @@ Q4Layout q4_layout(int32_t N, int32_t K, int32_t group) {
   L.tiles = (N + kTile - 1) / kTile;
   L.blocks = (K + kBlock - 1) / kBlock;
   L.groups = (K + group - 1) / group;
-  L.scale_off = (size_t)L.tiles * L.blocks * 512;
-  L.row_off = L.scale_off + (size_t)L.tiles * L.groups * 64;
+  L.row_groups = std::max(L.groups, L.blocks * kBlock / group);  // groups of 32: two for each block
+  L.scale_off = (size_t)L.tiles * L.blocks * kBlockBytes;
+  L.row_off = L.scale_off + (size_t)L.tiles * L.row_groups * kGroupBytes;
   L.total_bytes = L.row_off + (size_t)L.tiles * kTile * 4;
   return L;
 }
@@ -663,27 +705,25 @@ cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* bi
 
 namespace {
 
+constexpr int kSmallFill = 250;
 constexpr int kSmallRows = 16;  // bf16 io: more rows run linear_big_kernel
 
 template <typename T, int MT, int G>
 cudaError_t run_small(const T* x, int32_t M, int32_t K, const unsigned char* packed, const Q4Layout& L, int32_t N, T* y,
                       int32_t* status, cudaStream_t stream) {
-  using R = Ring<kSmallB, kSmallS>;
-  constexpr int smem = kSmallWarps * kSmallS * R::kSlot;
-  const int mg = (M + MT * 8 - 1) / (MT * 8), chunks = (L.blocks + kSmallB - 1) / kSmallB;
-  int S = 1;  // K over more blocks while row tiles leave SMs without one and a warp keeps two chunks
-  while (S < 8 && (int64_t)L.tiles * mg * S < 4 * kSms && chunks >= 4 * S * kSmallWarps) S *= 2;
-  const int per_row = std::max(1, 2 * kSms / mg / S);  // two blocks an SM
+  const int mg = (M + MT * 8 - 1) / (MT * 8);
+  int S = 1;  // blocks a tile: enough for two an SM, while every warp keeps a block of K
+  while (S < 8 && (int64_t)L.tiles * mg * S < kSmallFill && L.blocks >= 2 * S * kSmallWarps) S *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min(L.tiles, per_row) * S), (unsigned)mg);
+  cfg.gridDim = dim3((unsigned)(L.tiles * S), (unsigned)mg);
   cfg.blockDim = dim3(kSmallThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kSmallSmem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = S, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = S > 1 ? 1 : 0;
-  cudaError_t e = cudaFuncSetAttribute(linear_small_kernel<T, MT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(linear_small_kernel<T, MT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
   if (e != cudaSuccess) return e;
   LaunchScope scope(GDN_K_LINEAR_Q4, stream);
   return cudaLaunchKernelEx(&cfg, linear_small_kernel<T, MT, G>, x, M, K, packed, L, N, y, S, status);
@@ -697,23 +737,36 @@ cudaError_t run_small_g(const T* x, int32_t M, int32_t K, const unsigned char* p
 }
 
 struct BigPlan {
-  int tn, mp, S, grid;
+  int tn, mp, full, S, grid, rem;
 };
-// Rows of x a tile: one that leaves the fewest columns of products on the fullest SM.  A 64-channel step takes 2 cycles
-// a column, and 160 for the expansion of its weights at least.
+// Rows of x a tile, rounds of whole tiles and slices of the rest: the fewest cycles on the fullest SM.  A 64-channel
+// step takes 2 cycles a column in the products and about 300 for the expansion of its weights at least.
 BigPlan big_plan(int32_t M, const Q4Layout& L) {
-  const int64_t nt = (L.tiles * kTile + kBM - 1) / kBM;
-  BigPlan b{};
-  int64_t best = INT64_MAX;
+  const int64_t nt = L.tiles;
+  BigPlan best{};
+  double least = 1e30;
   for (int tn = 16; tn <= 256; tn += 16) {
-    const int64_t mt = (M + tn - 1) / tn, rounds = (nt * mt + kSms - 1) / kSms, cost = rounds * std::max(160, 2 * tn);
-    if (cost < best || (cost == best && nt * mt < nt * (b.mp / b.tn))) best = cost, b.tn = tn, b.mp = (int)(mt * tn);
+    BigPlan b;
+    const int64_t mt = (M + tn - 1) / tn, tiles = nt * mt;
+    b.tn = tn, b.mp = (int)(mt * tn), b.full = (int)(tiles / kSms), b.rem = (int)(tiles % kSms), b.S = 1;
+    if (b.rem) b.S = (int)std::min<int64_t>(std::min(kSms / b.rem, 8), std::max(1, L.blocks / 4));
+    b.grid = b.full ? kSms : b.rem * b.S;
+    const double steps = b.full * (double)L.blocks + (b.rem ? (double)L.blocks / b.S + (b.S > 1 ? 4 : 0) : 0.0);
+    const double cost = steps * std::max(300, 2 * tn);
+    if (cost < least * 0.995) least = cost, best = b;
   }
-  const int64_t tiles = nt * (b.mp / b.tn);
-  b.S = 1;
-  while (b.S < 8 && tiles * (b.S + 1) <= kSms && L.blocks >= 4 * (b.S + 1) && b.S * b.tn * kBM * 4 <= kBigRing) ++b.S;
-  b.grid = b.S > 1 ? (int)tiles * b.S : (int)std::min<int64_t>(tiles, kSms);
-  return b;
+  return best;
+}
+struct BigWs {
+  size_t xf, part, count, total;
+};
+BigWs big_ws(const BigPlan& b, const Q4Layout& L) {
+  BigWs w;
+  w.xf = (size_t)b.mp * L.blocks * 128;
+  w.part = (w.xf + (size_t)b.mp * 4 + 255) / 256 * 256;
+  w.count = w.part + (b.S > 1 ? (size_t)b.rem * b.S * b.tn * kTile * 4 : 0);
+  w.total = w.count + (size_t)b.rem * 4;
+  return w;
 }
 
 }  // namespace
@@ -721,8 +774,7 @@ BigPlan big_plan(int32_t M, const Q4Layout& L) {
 size_t linear_q4_ws_bytes(int32_t M, int32_t N, int32_t K, int32_t group, bool bf16) {
   if (!bf16 || M <= kSmallRows || N == 0) return 0;
   const Q4Layout L = q4_layout(N, K, group);
-  const BigPlan b = big_plan(M, L);
-  return (size_t)b.mp * (L.blocks * 128 + 4);
+  return big_ws(big_plan(M, L), L).total;
 }
 
 cudaError_t launch_linear_q4(bool bf16, const void* x, int32_t M, int32_t K, const void* packed, int32_t N,
@@ -741,27 +793,28 @@ cudaError_t launch_linear_q4(bool bf16, const void* x, int32_t M, int32_t K, con
     return cudaSuccess;
   }
   const BigPlan b = big_plan(M, L);
+  const BigWs bw = big_ws(b, L);
   unsigned char* xh = (unsigned char*)ws;
-  float* xf = (float*)(xh + (size_t)b.mp * L.blocks * 128);
+  float* xf = (float*)(xh + bw.xf);
+  int32_t* count = (int32_t*)(xh + bw.count);
   {
     LaunchScope scope(GDN_K_X_HALF, stream);
-    x_half_kernel<<<(unsigned)b.mp, 256, 0, stream>>>((const __nv_bfloat16*)x, M, K, L.blocks, b.mp, xh, xf);
+    x_half_kernel<<<(unsigned)b.mp, 256, 0, stream>>>((const __nv_bfloat16*)x, M, K, L.blocks, b.mp, xh, xf, count, b.rem);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(linear_big_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBigSmem)) != cudaSuccess) return e;
-  const BigArgs a{w, L, xh, xf, (__nv_bfloat16*)y, M, N, b.mp, b.tn, group == 32 ? 5 : group == 64 ? 6 : 7, b.S, status};
+  const BigArgs a{w, L, xh, xf, (float*)(xh + bw.part), count, (__nv_bfloat16*)y, M, N, b.mp, b.tn,
+                  group == 32 ? 5 : group == 64 ? 6 : 7, b.full, b.S, status};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)b.grid);
   cfg.blockDim = dim3(kBigThreads);
   cfg.dynamicSmemBytes = kBigSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = b.S, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
-  cfg.attrs = at, cfg.numAttrs = b.S > 1 ? 2 : 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
   LaunchScope scope(GDN_K_LINEAR_Q4, stream);
   return cudaLaunchKernelEx(&cfg, linear_big_kernel, a);
 }

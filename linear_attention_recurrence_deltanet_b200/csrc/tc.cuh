@@ -180,19 +180,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, uint64_t
   }
 }
 
-// The same with the limit in SM clock cycles, whose counter is read in a few cycles (for loops that wait every few
-// hundred).
-__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* m, uint32_t parity, int64_t limit) {
-  if (mbar_try_wait(m, parity)) return true;
+// The wait of a whole warp, all lanes together, with the limit in SM clock cycles: true for all lanes or for none.  A
+// converged warp is suspended in the instruction until the phase ends (about 110 cycles from the arrival, 3900 cycles at
+// most); a lane that polls alone is not, and its polls take the issue slots of the warps that work.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int64_t limit) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(m, parity))) return true;
   const int64_t t0 = clock64();
   while (true) {
-    if (mbar_try_wait(m, parity)) return true;
-    if (clock64() - t0 > limit) return false;
+    if (__all_sync(0xffffffffu, mbar_try_wait(m, parity))) return true;
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) return false;
   }
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
+}
+
+// True in one lane of a converged warp.  Branching on it (rather than on a lane number) lets the compiler keep the
+// operands of tcgen05 and bulk-copy instructions in uniform registers without a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 // ---------------------------------------------------------------- TMA

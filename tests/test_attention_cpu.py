@@ -260,8 +260,8 @@ def test_linear_refusals():
 
 def test_packed_bytes_cover_whole_tiles():
     size = ctypes.c_size_t()
-    for N, K, group, want in ((16, 64, 64, 512 + 64 + 64), (17, 72, 64, 2 * (2 * 512 + 2 * 64 + 64)), (0, 64, 32, 0),
-                              (16, 640, 128, 10 * 512 + 5 * 64 + 64)):
+    for N, K, group, want in ((16, 64, 64, 4096 + 512 + 512), (129, 72, 64, 2 * (2 * 4096 + 2 * 512 + 512)), (0, 64, 32, 0),
+                              (16, 640, 128, 10 * 4096 + 5 * 512 + 512), (16, 72, 32, 2 * 4096 + 4 * 512 + 512)):
         gdn.lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(size))
         assert size.value == want, (N, K, group)
 
