@@ -1063,7 +1063,7 @@ gdn_status gdn_attention_workspace_size(const gdn_attn_config* cfg, int64_t tota
   if (total_tokens < 0 || total_tokens > 0x7fffffffLL || num_seqs <= 0 || num_seqs > kMaxSeqs)
     return fail(GDN_E_INVAL, "bad sizes");
   *bytes = gdn::attention_ws_bytes((int32_t)total_tokens, num_seqs, cfg->num_q_heads, cfg->num_kv_heads,
-                                   cfg->head_dim);
+                                   cfg->head_dim, cfg->io_dtype == GDN_BF16);
   return GDN_OK;
 }
 
@@ -1082,7 +1082,7 @@ gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int64_t ldq,
     return s;
   if ((uintptr_t)lse & 3u) return fail(GDN_E_INVAL, "lse is not 4-byte aligned");
   const size_t need = gdn::attention_ws_bytes((int32_t)total, num_seqs, cfg->num_q_heads, cfg->num_kv_heads,
-                                              cfg->head_dim);
+                                              cfg->head_dim, cfg->io_dtype == GDN_BF16);
   if ((s = check_ws(workspace, workspace_bytes, need)) != GDN_OK) return s;
   int dev = 0;
   if ((s = check_device(&dev)) != GDN_OK) return s;

@@ -10,19 +10,12 @@
 // for fp32 io, whose queries go in three as well).  A 4-bit code becomes a bf16
 // by masking it into the low mantissa bits of 128.
 //
-// Split.  The query rows of a (sequence, key/value head) are cut into tiles of
-// 16 (query token, query head) rows, 8 where no sequence has more.  The 16-token
-// cache tiles of all (sequence, head, row tile) groups, end to end, are cut into
-// equal quotas, one a block, so that ragged lengths fill the SMs evenly.  A group
-// counts kGroupUnits tiles more than it has, for its queries, first copies and
-// join.  The four warps of a block take every fourth tile of its piece and join
-// at the piece's end.  A group that crosses blocks leaves unnormalised partial rows in
-// the workspace for attn_combine_kernel.
+// Row tiles of 16 rows, 8 where no sequence has more; tiles of 16 keys
+// (attention.cuh has the cutting).  The four warps of a block take every fourth
+// tile of its piece and join at the piece's end.
 #include <algorithm>
 
-#include "../../include/gdn.h"
-#include "internal.h"
-#include "kv4.cuh"
+#include "attention.cuh"
 #include "tc.cuh"
 
 namespace gdn {
@@ -32,8 +25,6 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroupUnits = 12;  // what a group costs beside its tiles, in tiles
 constexpr int kMinUnits = 24;    // the least quota
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;  // how far (powers of two) a score may pass the running maximum before it moves
 
 constexpr int stages(int D) { return D == 64 ? 8 : D == 128 ? 6 : 4; }
 constexpr int blocks_per_sm(int D) { return D == 256 ? 2 : 3; }
@@ -43,32 +34,6 @@ constexpr int smem_bytes(int D, int TQ) {
   return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
-// Partial rows of the blocks: slot 2b holds block b's part of a group that starts in an earlier block, slot 2b + 1
-// that of a group that starts in b and leaves it.
-struct Workspace {
-  float* o;     // [2 * blocks][16][D]
-  float2* ml;   // [2 * blocks][16]: running maximum (log2 units) and sum
-  int4* split;  // [blocks]: (sequence, head, row tile, last block) of the group that starts in b and leaves it, or last -1
-};
-
-struct Args {
-  AttnProblem p;
-  KvCache cache;
-  Workspace ws;
-  int32_t G;  // blocks
-  int32_t* status;
-};
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {  // 2^x to 2 ulp, subnormal results as zero
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8
 __device__ __forceinline__ uint32_t code128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
 __device__ __forceinline__ uint32_t code8(uint32_t w) {
@@ -83,50 +48,9 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// rows of a sequence's query tile, the keys they see, and the cache tiles that covers
-struct Rows {
-  int32_t rows;   // new * (Hq / Hkv)
-  int32_t first;  // keys that query token 0 sees: len - new + 1
-  int32_t cap;    // positions that the page table's row covers
-};
-__device__ __forceinline__ Rows rows_of(const Args& a, int n) {
-  const int nw = a.p.cu[n + 1] - a.p.cu[n];
-  return Rows{nw * (a.p.Hq / a.cache.Hkv), a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
-}
-template <int RT>
-__device__ __forceinline__ int tiles_of(const Args& a, const Rows& r, int rt) {
-  const int last = min(r.rows, (rt + 1) * RT) - 1;  // the tile's last row sees most
-  const int seen = min(r.first + last / (a.p.Hq / a.cache.Hkv), r.cap);
-  return max(1, (seen + kKvTile - 1) / kKvTile);  // at least one: somebody writes the rows
-}
-// units of a group: kGroupUnits, then its tiles
-template <int RT>
-__device__ __forceinline__ int64_t units_of(const Args& a, int n) {
-  const Rows r = rows_of(a, n);
-  int64_t u = 0;
-  for (int rt = 0; rt * RT < r.rows; ++rt) u += kGroupUnits + tiles_of<RT>(a, r, rt);
-  return u * a.cache.Hkv;
-}
-
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp) {  // inclusive, over the block's threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) v += s_warp[w];
-  return v;
-}
 
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const __grid_constant__ AttnArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int TQ = F32 ? 3 : 1;          // bf16 parts of a query
   constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, NM = D / 16;
@@ -149,55 +73,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
   if (threadIdx.x < kWarps * S) tc::mbar_init(&s_full[threadIdx.x / S][threadIdx.x % S], 1);
   tc::mbar_init_fence();
 
-  // the block's quota of the units, and the sequence it starts in
-  int64_t total = 0;
-  for (int n0 = 0; n0 < p.N; n0 += kThreads) {
-    const int n = n0 + threadIdx.x;
-    const int64_t s = block_scan(n < p.N ? units_of<RT>(a, n) : 0, s_warp);
-    __syncthreads();
-    if (threadIdx.x == kThreads - 1) s_found[0] = s;
-    __syncthreads();
-    total += s_found[0];
-  }
-  const int64_t quota = max((int64_t)kMinUnits, (total + a.G - 1) / a.G);
-  int64_t u = quota * blockIdx.x;
-  const int64_t u_end = min(total, u + quota);
-  if (threadIdx.x == 0) a.ws.split[blockIdx.x] = make_int4(0, 0, 0, -1);
-  if (u >= u_end) return;
-  int64_t before = 0;
-  for (int n0 = 0; n0 < p.N; n0 += kThreads) {
-    const int n = n0 + threadIdx.x;
-    const int64_t own = n < p.N ? units_of<RT>(a, n) : 0;
-    const int64_t s = before + block_scan(own, s_warp);
-    __syncthreads();
-    if (n < p.N && s - own <= u && u < s) s_found[0] = n, s_found[1] = s - own;
-    if (threadIdx.x == kThreads - 1) s_warp[0] = s;
-    __syncthreads();
-    before = s_warp[0];
-    __syncthreads();
-    if (before > u) break;
-  }
-  int n = (int)s_found[0];
-  int64_t at = u - s_found[1];  // units of sequence n before u
-
-  // (head, row tile) of sequence n and the tile within it; group: its index over all sequences
+  AttnWalk<RT, kKvTile, kGroupUnits, kMinUnits> walk;
+  if (!walk.start(a, kThreads, s_warp, s_found)) return;
   const float c_log2 = p.scale * kLog2e;
-  Rows rw = rows_of(a, n);
-  int h = 0, rt = 0;
-  {
-    const int64_t per_head = units_of<RT>(a, n) / a.cache.Hkv;
-    h = (int)(at / per_head);
-    at -= h * per_head;
-    for (int w; at >= (w = kGroupUnits + tiles_of<RT>(a, rw, rt)); ++rt) at -= w;
-  }
   uint32_t phase = 0;  // bit s: parity of the ring's stage s
   bool dead = false;
 
   while (true) {
-    const int tiles = tiles_of<RT>(a, rw, rt);
-    const int64_t left = at + (u_end - u) - kGroupUnits;  // the quota's end, from the group's first tile
-    const int t_begin = (int)max((int64_t)0, at - kGroupUnits), t_end = (int)max((int64_t)0, min((int64_t)tiles, left));
-    if (t_begin < t_end) {
+    if (walk.piece(a)) {
+    const int n = walk.n, h = walk.h, rt = walk.rt, t_begin = walk.t0, t_end = walk.t1;
+    const AttnRows rw = walk.rw;
     // rows of this thread: keys seen by each (0 for a row that is none)
     int lim[NR];
 #pragma unroll
@@ -531,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
           }
     }
     __syncthreads();
-    const bool from_start = t_begin == 0, to_end = t_end == tiles;
+    const bool from_start = t_begin == 0, to_end = t_end == walk.tiles;
     const int rows_here = row_last - rt * RT + 1;
     const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
     for (int x = threadIdx.x; x < rows_here * (D / 4); x += kThreads) {
@@ -566,24 +451,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
         if (c == 0) a.ws.ml[slot * 16 + row] = make_float2(m, sl);
       }
     }
-    if (threadIdx.x == 0 && from_start && !to_end)
-      a.ws.split[blockIdx.x] = make_int4(n, h, rt, (int)((u - at + kGroupUnits + tiles - 1) / quota));
+    if (threadIdx.x == 0 && from_start && !to_end) a.ws.split[blockIdx.x] = make_int4(n, h, rt, walk.last_block());
     }  // a piece with tiles
-    u += kGroupUnits + tiles - at;
-    if (u >= u_end) break;
+    if (!walk.next(a)) break;
     tc::fence_async_all();  // the join's writes to the ring, before the next piece's copies into it
     __syncthreads();
-    at = 0;
-    if ((rt + 1) * RT < rw.rows) {
-      ++rt;
-    } else {
-      rt = 0;
-      if (++h == a.cache.Hkv) {
-        h = 0;
-        do ++n; while (p.cu[n + 1] == p.cu[n]);  // a sequence without queries has no units
-        rw = rows_of(a, n);
-      }
-    }
   }
 }
 
@@ -592,31 +464,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 // 2^(m_i - m) of all parts first, so that the loads of the rows do not wait on one another.
 constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kMaxBlocks = 512;
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ float4 s_o[kCombineThreads];
   __shared__ float s_w[kMaxBlocks], s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ int s_count[kMaxBlocks / 32], s_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
-  if (threadIdx.x == 0) s_first = -1;
-  uint32_t ball[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int b = i * kCombineThreads + threadIdx.x;
-    ball[i] = __ballot_sync(0xffffffffu, b < a.G && a.ws.split[b].w >= 0);
-    if (lane == 0) s_count[i * kCombineWarps + warp] = __popc(ball[i]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    int before = __popc(ball[i] & ((1u << lane) - 1u));
-    for (int w = 0; w < i * kCombineWarps + warp; ++w) before += s_count[w];
-    if (((ball[i] >> lane) & 1u) && before == (int)blockIdx.x) s_first = i * kCombineThreads + threadIdx.x;
-  }
-  __syncthreads();
-  const int first = s_first;
+  const int first = split_group(a, blockIdx.x, s_count, &s_first);
   if (first < 0) return;
   const int4 sp = a.ws.split[first];
-  const Rows rw = rows_of(a, sp.x);
+  const AttnRows rw = rows_of(a, sp.x);
   const int gr = sp.z * RT + row;
   if (gr >= rw.rows) return;
   const int Gq = a.p.Hq / a.cache.Hkv, parts = sp.w - first + 1;
@@ -677,28 +533,32 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   if (c == 0 && a.p.lse) a.p.lse[out] = sl == 0.0f ? -INFINITY : (m + log2f(sl)) * kLn2;
 }
 
-constexpr int kSms = 148;
-int grid_of(int D) { return kSms * blocks_per_sm(D); }
-static_assert(kSms * blocks_per_sm(64) <= kMaxBlocks, "the combine kernel looks at two blocks a thread");
+int grid_of(int D) { return kAttnSms * blocks_per_sm(D); }
+static_assert(kAttnSms * blocks_per_sm(64) <= kMaxBlocks, "split_group looks at two blocks a thread");
 
 struct WsLayout {
   size_t o, ml, split, total;
 };
-WsLayout ws_layout(int D) {
-  const size_t g = (size_t)grid_of(D);
+WsLayout ws_layout(int D, int blocks, int rows) {
+  const size_t g = (size_t)blocks;
   WsLayout w;
   w.o = 0;
-  w.ml = w.o + g * 2 * 16 * D * sizeof(float);
-  w.split = w.ml + g * 2 * 16 * sizeof(float2);
+  w.ml = w.o + g * 2 * rows * D * sizeof(float);
+  w.split = w.ml + g * 2 * rows * sizeof(float2);
   w.total = (w.split + g * sizeof(int4) + 255) / 256 * 256;
   return w;
 }
+AttnWorkspace ws_at(const WsLayout& w, void* ws) {
+  unsigned char* b = (unsigned char*)ws;
+  return AttnWorkspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)};
+}
+
+// bf16 io and heads of up to 128 channels: sequences with more rows a key/value head than this run the long row tiles
+constexpr int kPrefillFrom = 64;
 
 template <typename T, int D, int RT>
 cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
-  const WsLayout w = ws_layout(D);
-  unsigned char* b = (unsigned char*)ws;
-  const Args a{p, cache, Workspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)}, grid_of(D), status};
+  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D), 16), ws), grid_of(D), status};
   constexpr int bytes = smem_bytes(D, sizeof(T) == 4 ? 3 : 1);
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -714,7 +574,7 @@ cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* s
   const int64_t x = std::min<int64_t>(groups, a.G);
   // few rows have many parts: the channels go to D / 32 blocks (131072 tokens, 24 rows: 15.6 -> 6.3 us); many rows have
   // few, and the blocks that find no group cost more (64 sequences of 8 heads: 6.6 us against 14.4)
-  const int z = x * rows <= 2 * kSms ? D / 32 : 1;
+  const int z = x * rows <= 2 * kAttnSms ? D / 32 : 1;
   LaunchScope scope(GDN_K_ATTN_COMBINE, stream);
   attn_combine_kernel<T, D, RT><<<dim3((unsigned)x, rows, z), kCombineThreads, 0, stream>>>(a);
   return cudaGetLastError();
@@ -730,10 +590,17 @@ cudaError_t run_d(const AttnProblem& p, const KvCache& c, void* ws, int32_t* sta
 
 }  // namespace
 
-size_t attention_ws_bytes(int32_t, int32_t, int32_t, int32_t, int32_t D) { return ws_layout(D).total; }
+size_t attention_ws_bytes(int32_t T, int32_t, int32_t Hq, int32_t Hkv, int32_t D, bool bf16) {
+  size_t w = ws_layout(D, grid_of(D), 16).total;
+  if (bf16 && D <= 128 && (int64_t)T * (Hq / Hkv) > kPrefillFrom)
+    w = std::max(w, ws_layout(D, kAttnSms, kPrefillRows).total);
+  return w;
+}
 
 cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
                              cudaStream_t stream) {
+  if (p.bf16 && p.D <= 128 && (int64_t)p.max_q * (p.Hq / cache.Hkv) > kPrefillFrom)
+    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, kPrefillRows), ws), kAttnSms, status}, stream);
   if (p.D == 64) return run_d<64>(p, cache, ws, status, stream);
   if (p.D == 128) return run_d<128>(p, cache, ws, status, stream);
   return run_d<256>(p, cache, ws, status, stream);

@@ -1,0 +1,189 @@
+// What the two attention kernels over the 4-bit cache share: the rows of a
+// sequence's query tiles, the cutting of their cache tiles into equal quotas, one
+// a block, and the partial rows that the blocks leave.
+//
+// Groups.  The query rows of a (sequence, key/value head) are (query token, query
+// head) pairs, cut into row tiles of RT rows; a group is one row tile and counts
+// GU units, for its queries and its output, and one unit for each TT keys that its
+// last row sees.  The units of all groups, end to end, are cut into equal quotas,
+// so that ragged lengths fill the SMs evenly.  A group that crosses blocks leaves
+// unnormalised partial rows in the workspace for a combine kernel.
+#pragma once
+
+#include "../../include/gdn.h"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace gdn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;  // how far (powers of two) a score may pass the running maximum before it moves
+constexpr int kAttnSms = 148;
+
+// Partial rows of the blocks: slot 2b holds block b's part of a group that starts in an earlier block, slot 2b + 1
+// that of a group that starts in b and leaves it.
+struct AttnWorkspace {
+  float* o;     // [2 * blocks][rows][D]
+  float2* ml;   // [2 * blocks][rows]: running maximum (log2 units) and sum
+  int4* split;  // [blocks]: (sequence, head, row tile, last block) of the group that starts in b and leaves it, or last -1
+};
+
+struct AttnArgs {
+  AttnProblem p;
+  KvCache cache;
+  AttnWorkspace ws;
+  int32_t G;  // blocks
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {  // 2^x to 2 ulp, subnormal results as zero
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// rows of a sequence's query tiles and the keys they see
+struct AttnRows {
+  int32_t rows;   // new * (Hq / Hkv)
+  int32_t first;  // keys that query token 0 sees: len - new + 1
+  int32_t cap;    // positions that the page table's row covers
+};
+__device__ __forceinline__ AttnRows rows_of(const AttnArgs& a, int n) {
+  const int nw = a.p.cu[n + 1] - a.p.cu[n];
+  return AttnRows{nw * (a.p.Hq / a.cache.Hkv), a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
+}
+
+// inclusive sum over the block's threads
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += s_warp[w];
+  return v;
+}
+
+// A block's walk over the pieces of its quota.
+template <int RT, int TT, int GU, int MIN>
+struct AttnWalk {
+  int64_t u, u_end, at, quota;  // units: here, the quota's end, into the group, a quota
+  int n, h, rt, tiles;          // sequence, head, row tile; the group's tiles
+  int t0, t1;                   // the piece's tiles
+  AttnRows rw;
+
+  __device__ __forceinline__ int tiles_of(const AttnArgs& a, const AttnRows& r, int i) const {
+    const int last = min(r.rows, (i + 1) * RT) - 1;  // the tile's last row sees most
+    const int seen = min(r.first + last / (a.p.Hq / a.cache.Hkv), r.cap);
+    return max(1, (seen + TT - 1) / TT);  // at least one: somebody writes the rows
+  }
+  __device__ __forceinline__ int64_t head_units(const AttnArgs& a, int i) const {  // of one head of sequence i
+    const AttnRows r = rows_of(a, i);
+    int64_t x = 0;
+    for (int j = 0; j * RT < r.rows; ++j) x += GU + tiles_of(a, r, j);
+    return x;
+  }
+  // Every thread of the block; false: nothing to do.  s_warp: a word a warp, s_found: two.
+  __device__ __forceinline__ bool start(const AttnArgs& a, int threads, int64_t* s_warp, int64_t* s_found) {
+    const int tid = threadIdx.x;
+    int64_t total = 0;
+    for (int n0 = 0; n0 < a.p.N; n0 += threads) {
+      const int i = n0 + tid;
+      const int64_t s = block_scan(i < a.p.N ? head_units(a, i) * a.cache.Hkv : 0, s_warp);
+      __syncthreads();
+      if (tid == threads - 1) s_found[0] = s;
+      __syncthreads();
+      total += s_found[0];
+    }
+    quota = max((int64_t)MIN, (total + a.G - 1) / a.G);
+    u = quota * blockIdx.x;
+    u_end = min(total, u + quota);
+    if (tid == 0) a.ws.split[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (u >= u_end) return false;
+    int64_t before = 0;
+    for (int n0 = 0; n0 < a.p.N; n0 += threads) {
+      const int i = n0 + tid;
+      const int64_t own = i < a.p.N ? head_units(a, i) * a.cache.Hkv : 0;
+      const int64_t s = before + block_scan(own, s_warp);
+      __syncthreads();
+      if (i < a.p.N && s - own <= u && u < s) s_found[0] = i, s_found[1] = s - own;
+      if (tid == threads - 1) s_warp[0] = s;
+      __syncthreads();
+      before = s_warp[0];
+      __syncthreads();
+      if (before > u) break;
+    }
+    n = (int)s_found[0];
+    at = u - s_found[1];
+    rw = rows_of(a, n);
+    const int64_t per_head = head_units(a, n);
+    h = (int)(at / per_head), rt = 0;
+    at -= h * per_head;
+    for (int w; at >= (w = GU + tiles_of(a, rw, rt)); ++rt) at -= w;
+    return true;
+  }
+  // the piece at u; false when the quota holds none of the group's tiles
+  __device__ __forceinline__ bool piece(const AttnArgs& a) {
+    tiles = tiles_of(a, rw, rt);
+    const int64_t left = at + (u_end - u) - GU;  // the quota's end, from the group's first tile
+    t0 = (int)max((int64_t)0, at - GU), t1 = (int)max((int64_t)0, min((int64_t)tiles, left));
+    return t0 < t1;
+  }
+  __device__ __forceinline__ int rows_here() const { return min(RT, rw.rows - rt * RT); }
+  __device__ __forceinline__ int last_block() const { return (int)((u - at + GU + tiles - 1) / quota); }  // of the group
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    u += GU + tiles - at;
+    at = 0;
+    if (u >= u_end) return false;
+    if ((rt + 1) * RT < rw.rows) {
+      ++rt;
+      return true;
+    }
+    rt = 0;
+    if (++h == a.cache.Hkv) {
+      h = 0;
+      do ++n; while (a.p.cu[n + 1] == a.p.cu[n]);  // a sequence without queries has no units
+      rw = rows_of(a, n);
+    }
+    return true;
+  }
+};
+
+// the x-th block that started a group and did not finish it, or -1 (256 threads, up to 512 blocks)
+__device__ __forceinline__ int split_group(const AttnArgs& a, int x, int* s_count, int* s_first) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) *s_first = -1;
+  uint32_t ball[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = i * 256 + threadIdx.x;
+    ball[i] = __ballot_sync(0xffffffffu, b < a.G && a.ws.split[b].w >= 0);
+    if (lane == 0) s_count[i * 8 + warp] = __popc(ball[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int before = __popc(ball[i] & ((1u << lane) - 1u));
+    for (int w = 0; w < i * 8 + warp; ++w) before += s_count[w];
+    if (((ball[i] >> lane) & 1u) && before == x) *s_first = i * 256 + threadIdx.x;
+  }
+  __syncthreads();
+  return *s_first;
+}
+
+// attention_prefill.cu: bf16 io, head dims up to 128, long row tiles
+constexpr int kPrefillRows = 256;
+cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t stream);
+
+}  // namespace gdn

@@ -188,7 +188,7 @@ struct AttnProblem {
   float scale;
   bool bf16;
 };
-size_t attention_ws_bytes(int32_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
+size_t attention_ws_bytes(int32_t T, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, bool bf16);
 cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
                              cudaStream_t stream);
 

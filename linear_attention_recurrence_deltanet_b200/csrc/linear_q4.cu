@@ -417,25 +417,6 @@ __device__ __forceinline__ uint4 expand(uint32_t w, __half2 s, __half2 b) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A named barrier of n threads: whether any of them passed true.  One warp of a group polls an mbarrier and the others
-// wait here: an arrival at any mbarrier wakes every warp that polls one, and with 20 of them polling their tries took
-// more issue slots than the expansion (2048 rows: 232 us).
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-// a group's wait for up to two mbarriers
-__device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* m0, uint32_t p0, uint64_t* m1, uint32_t p1) {
-  bool ok = true;
-  if (polls) ok = tc::mbar_wait_warp(m0, p0, kWaitCycles) && (!m1 || tc::mbar_wait_warp(m1, p1, kWaitCycles));
-  return !bar_or(id, n, !ok);
-}
-
 __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid_constant__ BigArgs a) {
   using namespace tc;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -579,7 +560,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         uint32_t re = round;
         if (se >= stages) se -= stages, ++re;
         if (!group_wait(2 + grp, 32 * kStrips, strip == 0, &full_c[c], slot_phase, here && re > 0 ? &empty[se] : nullptr,
-                        (re & 1) ^ 1)) {
+                        (re & 1) ^ 1, kWaitCycles)) {
           bad = true;
           break;
         }
@@ -601,7 +582,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
           *reinterpret_cast<uint4*>(d + 1024 + c1) = expand(w.w, sh[1], bh[1]);
           fence_async_smem();
         }
-        asm volatile("bar.sync %0, %1;" ::"r"(2 + grp), "n"(32 * kStrips) : "memory");
+        bar_sync(2 + grp, 32 * kStrips);
         if (strip == 0 && lane == 0) {
           if (here) mbar_arrive(&full[se]);
           mbar_arrive(&free_c[c]);
@@ -619,7 +600,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       const int ab = j & 1, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
       const bool split = p.k1 - p.k0 < a.L.blocks;
       const float wf = n < a.N ? 1.0f / __ldg(row_inv + n) : 0.0f;
-      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0)) {  // the four warps leave together
+      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0, kWaitCycles)) {  // the four warps leave together
         bad = true;
         break;
       }

@@ -192,6 +192,27 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int
   }
 }
 
+// A named barrier of n threads: whether any of them passed true.
+__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// A group of warps (n threads, barrier id) waits for up to two mbarriers: one warp polls, the others wait at the barrier.
+// An arrival at any mbarrier wakes every warp that polls one; with 20 of them polling, their tries took more issue
+// slots than the work (the 4-bit product of 2048 rows).  True for all threads or for none.
+__device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* m0, uint32_t p0, uint64_t* m1, uint32_t p1,
+                                           int64_t limit) {
+  bool ok = true;
+  if (polls) ok = mbar_wait_warp(m0, p0, limit) && (!m1 || mbar_wait_warp(m1, p1, limit));
+  return !bar_or(id, n, !ok);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
 }
