@@ -48,7 +48,7 @@ class K:
     (CONV_PREFILL, CONV_STEP, CONV_HISTORY, SCHEDULE, PREFILL_RECURRENT, PREFILL_CHUNKED, DECODE, STATE_CHECKSUM,
      SPLIT_CONV, SPLIT_PREP, SPLIT_CHAIN, SLOT_COPY, GEMM, SEQPAR, DIAG, WY_CONV, WY_PREP, WY_CHAIN, ROPE, KV_APPEND,
      KV_READ, ATTENTION, ATTN_COMBINE, Q4_PACK, LINEAR_Q4, X_HALF) = range(26)
-    COUNT = 25
+    COUNT = 26
 
 
 # Every symbol include/gdn.h declares.
@@ -354,7 +354,25 @@ def _need(ok: bool, message: str):
         raise GdnError(-1, message)
 
 
+class _Torch:
+    """torch's types and the calls behind torch.cuda.current_device and current_stream, bound at the first use (the
+    package imports without torch)."""
+    bf16 = f32 = i32 = u8 = device = raw_stream = None
+
+
+def _torch():
+    import torch
+    _Torch.bf16, _Torch.f32, _Torch.i32, _Torch.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    _Torch.device = torch.cuda.current_device
+    _Torch.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _io(dtype) -> int:
+    if dtype is _Torch.bf16 and dtype is not None:
+        return BF16
+    if dtype is _Torch.f32 and dtype is not None:
+        return F32
     name = str(dtype)
     if name in ("torch.bfloat16", "bf16"):
         return BF16
@@ -364,18 +382,18 @@ def _io(dtype) -> int:
 
 
 def _device(t, stream):
-    """(current device, raw stream); t is on that device."""
-    import torch
-    _need(t.is_cuda, "tensors must be CUDA tensors")
-    dev = torch.cuda.current_device()
-    if stream is not None:
-        return dev, _stream(stream)
-    return dev, torch.cuda.current_stream().cuda_stream
+    """(current device, raw stream); t is on a CUDA device (_ptr and _heads check that it is the current one)."""
+    if _Torch.device is None:
+        _torch()
+    if t.get_device() < 0:
+        raise GdnError(-1, "tensors must be CUDA tensors")
+    dev = _Torch.device()
+    return dev, _Torch.raw_stream(dev) if stream is None else _stream(stream)
 
 
-def _ptr(t, dev: int, name: str, dtype: str, numel: Optional[int] = None) -> int:
+def _ptr(t, dev: int, name: str, dtype, numel: Optional[int] = None) -> int:
     """Pointer of a contiguous tensor of a type (and, if given, at least numel elements) on device dev."""
-    if t.get_device() != dev or str(t.dtype) != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise GdnError(-1, f"{name} must be a contiguous {dtype} tensor on device {dev}")
     if numel is not None and t.numel() < numel:
         raise GdnError(-1, f"{name} has {t.numel()} elements, {numel} are needed")
@@ -384,8 +402,7 @@ def _ptr(t, dev: int, name: str, dtype: str, numel: Optional[int] = None) -> int
 
 def _heads(t, dev: int, name: str, io: int, T: int, H: int, D: int):
     """(pointer, elements between tokens) of rows [T, H, D] whose heads are contiguous within a token."""
-    if (t.get_device() != dev or tuple(t.shape) != (T, H, D)
-            or str(t.dtype) != ("torch.bfloat16" if io == BF16 else "torch.float32")):
+    if (t.shape != (T, H, D) or t.dtype is not (_Torch.bf16 if io == BF16 else _Torch.f32) or t.get_device() != dev):
         raise GdnError(-1, f"{name} must be [{T}, {H}, {D}] in the io type on device {dev}, got {list(t.shape)} {t.dtype}")
     st = t.stride()
     if T > 0 and (st[2] != 1 or (H > 1 and st[1] != D)):
@@ -393,20 +410,32 @@ def _heads(t, dev: int, name: str, io: int, T: int, H: int, D: int):
     return t.data_ptr(), st[0] if T > 1 else max(st[0], H * D)
 
 
-def _cu_host(cu_host) -> np.ndarray:
-    if type(cu_host) is np.ndarray and cu_host.dtype == np.int32 and cu_host.flags.c_contiguous:
-        return cu_host
-    return _host_cu(cu_host)
+def _cu_host(cu_host):
+    """(array of int32, its pointer, sequences, tokens)"""
+    if not (type(cu_host) is np.ndarray and cu_host.dtype == np.int32 and cu_host.flags.c_contiguous):
+        cu_host = _host_cu(cu_host)
+    n = cu_host.size - 1
+    if n < 1:
+        raise GdnError(-1, "cu_seqlens needs two entries or more")
+    return cu_host, cu_host.ctypes.data, n, int(cu_host[n])
 
 
-def _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table) -> KvCache:
-    n = cu_h.size - 1
-    _need(n >= 1, "cu_seqlens needs two entries or more")
-    _ptr(cu_dev, dev, "cu_seqlens", "torch.int32", n + 1)
-    _need(page_table.dim() == 2 and page_table.shape[0] >= n, "page_table must be [num_seqs, pages_per_seq]")
-    _need(pool.dim() == 2 and pool.shape[1] == kv_page_bytes(cfg), "pool must be [num_pages, kv_page_bytes]")
-    return KvCache(_ptr(pool, dev, "pool", "torch.uint8"), _ptr(page_table, dev, "page_table", "torch.int32"),
-                   _ptr(kv_lens, dev, "kv_lens", "torch.int32", n), pool.shape[0], page_table.shape[1])
+_PAGE_BYTES = {}  # kv_page_bytes by the sizes it depends on
+
+
+def _cache(cfg, dev, cu_dev, n, kv_lens, pool, page_table) -> KvCache:
+    _ptr(cu_dev, dev, "cu_seqlens", _Torch.i32, n + 1)
+    key = (cfg.num_kv_heads, cfg.head_dim, cfg.page_size)
+    size = _PAGE_BYTES.get(key)
+    if size is None:
+        size = _PAGE_BYTES[key] = kv_page_bytes(cfg)
+    rows, pages = page_table.shape, pool.shape
+    if len(rows) != 2 or rows[0] < n:
+        raise GdnError(-1, "page_table must be [num_seqs, pages_per_seq]")
+    if len(pages) != 2 or pages[1] != size:
+        raise GdnError(-1, "pool must be [num_pages, kv_page_bytes]")
+    return KvCache(_ptr(pool, dev, "pool", _Torch.u8), _ptr(page_table, dev, "page_table", _Torch.i32),
+                   _ptr(kv_lens, dev, "kv_lens", _Torch.i32, n), pages[0], rows[1])
 
 
 def make_attn_config(num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int = 64, io_dtype="bf16",
@@ -433,15 +462,17 @@ def rope_plan(rotary_dim: int, theta: float = 10000.0, sections=None, layout: st
 
 
 def _positions(plan, positions, dev, T: int) -> int:
-    _need(tuple(positions.shape) == (plan.num_axes, T) or (plan.num_axes == 1 and tuple(positions.shape) == (T,)),
-          f"positions must be [{plan.num_axes}, {T}], got {list(positions.shape)}")
-    return _ptr(positions, dev, "positions", "torch.int32")
+    shape = positions.shape
+    if shape != (plan.num_axes, T) and not (plan.num_axes == 1 and shape == (T,)):
+        raise GdnError(-1, f"positions must be [{plan.num_axes}, {T}], got {list(shape)}")
+    return _ptr(positions, dev, "positions", _Torch.i32)
 
 
 def rope(plan, x, positions, out, inverse: bool = False, stream=None):
     """gdn_rope: out = x [T, heads, head_dim] rotated (out may be x); positions [axes, T] int32."""
     dev, st = _device(x, stream)
-    _need(x.dim() == 3, "x must be [tokens, heads, head_dim]")
+    if x.dim() != 3:
+        raise GdnError(-1, "x must be [tokens, heads, head_dim]")
     io, (T, H, D) = _io(x.dtype), x.shape
     px, ldx = _heads(x, dev, "x", io, T, H, D)
     po, ldo = _heads(out, dev, "out", io, T, H, D)
@@ -459,26 +490,26 @@ def kv_append(cfg, plan, q, k, v, positions, cu_dev, cu_host, kv_lens, pool, pag
     """gdn_kv_append: q [T, Hq, D] rotated into q_out, k and v [T, Hkv, D] into the 4-bit cache (k rotated).  plan None:
     no rotation; positions None: the cache positions; q and q_out may be None."""
     dev, st = _device(k, stream)
-    cu_h = _cu_host(cu_host)
-    T, io = int(cu_h[-1]), cfg.io_dtype
-    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
-    pk, ldk = _heads(k, dev, "k", io, T, cfg.num_kv_heads, cfg.head_dim)
-    pv, ldv = _heads(v, dev, "v", io, T, cfg.num_kv_heads, cfg.head_dim)
-    pq, ldq = (None, 0) if q is None else _heads(q, dev, "q", io, T, cfg.num_q_heads, cfg.head_dim)
-    po, ldo = (None, 0) if q_out is None else _heads(q_out, dev, "q_out", io, T, cfg.num_q_heads, cfg.head_dim)
+    cu_h, pcu, n, T = _cu_host(cu_host)
+    io, D, hq, hkv = cfg.io_dtype, cfg.head_dim, cfg.num_q_heads, cfg.num_kv_heads
+    c = _cache(cfg, dev, cu_dev, n, kv_lens, pool, page_table)
+    pk, ldk = _heads(k, dev, "k", io, T, hkv, D)
+    pv, ldv = _heads(v, dev, "v", io, T, hkv, D)
+    pq, ldq = (None, 0) if q is None else _heads(q, dev, "q", io, T, hq, D)
+    po, ldo = (None, 0) if q_out is None else _heads(q_out, dev, "q_out", io, T, hq, D)
     _check(lib().gdn_kv_append(ctypes.byref(cfg), None if plan is None else ctypes.byref(plan), pq, ldq, pk, ldk, pv,
                                ldv, None if positions is None or plan is None else _positions(plan, positions, dev, T),
-                               cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1, ctypes.byref(c), po, ldo, st))
+                               cu_dev.data_ptr(), pcu, n, ctypes.byref(c), po, ldo, st))
 
 
 def kv_read(cfg, cu_dev, cu_host, kv_lens, pool, page_table, k_out, v_out, stream=None):
     """gdn_kv_read: the cache's values for the last tokens of each sequence, k_out and v_out [T, Hkv, D]."""
     dev, st = _device(pool, stream)
-    cu_h = _cu_host(cu_host)
-    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
-    dt = "torch.bfloat16" if cfg.io_dtype == BF16 else "torch.float32"
-    need = int(cu_h[-1]) * cfg.num_kv_heads * cfg.head_dim
-    _check(lib().gdn_kv_read(ctypes.byref(cfg), cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1, ctypes.byref(c),
+    cu_h, pcu, n, T = _cu_host(cu_host)
+    c = _cache(cfg, dev, cu_dev, n, kv_lens, pool, page_table)
+    dt = _Torch.bf16 if cfg.io_dtype == BF16 else _Torch.f32
+    need = T * cfg.num_kv_heads * cfg.head_dim
+    _check(lib().gdn_kv_read(ctypes.byref(cfg), cu_dev.data_ptr(), pcu, n, ctypes.byref(c),
                              _ptr(k_out, dev, "k_out", dt, need), _ptr(v_out, dev, "v_out", dt, need), st))
 
 
@@ -491,15 +522,15 @@ def attention_workspace_size(cfg, total_tokens: int, num_seqs: int) -> int:
 def attention(cfg, q, cu_dev, cu_host, kv_lens, pool, page_table, o, lse=None, workspace=None, stream=None):
     """gdn_attention: causal attention of q [T, Hq, D] over the 4-bit cache into o [T, Hq, D] (and lse [T, Hq] fp32)."""
     dev, st = _device(q, stream)
-    cu_h = _cu_host(cu_host)
-    T, io = int(cu_h[-1]), cfg.io_dtype
-    c = _cache(cfg, dev, cu_dev, cu_h, kv_lens, pool, page_table)
-    pq, ldq = _heads(q, dev, "q", io, T, cfg.num_q_heads, cfg.head_dim)
-    po = _ptr(o, dev, "o", "torch.bfloat16" if io == BF16 else "torch.float32", T * cfg.num_q_heads * cfg.head_dim)
-    pl = None if lse is None else _ptr(lse, dev, "lse", "torch.float32", T * cfg.num_q_heads)
-    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", "torch.uint8"), workspace.numel())
-    _check(lib().gdn_attention(ctypes.byref(cfg), pq, ldq, cu_dev.data_ptr(), cu_h.ctypes.data, cu_h.size - 1,
-                               ctypes.byref(c), po, pl, pw, nw, st))
+    cu_h, pcu, n, T = _cu_host(cu_host)
+    io, hq, D = cfg.io_dtype, cfg.num_q_heads, cfg.head_dim
+    c = _cache(cfg, dev, cu_dev, n, kv_lens, pool, page_table)
+    pq, ldq = _heads(q, dev, "q", io, T, hq, D)
+    po = _ptr(o, dev, "o", _Torch.bf16 if io == BF16 else _Torch.f32, T * hq * D)
+    pl = None if lse is None else _ptr(lse, dev, "lse", _Torch.f32, T * hq)
+    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", _Torch.u8), workspace.numel())
+    _check(lib().gdn_attention(ctypes.byref(cfg), pq, ldq, cu_dev.data_ptr(), pcu, n, ctypes.byref(c), po, pl, pw, nw,
+                               st))
 
 
 class Q4Weight:
@@ -521,8 +552,8 @@ def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     _need(tuple(codes.shape) == (N, G * group // 2), f"codes must be [{N}, {G * group // 2}], got {list(codes.shape)}")
     _need(tuple(scales.shape) == (N, G) and tuple(biases.shape) == (N, G), f"scales and biases must be [{N}, {G}]")
     data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
-    _check(lib().gdn_q4_pack(_ptr(codes, dev, "codes", "torch.uint8"), _ptr(scales, dev, "scales", "torch.bfloat16"),
-                             _ptr(biases, dev, "biases", "torch.bfloat16"), N, K, group, data.data_ptr(), st))
+    _check(lib().gdn_q4_pack(_ptr(codes, dev, "codes", _Torch.u8), _ptr(scales, dev, "scales", _Torch.bf16),
+                             _ptr(biases, dev, "biases", _Torch.bf16), N, K, group, data.data_ptr(), st))
     return Q4Weight(data, N, K, group)
 
 
@@ -535,12 +566,14 @@ def linear_q4_workspace_size(M: int, N: int, K: int, group: int, io_dtype="bf16"
 def linear_q4(x, w: Q4Weight, y, workspace=None, stream=None):
     """gdn_linear_q4: y [M, N] = x [M, K] @ w^T for a packed 4-bit weight."""
     dev, st = _device(x, stream)
-    _need(x.dim() == 2 and x.shape[1] == w.K, f"x must be [rows, {w.K}], got {list(x.shape)}")
-    io, M = _io(x.dtype), x.shape[0]
-    dt = str(x.dtype)
-    _need(tuple(y.shape) == (M, w.N), f"y must be [{M}, {w.N}], got {list(y.shape)}")
-    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", "torch.uint8"), workspace.numel())
-    _check(lib().gdn_linear_q4(io, _ptr(x, dev, "x", dt), M, w.K, _ptr(w.data, dev, "w", "torch.uint8"), w.N, w.group,
+    shape, dt, N, K = x.shape, x.dtype, w.N, w.K
+    if len(shape) != 2 or shape[1] != K:
+        raise GdnError(-1, f"x must be [rows, {K}], got {list(shape)}")
+    io, M = _io(dt), shape[0]
+    if y.shape != (M, N):
+        raise GdnError(-1, f"y must be [{M}, {N}], got {list(y.shape)}")
+    pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", _Torch.u8), workspace.numel())
+    _check(lib().gdn_linear_q4(io, _ptr(x, dev, "x", dt), M, K, _ptr(w.data, dev, "w", _Torch.u8), N, w.group,
                                _ptr(y, dev, "y", dt), pw, nw, st))
 
 
