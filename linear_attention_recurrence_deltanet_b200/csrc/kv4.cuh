@@ -1,5 +1,5 @@
-// The 4-bit key/value cache: page layout, quantisation of a group and the
-// rotation of eight channels, shared by the kernels that write and read it.
+// The 4-bit key/value cache: page layout, quantisation of a group and the angles
+// of the rotation, shared by the kernels that write and read it.
 //
 // A page holds page_size tokens (a multiple of 16) of every key/value head as
 //   [Hkv][page_size / 16] tiles of 16 tokens, tile_bytes each:
@@ -134,41 +134,6 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   } else {
     st16(p, Vec16<T>::pack(x));
     st16(p + 4, Vec16<T>::pack(x + 4));
-  }
-}
-
-// Channels c .. c+7 of a head after the rotation of the pairs (j, j + half),
-// j < half, by the angles with cosine and sine cs[j]:
-//   x'_j = x_j cos - x_{j+half} sin,  x'_{j+half} = x_{j+half} cos + x_j sin.
-// Products and sums are rounded one by one (see quantise8).  With half a
-// multiple of 8 the eight partners are one aligned vector; else they are read
-// one by one.
-template <typename T>
-__device__ __forceinline__ void rotate8(const T* head, int c, int half, const float2* cs, float (&x)[8]) {
-  load8(head + c, x);
-  if (c >= 2 * half) return;
-  if ((half & 7) == 0) {
-    const bool first = c < half;
-    const int j = first ? c : c - half;
-    float y[8];
-    load8(head + (first ? c + half : j), y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[j + i];
-      const float a = __fmul_rn(x[i], t.x), b = __fmul_rn(y[i], t.y);
-      x[i] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = c + i;
-      if (e >= 2 * half) break;
-      const bool first = e < half;
-      const int j = first ? e : e - half;
-      const float2 t = cs[j];
-      const float a = __fmul_rn(x[i], t.x), b = __fmul_rn(to_f(head[first ? e + half : j]), t.y);
-      x[i] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
-    }
   }
 }
 

@@ -5,8 +5,9 @@
 // All three stream their rows once: a lane owns eight channels of a head (16
 // bytes of bf16), D / 8 lanes a head, whole heads per warp.  The partner half
 // of a rotated pair is read by the lane that needs it (an L1 hit) rather than
-// exchanged.  A token's angles are shared by its heads: each block computes
-// those of its tokens once, in shared memory.
+// exchanged.  A token's angles are shared by its heads: a block computes those of
+// its tokens once, in shared memory, and a lane keeps the eight it needs in
+// registers while its warp passes over the token's heads.
 #include "../../include/gdn.h"
 #include "internal.h"
 #include "kv4.cuh"
@@ -15,7 +16,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxTok = 4;     // tokens of a block
+constexpr int kMaxTok = 8;     // tokens of a block
 constexpr int kMaxHalf = GDN_ROPE_MAX_PAIRS;
 
 struct RopeArgs {
@@ -26,27 +27,74 @@ struct RopeArgs {
   int32_t T, H, D, inverse;
 };
 
+// float2 j of a token's angles, one padded every eight: the lanes of a head read 16 different bank pairs
+__device__ __forceinline__ int at8(int j) { return j + (j >> 3); }
+constexpr int kLdCs = kMaxHalf + kMaxHalf / 8;
+
+// The angles of one lane's channels c .. c + 7, sines with the sign of its half, and the pairs' other channels.
+struct LaneAngles {
+  float c[8], s[8];
+  int partner;  // channel of the first partner; -1: not rotated, -2: half is not a multiple of 8, one by one
+  __device__ __forceinline__ void load(const float2* cs, int ch, int half) {
+    partner = ch >= 2 * half ? -1 : (half & 7) ? -2 : ch < half ? ch + half : ch - half;
+    if (partner < 0) return;
+    const int j = ch < half ? ch : ch - half;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 t = cs[at8(j + i)];
+      c[i] = t.x, s[i] = ch < half ? -t.y : t.y;
+    }
+  }
+};
+// Products and sums are rounded one by one (see quantise8).
+template <typename T>
+__device__ __forceinline__ void rotate(const T* head, int ch, int half, const LaneAngles& a, const float2* cs, float (&x)[8]) {
+  load8(head + ch, x);
+  if (a.partner >= 0) {
+    float y[8];
+    load8(head + a.partner, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(y[i], a.s[i]));
+  } else if (a.partner == -2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = ch + i;
+      if (e >= 2 * half) break;
+      const bool first = e < half;
+      const int j = first ? e : e - half;
+      const float2 t = cs[at8(j)];
+      const float p = __fmul_rn(x[i], t.x), q = __fmul_rn(to_f(head[first ? e + half : j]), t.y);
+      x[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ gdn_rope_plan plan, RopeArgs a, int tok) {
-  __shared__ float2 cs[kMaxTok * kMaxHalf];
+  __shared__ float2 cs[kMaxTok][kLdCs];
   const int half = plan.rotary_dim / 2, t0 = blockIdx.x * tok, nt = min(tok, a.T - t0);
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, j = i - t * half;
     const int p = a.pos[(int64_t)plan.axis[j] * a.T + t0 + t];
     const float2 r = rope_angle(plan, j, p);
-    cs[i] = make_float2(r.x, a.inverse ? -r.y : r.y);
+    cs[t][at8(j)] = make_float2(r.x, a.inverse ? -r.y : r.y);
   }
   __syncthreads();
   const int lph = a.D / 8, hpw = 32 / lph;  // lanes a head, heads a warp
   const int lane = threadIdx.x & 31, sub = lane / lph, c = (lane - sub * lph) * 8;
-  const int upt = (a.H + hpw - 1) / hpw;  // warp steps a token
-  for (int u = threadIdx.x >> 5; u < nt * upt; u += kWarps) {
-    const int t = u / upt, h = (u - t * upt) * hpw + sub;
+  const int wpt = kWarps / tok, t = (threadIdx.x >> 5) / wpt;  // warps a token; this warp's token
+  if (t >= nt) return;
+  LaneAngles ang;
+  ang.load(cs[t], sub < hpw ? c : a.D, half);
+  const T* x_row = (const T*)a.x + (int64_t)(t0 + t) * a.ldx;
+  T* o_row = (T*)a.out + (int64_t)(t0 + t) * a.ldo;
+#pragma unroll 2
+  for (int h = ((threadIdx.x >> 5) % wpt) * hpw + sub; h - sub < a.H; h += wpt * hpw) {
     const bool on = sub < hpw && h < a.H;
     float x[8];
-    if (on) rotate8((const T*)a.x + (int64_t)(t0 + t) * a.ldx + (int64_t)h * a.D, c, half, cs + t * half, x);
+    if (on) rotate(x_row + h * a.D, c, half, ang, cs[t], x);
     __syncwarp();  // out may be x: every lane has read its head before one writes
-    if (on) store8((T*)a.out + (int64_t)(t0 + t) * a.ldo + (int64_t)h * a.D + c, x);
+    if (on) store8(o_row + h * a.D + c, x);
   }
 }
 
@@ -61,33 +109,47 @@ struct AppendArgs {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(const __grid_constant__ gdn_rope_plan plan, AppendArgs a, KvCache cache, int tok, int32_t* status) {
-  __shared__ float2 cs[kMaxTok * kMaxHalf];
+  __shared__ float2 cs[kMaxTok][kLdCs];
   __shared__ int s_seq[kMaxTok], s_at[kMaxTok];
   const int half = plan.rotary_dim / 2, t0 = blockIdx.x * tok, nt = min(tok, a.T - t0);
-  if (threadIdx.x < nt) {
-    const int t = t0 + threadIdx.x, n = seq_of(a.cu, a.N, t);
-    s_seq[threadIdx.x] = n;
-    s_at[threadIdx.x] = cache.lens[n] - (a.cu[n + 1] - t);  // position in the cache; negative: not stored
+  // the tokens' sequences: every thread looks at some (one round of loads), beyond 1024 by bisection (ten or more, but
+  // a few threads)
+  if (a.N <= 4 * kThreads) {
+    for (int n = threadIdx.x; n < a.N; n += kThreads) {
+      const int lo = max(a.cu[n], t0), hi = min(a.cu[n + 1], t0 + nt);
+      for (int t = lo; t < hi; ++t) s_seq[t - t0] = n;
+    }
+    __syncthreads();
+  } else if (threadIdx.x < nt) {
+    s_seq[threadIdx.x] = seq_of(a.cu, a.N, t0 + threadIdx.x);
   }
-  __syncthreads();
+  if (threadIdx.x < nt) {
+    const int n = s_seq[threadIdx.x];
+    s_at[threadIdx.x] = cache.lens[n] - (a.cu[n + 1] - (t0 + threadIdx.x));  // position in the cache; negative: not stored
+  }
+  if (!a.pos) __syncthreads();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, j = i - t * half;
-    cs[i] = rope_angle(plan, j, a.pos ? a.pos[(int64_t)plan.axis[j] * a.T + t0 + t] : s_at[t]);
+    cs[t][at8(j)] = rope_angle(plan, j, a.pos ? a.pos[(int64_t)plan.axis[j] * a.T + t0 + t] : s_at[t]);
   }
   __syncthreads();
   constexpr int lph = D / 8, hpw = 32 / lph;
   const int lane = threadIdx.x & 31, sub = lane / lph, c = (lane % lph) * 8;
   const int uq = (a.Hq + hpw - 1) / hpw, uk = (cache.Hkv + hpw - 1) / hpw, upt = uq + 2 * uk;
-  for (int u = threadIdx.x >> 5; u < nt * upt; u += kWarps) {
-    const int t = u / upt, w = u - t * upt;
-    const int64_t row = t0 + t;
+  const int wpt = kWarps / tok, t = (threadIdx.x >> 5) / wpt;  // warps a token; this warp's token
+  if (t >= nt) return;
+  LaneAngles ang;
+  ang.load(cs[t], c, half);
+  const int64_t row = t0 + t;
+#pragma unroll 2
+  for (int w = (threadIdx.x >> 5) % wpt; w < upt; w += wpt) {
     float x[8];
     if (w < uq) {
       const int h = w * hpw + sub;
       const bool on = h < a.Hq;
-      if (on) rotate8((const T*)a.q + row * a.ldq + (int64_t)h * D, c, half, cs + t * half, x);
+      if (on) rotate((const T*)a.q + row * a.ldq + h * D, c, half, ang, cs[t], x);
       __syncwarp();  // q_out may be q
-      if (on) store8((T*)a.q_out + row * a.ldqo + (int64_t)h * D + c, x);
+      if (on) store8((T*)a.q_out + row * a.ldqo + h * D + c, x);
       continue;
     }
     const bool key = w < uq + uk;
@@ -96,9 +158,9 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.0f;
     if (on && key)
-      rotate8((const T*)a.k + row * a.ldk + (int64_t)h * D, c, half, cs + t * half, x);
+      rotate((const T*)a.k + row * a.ldk + h * D, c, half, ang, cs[t], x);
     else if (on)
-      load8((const T*)a.v + row * a.ldv + (int64_t)h * D + c, x);
+      load8((const T*)a.v + row * a.ldv + h * D + c, x);
     uint32_t sw;
     const uint32_t word = quantise8(x, (key ? kKGroup : v_group(D)) / 8, sw);
     const int p = s_at[t];
@@ -156,8 +218,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// tokens a block: several share the block's angle pass when there are enough tokens to fill the SMs
-int tokens_per_block(int32_t T) { return T >= 4 * 148 * kMaxTok ? kMaxTok : 1; }
+// Tokens a block: a warp each, which then reads its angles once for all heads, when there are enough to fill the SMs
+// (16384 tokens of 26 heads: 95 us with four tokens' heads dealt out to all warps); else the warps share a token's heads.
+int tokens_per_block(int32_t T) { return T >= 4 * 148 * kMaxTok ? kMaxTok : T >= 148 * 16 ? 4 : T >= 148 * 8 ? 2 : 1; }
 
 template <typename T>
 void append_d(int D, int grid, const gdn_rope_plan& plan, const AppendArgs& a, const KvCache& c, int tok, int32_t* status,
