@@ -137,12 +137,12 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
-// Cosine and sine of pair j at a position.  turn[j] is the frequency in turns
-// per position as a 64-bit fraction, so pos * turn[j] mod 2^64 is the angle's
+// Cosine and sine of a pair at a position.  turn is the frequency in turns per
+// position as a 64-bit fraction, so pos * turn mod 2^64 is the angle's
 // fraction of a turn without a range reduction: its error is |pos| * 2^-65
 // turns, at any position.  Evaluated in fp64 and rounded once.
-__device__ __forceinline__ float2 rope_angle(const gdn_rope_plan& plan, int j, int pos) {
-  const uint64_t ph = (uint64_t)(int64_t)pos * plan.turn[j];
+__device__ __forceinline__ float2 rope_angle(uint64_t turn, int64_t pos) {
+  const uint64_t ph = (uint64_t)pos * turn;
   double s, c;
   sincospi((double)(int64_t)ph * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
   return make_float2((float)c, (float)s);

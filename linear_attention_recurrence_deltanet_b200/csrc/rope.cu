@@ -46,56 +46,108 @@ struct LaneAngles {
     }
   }
 };
-// Products and sums are rounded one by one (see quantise8).
+// Eight channels of a head and their partners, as loaded: the loads of several heads go out together, before the
+// stores of the first, which may be to the same rows.
 template <typename T>
-__device__ __forceinline__ void rotate(const T* head, int ch, int half, const LaneAngles& a, const float2* cs, float (&x)[8]) {
-  load8(head + ch, x);
-  if (a.partner >= 0) {
-    float y[8];
-    load8(head + a.partner, y);
+struct Loaded {
+  static constexpr int V = sizeof(T) / 2;  // 16-byte pieces of eight channels
+  uint4 x[V], y[V];
+  const T* head;
+  __device__ __forceinline__ void load(const T* h, int ch, const LaneAngles& a) {
+    head = h;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(y[i], a.s[i]));
-  } else if (a.partner == -2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = ch + i;
-      if (e >= 2 * half) break;
-      const bool first = e < half;
-      const int j = first ? e : e - half;
-      const float2 t = cs[at8(j)];
-      const float p = __fmul_rn(x[i], t.x), q = __fmul_rn(to_f(head[first ? e + half : j]), t.y);
-      x[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
+    for (int i = 0; i < V; ++i) {
+      x[i] = ld16_rw(h + ch + 8 / V * i);
+      if (a.partner >= 0) y[i] = ld16_rw(h + a.partner + 8 / V * i);
     }
   }
+  // the rotated channels.  Products and sums are rounded one by one (see quantise8).
+  __device__ __forceinline__ void rotate(int ch, int half, const LaneAngles& a, const float2* cs, float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) Vec16<T>::unpack(x[i], o + 8 / V * i);
+    if (a.partner >= 0) {
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < V; ++i) Vec16<T>::unpack(y[i], p + 8 / V * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __fadd_rn(__fmul_rn(o[i], a.c[i]), __fmul_rn(p[i], a.s[i]));
+    } else if (a.partner == -2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = ch + i;
+        if (e >= 2 * half) break;
+        const bool first = e < half;
+        const int j = first ? e : e - half;
+        const float2 t = cs[at8(j)];
+        const float p = __fmul_rn(o[i], t.x), q = __fmul_rn(to_f(head[first ? e + half : j]), t.y);
+        o[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
+      }
+    }
+  }
+};
+
+// Heads h0, h0 + step, .. of one token's row, rotated from x to out (which may be x): U of them in flight.
+template <int U, typename T>
+__device__ __forceinline__ void rotate_heads_by(const T* x, T* out, int h0, int step, int H, int D, bool lane_on, int c, int half,
+                                                const LaneAngles& a, const float2* cs) {
+  for (; __any_sync(0xffffffffu, h0 < H); h0 += U * step) {
+    Loaded<T> in[U];
+    float o[8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane_on && h0 + u * step < H) in[u].load(x + (h0 + u * step) * D, c, a);
+    if (U == 1 && lane_on && h0 < H) in[0].rotate(c, half, a, cs, o);  // partners read one by one: before the store
+    __syncwarp();  // every lane has read its heads before one writes
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane_on && h0 + u * step < H) {
+        if (U > 1) in[u].rotate(c, half, a, cs, o);
+        store8(out + (h0 + u * step) * D + c, o);
+      }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void rotate_heads(const T* x, T* out, int h0, int step, int H, int D, bool lane_on, int c, int half,
+                                             const LaneAngles& a, const float2* cs) {
+  if (half & 7) rotate_heads_by<1>(x, out, h0, step, H, D, lane_on, c, half, a, cs);
+  else rotate_heads_by<8 / sizeof(T)>(x, out, h0, step, H, D, lane_on, c, half, a, cs);
+}
+
+// The angles of a block's tokens.  A plan is read from parameter space, one lane after the other where their pairs
+// differ; several tokens read it from shared memory (16384 tokens: 58 -> 50 us).
+template <typename F>
+__device__ __forceinline__ void make_angles(const gdn_rope_plan& plan, float2 (*cs)[kLdCs], int half, int nt, const F& pos_of) {
+  __shared__ uint64_t s_turn[kMaxHalf];
+  __shared__ uint8_t s_axis[kMaxHalf];
+  if (nt > 1) {
+    for (int j = threadIdx.x; j < half; j += kThreads) s_turn[j] = plan.turn[j], s_axis[j] = plan.axis[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+      const int t = i / half, j = i - t * half;
+      cs[t][at8(j)] = rope_angle(s_turn[j], pos_of(t, s_axis[j]));
+    }
+  } else {
+    for (int j = threadIdx.x; j < half; j += kThreads) cs[0][at8(j)] = rope_angle(plan.turn[j], pos_of(0, plan.axis[j]));
+  }
+  __syncthreads();
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ gdn_rope_plan plan, RopeArgs a, int tok) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ gdn_rope_plan plan, RopeArgs a, int tok) {
   __shared__ float2 cs[kMaxTok][kLdCs];
   const int half = plan.rotary_dim / 2, t0 = blockIdx.x * tok, nt = min(tok, a.T - t0);
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = i / half, j = i - t * half;
-    const int p = a.pos[(int64_t)plan.axis[j] * a.T + t0 + t];
-    const float2 r = rope_angle(plan, j, p);
-    cs[t][at8(j)] = make_float2(r.x, a.inverse ? -r.y : r.y);
-  }
-  __syncthreads();
+  make_angles(plan, cs, half, nt, [&](int t, int axis) {
+    const int64_t p = a.pos[(int64_t)axis * a.T + t0 + t];
+    return a.inverse ? -p : p;  // the inverse turns back
+  });
   const int lph = a.D / 8, hpw = 32 / lph;  // lanes a head, heads a warp
   const int lane = threadIdx.x & 31, sub = lane / lph, c = (lane - sub * lph) * 8;
   const int wpt = kWarps / tok, t = (threadIdx.x >> 5) / wpt;  // warps a token; this warp's token
   if (t >= nt) return;
   LaneAngles ang;
   ang.load(cs[t], sub < hpw ? c : a.D, half);
-  const T* x_row = (const T*)a.x + (int64_t)(t0 + t) * a.ldx;
-  T* o_row = (T*)a.out + (int64_t)(t0 + t) * a.ldo;
-#pragma unroll 2
-  for (int h = ((threadIdx.x >> 5) % wpt) * hpw + sub; h - sub < a.H; h += wpt * hpw) {
-    const bool on = sub < hpw && h < a.H;
-    float x[8];
-    if (on) rotate(x_row + h * a.D, c, half, ang, cs[t], x);
-    __syncwarp();  // out may be x: every lane has read its head before one writes
-    if (on) store8(o_row + h * a.D + c, x);
-  }
+  rotate_heads((const T*)a.x + (int64_t)(t0 + t) * a.ldx, (T*)a.out + (int64_t)(t0 + t) * a.ldo,
+               ((threadIdx.x >> 5) % wpt) * hpw + sub, wpt * hpw, a.H, a.D, sub < hpw, c, half, ang, cs[t]);
 }
 
 struct AppendArgs {
@@ -107,7 +159,7 @@ struct AppendArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     append_kernel(const __grid_constant__ gdn_rope_plan plan, AppendArgs a, KvCache cache, int tok, int32_t* status) {
   __shared__ float2 cs[kMaxTok][kLdCs];
   __shared__ int s_seq[kMaxTok], s_at[kMaxTok];
@@ -128,39 +180,36 @@ __global__ void __launch_bounds__(kThreads)
     s_at[threadIdx.x] = cache.lens[n] - (a.cu[n + 1] - (t0 + threadIdx.x));  // position in the cache; negative: not stored
   }
   if (!a.pos) __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = i / half, j = i - t * half;
-    cs[t][at8(j)] = rope_angle(plan, j, a.pos ? a.pos[(int64_t)plan.axis[j] * a.T + t0 + t] : s_at[t]);
-  }
-  __syncthreads();
+  make_angles(plan, cs, half, nt, [&](int t, int axis) {
+    return (int64_t)(a.pos ? a.pos[(int64_t)axis * a.T + t0 + t] : s_at[t]);
+  });
   constexpr int lph = D / 8, hpw = 32 / lph;
   const int lane = threadIdx.x & 31, sub = lane / lph, c = (lane % lph) * 8;
-  const int uq = (a.Hq + hpw - 1) / hpw, uk = (cache.Hkv + hpw - 1) / hpw, upt = uq + 2 * uk;
+  const int uq = (a.Hq + hpw - 1) / hpw, uk = (cache.Hkv + hpw - 1) / hpw;
   const int wpt = kWarps / tok, t = (threadIdx.x >> 5) / wpt;  // warps a token; this warp's token
   if (t >= nt) return;
   LaneAngles ang;
   ang.load(cs[t], c, half);
   const int64_t row = t0 + t;
-#pragma unroll 2
-  for (int w = (threadIdx.x >> 5) % wpt; w < upt; w += wpt) {
-    float x[8];
-    if (w < uq) {
-      const int h = w * hpw + sub;
-      const bool on = h < a.Hq;
-      if (on) rotate((const T*)a.q + row * a.ldq + h * D, c, half, ang, cs[t], x);
-      __syncwarp();  // q_out may be q
-      if (on) store8((T*)a.q_out + row * a.ldqo + h * D + c, x);
-      continue;
-    }
-    const bool key = w < uq + uk;
-    const int h = (key ? w - uq : w - uq - uk) * hpw + sub;
+  const int w0 = (threadIdx.x >> 5) % wpt;
+  if (a.Hq)
+    rotate_heads((const T*)a.q + row * a.ldq, (T*)a.q_out + row * a.ldqo, w0 * hpw + sub, wpt * hpw, a.Hq, D, true, c, half,
+                 ang, cs[t]);
+  // keys, then values; the warps that had a query step less begin
+  for (int w = (w0 + wpt - uq % wpt) % wpt; w < 2 * uk; w += wpt) {
+    const bool key = w < uk;
+    const int h = (key ? w : w - uk) * hpw + sub;
     const bool on = h < cache.Hkv;
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-    if (on && key)
-      rotate((const T*)a.k + row * a.ldk + h * D, c, half, ang, cs[t], x);
-    else if (on)
+    if (on && key) {
+      Loaded<T> in;
+      in.load((const T*)a.k + row * a.ldk + h * D, c, ang);
+      in.rotate(c, half, ang, cs[t], x);
+    } else if (on) {
       load8((const T*)a.v + row * a.ldv + h * D + c, x);
+    }
     uint32_t sw;
     const uint32_t word = quantise8(x, (key ? kKGroup : v_group(D)) / 8, sw);
     const int p = s_at[t];
