@@ -24,9 +24,9 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroupUnits = 12;  // what a group costs beside its tiles, in tiles
 constexpr int kMinUnits = 24;    // the least quota
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 
-constexpr int stages(int D) { return D == 64 ? 8 : D == 128 ? 6 : 4; }
+constexpr int stages(int D) { return D == 256 ? 4 : 8; }
 constexpr int blocks_per_sm(int D) { return D == 256 ? 2 : 3; }
 // queries in shared memory where a warp's copy would take over half of its registers
 constexpr bool q_in_smem(int D, int TQ) { return D * TQ > 128; }
@@ -34,19 +34,36 @@ constexpr int smem_bytes(int D, int TQ) {
   return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
-// two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8
-__device__ __forceinline__ uint32_t code128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t code8(uint32_t w) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(code128(w)), "r"(0x43084308u));
-  return r;
-}
+// Two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8.  The mask and the exponent sit in registers whose
+// values the compiler does not know (a kernel argument that is 0 is in them), so that one instruction takes both.
+struct Codes {
+  uint32_t mask, magic;
+  __device__ __forceinline__ explicit Codes(uint32_t zero) : mask(0x000f000fu + zero), magic(0x43004300u + zero) {}
+  __device__ __forceinline__ uint32_t c128(uint32_t w) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));  // (w & mask) | magic
+    return r;
+  }
+  __device__ __forceinline__ uint32_t c8(uint32_t w) const {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c128(w)), "r"(0x43084308u));
+    return r;
+  }
+};
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {  // C = 0
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 template <typename T, int D, int RT>
@@ -76,7 +93,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
   AttnWalk<RT, kKvTile, kGroupUnits, kMinUnits> walk;
   if (!walk.start(a, kThreads, s_warp, s_found)) return;
   const float c_log2 = p.scale * kLog2e;
-  uint32_t phase = 0;  // bit s: parity of the ring's stage s
+  const Codes codes(a.zero);
+  uint32_t used = 0;  // tiles this warp has passed: stage used % S, phase used / S
   bool dead = false;
 
   while (true) {
@@ -95,6 +113,35 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
     // every row of the group sees the tiles before this one whole
     const int whole = row_last - rt * RT + 1 == RT ? min(rw.first + rt * RT / Gq, rw.cap) / kKvTile : 0;
     const int seen_tiles = (max(0, min(rw.first + row_last / Gq, rw.cap)) + kKvTile - 1) / kKvTile;
+
+    // This warp's tiles: t_begin + warp + 4 j.  Every 32 of them, lane j looks up the place of the j-th, and asks for it
+    // when its turn comes, S - 1 tiles ahead.  A tile without a page passes through the ring as an empty stage.
+    const int stop = min(t_end, seen_tiles);
+    const int count = !dead && t_begin + warp < stop ? (stop - t_begin - warp + kWarps - 1) / kWarps : 0;
+    int64_t place = -1;
+    auto look_up = [&](int j0) {
+      const int t = t_begin + warp + kWarps * (j0 + lane);
+      place = -1;
+      if (j0 + lane < count) {
+        place = kv_tile_at(a.cache, D, n, t * kKvTile, h);
+        if (place < 0) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
+      }
+    };
+    auto fetch = [&](int j) {  // by the lane that looked tile j up
+      if (lane == (j & 31) && j < count) {
+        const uint32_t s = (used + j) & (S - 1);  // (used: before the piece)
+        if (place >= 0) {
+          tc::mbar_expect_tx(&s_full[warp][s], TB);
+          tc::bulk_load(ring + s * TB, a.cache.pool + place, TB, &s_full[warp][s]);
+        } else {
+          tc::mbar_arrive(&s_full[warp][s]);
+        }
+      }
+    };
+    look_up(0);
+    uint32_t valid = __ballot_sync(0xffffffffu, place >= 0), valid_next = valid;  // of the 32 tiles around the use side
+#pragma unroll 1
+    for (int j = 0; j < S - 1; ++j) fetch(j);
 
     // queries as A fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64, paired (c, c + 4) as the codes are
     uint32_t qf[QS ? 1 : NM][4];
@@ -170,55 +217,25 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) rs[g][e] = 0.0f;
 
-    // this warp's tiles: t_begin + warp + 4 j.  Every 32 of them, lane j looks up the place of the j-th.
-    const int stop = min(t_end, seen_tiles);
-    const int count = !dead && t_begin + warp < stop ? (stop - t_begin - warp + kWarps - 1) / kWarps : 0;
-    int64_t place = -1;
-    auto look_up = [&](int j0) {
-      const int t = t_begin + warp + kWarps * (j0 + lane);
-      place = -1;
-      if (j0 + lane < count) {
-        place = kv_tile_at(a.cache, D, n, t * kKvTile, h);
-        if (place < 0) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
-      }
-    };
-    auto fetch = [&](int64_t from, int s) {  // lane 0
-      tc::mbar_expect_tx(&s_full[warp][s], TB);
-      tc::bulk_load(ring + s * TB, a.cache.pool + from, TB, &s_full[warp][s]);
-    };
-    // tile j uses stage j % S; a tile without a page is skipped on both sides
-    look_up(0);
-    int64_t next_place = place;  // places of tiles j0 .. j0 + 31 of the fetch side
-    for (int j = 0; j < S - 1; ++j) {
-      const int64_t f = __shfl_sync(0xffffffffu, next_place, j);
-      if (lane == 0 && j < count && f >= 0) fetch(f, j % S);
-    }
-    int s_use = 0, s_fetch = S - 1;
-    uint32_t valid = __ballot_sync(0xffffffffu, next_place >= 0);  // of the 32 tiles around the use side
-    uint32_t valid_next = valid;
-    for (int j = 0; j < count && !dead; ++j) {
+    int done = count;  // tiles passed (fewer after a wait that ran out)
+    for (int j = 0; j < count; ++j) {
       const int jf = j + S - 1;
-      if (jf % 32 == 0) {
+      if ((jf & 31) == 0) {
         look_up(jf);
-        next_place = place;
-        valid_next = __ballot_sync(0xffffffffu, next_place >= 0);
+        valid_next = __ballot_sync(0xffffffffu, place >= 0);
       }
-      if (j % 32 == 0 && j > 0) valid = valid_next;
-      {
-        const int64_t f = __shfl_sync(0xffffffffu, next_place, jf % 32);
-        if (lane == 0 && jf < count && f >= 0) fetch(f, s_fetch);
-        s_fetch = s_fetch + 1 == S ? 0 : s_fetch + 1;
+      if ((j & 31) == 0) valid = valid_next;
+      fetch(jf);
+      const uint32_t stage = (used + j) & (S - 1);
+      if (!tc::mbar_wait_warp(&s_full[warp][stage], ((used + j) / S) & 1, kWaitCycles)) {
+        set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));
+        dead = true;
+        done = j;
+        break;
       }
-      const bool here = (valid >> (j % 32)) & 1u;
-      if (here) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_full[warp][s_use], (phase >> s_use) & 1u, kWaitNs))) {
-          set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));
-          dead = true;
-          break;
-        }
-        phase ^= 1u << s_use;
-        const unsigned char* tile = ring + s_use * TB;
+      if ((valid >> (j & 31)) & 1u) {
         const int t = t_begin + warp + kWarps * j;
+        const unsigned char* tile = ring + stage * TB;
 
         // scores of the tile's 16 tokens: two 8-token products, tokens 2q and 2q + 1 of each in this thread
         float s[2][2 * NR];
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
           for (int e = 0; e < 2 * NR; ++e) s[i][e] = 0.0f;
 #pragma unroll
         for (int g = 0; g < GK; ++g) {
-          float acc[2][4] = {};
+          float acc[2][4];
           uint2 kw[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -240,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
-              b0[i] = F32 ? code8(w >> sh) : code128(w >> sh);
-              b1[i] = F32 ? code8(w >> (sh + 4)) : code128(w >> (sh + 4));
+              b0[i] = F32 ? codes.c8(w >> sh) : codes.c128(w >> sh);
+              b1[i] = F32 ? codes.c8(w >> (sh + 4)) : codes.c128(w >> (sh + 4));
             }
 #pragma unroll
             for (int term = 0; term < TQ; ++term) {
@@ -249,7 +266,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
               if constexpr (QS) f = s_q[((g * 4 + m) * TQ + term) * 32 + lane];
               else f = make_uint4(qf[g * 4 + m][0], qf[g * 4 + m][1], qf[g * 4 + m][2], qf[g * 4 + m][3]);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) mma(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
+              for (int i = 0; i < 2; ++i) {
+                if (m == 0 && term == 0) mma0(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
+                else mma(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
+              }
             }
           }
 #pragma unroll
@@ -274,9 +294,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 #pragma unroll
           for (int e = 0; e < 2 * NR; ++e) {
             s[i][e] *= c_log2;
-            if (masked && t * kKvTile + 8 * i + 2 * q + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
-            over |= s[i][e] > mx[e >> 1] + kSlack;
           }
+        if (masked) {
+          __syncwarp();  // (keeps the branch a branch)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * NR; ++e)
+              if (t * kKvTile + 8 * i + 2 * q + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
+          over |= fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1])) > mx[k] + kSlack;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int k = 0; k < NR; ++k) {
@@ -362,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
               const uint32_t w01 = __byte_perm(w[0], w[1], sel), w23 = __byte_perm(w[2], w[3], sel);
 #pragma unroll
               for (int jj = 0; jj < 4; ++jj) {
-                const uint32_t b0 = F32 ? code8(w01 >> (4 * jj)) : code128(w01 >> (4 * jj));
-                const uint32_t b1 = F32 ? code8(w23 >> (4 * jj)) : code128(w23 >> (4 * jj));
+                const uint32_t b0 = F32 ? codes.c8(w01 >> (4 * jj)) : codes.c128(w01 >> (4 * jj));
+                const uint32_t b1 = F32 ? codes.c8(w23 >> (4 * jj)) : codes.c128(w23 >> (4 * jj));
                 float(&c)[4] = o[cb][half * 4 + jj];
                 mma(c, ph[0], ph[1], ph[2], ph[3], b0, b1);
                 if constexpr (NR == 2) mma(c, pl[0], pl[1], pl[2], pl[3], b0, b1);
@@ -372,14 +401,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
             }
           }
         }
-        __syncwarp();  // the stage is read before lane 0 refills it
+        __syncwarp();  // the stage is read before it is refilled
       }
-      s_use = s_use + 1 == S ? 0 : s_use + 1;
     }
-    // a wait that ran out: the copies still in flight land before the ring is used for the join
-    if (dead) {
-      for (int s = 0; s < S; ++s) tc::mbar_wait(&s_full[warp][s], (phase >> s) & 1u, kWaitNs / 100);
-    }
+    if (dead)  // the copies still in flight land before the ring is used for the join
+      for (int j = done; j < min(count, done + S); ++j)
+        tc::mbar_wait_warp(&s_full[warp][(used + j) & (S - 1)], ((used + j) / S) & 1, kWaitCycles / 100);
+    used += count;
 
     // the join: every warp's rows (unnormalised, bias added) into its ring, then all threads over rows and channels
     float* mine = reinterpret_cast<float*>(ring);
@@ -558,7 +586,7 @@ constexpr int kPrefillFrom = 64;
 
 template <typename T, int D, int RT>
 cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
-  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D), 16), ws), grid_of(D), status};
+  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D), 16), ws), grid_of(D), status, 0};
   constexpr int bytes = smem_bytes(D, sizeof(T) == 4 ? 3 : 1);
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -600,7 +628,7 @@ size_t attention_ws_bytes(int32_t T, int32_t, int32_t Hq, int32_t Hkv, int32_t D
 cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
                              cudaStream_t stream) {
   if (p.bf16 && p.D <= 128 && (int64_t)p.max_q * (p.Hq / cache.Hkv) > kPrefillFrom)
-    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, kPrefillRows), ws), kAttnSms, status}, stream);
+    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, kPrefillRows), ws), kAttnSms, status, 0}, stream);
   if (p.D == 64) return run_d<64>(p, cache, ws, status, stream);
   if (p.D == 128) return run_d<128>(p, cache, ws, status, stream);
   return run_d<256>(p, cache, ws, status, stream);

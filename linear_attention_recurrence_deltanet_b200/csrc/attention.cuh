@@ -34,6 +34,7 @@ struct AttnArgs {
   AttnWorkspace ws;
   int32_t G;  // blocks
   int32_t* status;
+  uint32_t zero;  // 0, unknown to the compiler
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
