@@ -10,6 +10,11 @@
 // for fp32 io, whose queries go in three as well).  A 4-bit code becomes a bf16
 // by masking it into the low mantissa bits of 128.
 //
+// Keys and values are the A operand (16 keys x 16 channels, 16 channels x 16
+// keys), eight query rows the B operand: a lane then scales two keys for all rows,
+// and a tile of eight rows wastes nothing.  The probabilities turn from an output
+// into an operand by movmatrix.
+//
 // Row tiles of 16 rows, 8 where no sequence has more; tiles of 16 keys
 // (attention.cuh has the cutting).  The four warps of a block take every fourth
 // tile of its piece and join at the piece's end.
@@ -26,12 +31,12 @@ constexpr int kGroupUnits = 12;  // what a group costs beside its tiles, in tile
 constexpr int kMinUnits = 24;    // the least quota
 constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 
-constexpr int stages(int D) { return D == 256 ? 4 : 8; }
-constexpr int blocks_per_sm(int D) { return D == 256 ? 2 : 3; }
-// queries in shared memory where a warp's copy would take over half of its registers
-constexpr bool q_in_smem(int D, int TQ) { return D * TQ > 128; }
-constexpr int smem_bytes(int D, int TQ) {
-  return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, TQ) ? D / 16 * TQ * 512 : 0);
+constexpr int stages(int D) { return D == 64 ? 8 : 4; }
+constexpr int blocks_per_sm(int D, int RT) { return D == 256 ? (RT == 8 ? 3 : 2) : RT == 8 ? 4 : 3; }
+// queries in shared memory where a warp's copy would take too many registers
+constexpr bool q_in_smem(int D, int RT, int TQ) { return D * TQ * (RT / 8) > 128; }
+constexpr int smem_bytes(int D, int RT, int TQ) {
+  return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, RT, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
 // Two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8.  The mask and the exponent sit in registers whose
@@ -66,14 +71,21 @@ __device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {  // of bf16: lane (r, q) has row r, columns 2q, 2q + 1
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(const __grid_constant__ AttnArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int TQ = F32 ? 3 : 1;          // bf16 parts of a query
+  constexpr int TP = F32 ? 3 : 2;          // bf16 parts of p_t s_t
   constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, NM = D / 16;
   constexpr int S = stages(D), TB = kv_tile_bytes(D);
-  constexpr bool QS = q_in_smem(D, TQ);
-  constexpr int NR = RT / 8;               // rows a thread holds: r, and r + 8 with 16-row tiles
+  constexpr bool QS = q_in_smem(D, RT, TQ);
+  constexpr int NR = RT / 8;               // groups of eight rows: a lane has rows 2q, 2q + 1 of each
   static_assert(!F32 || RT == 16, "fp32 io runs 16-row tiles");
 
   extern __shared__ __align__(128) unsigned char smem[];
@@ -101,17 +113,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
     if (walk.piece(a)) {
     const int n = walk.n, h = walk.h, rt = walk.rt, t_begin = walk.t0, t_end = walk.t1;
     const AttnRows rw = walk.rw;
-    // rows of this thread: keys seen by each (0 for a row that is none)
-    int lim[NR];
+    // keys that this lane's rows see; a row that is none sees all and is not written
+    int lim[NR][2];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int row = rt * RT + r + 8 * i;
-      lim[i] = row < rw.rows ? max(0, min(rw.first + row / Gq, rw.cap)) : 0;
-      if (row < rw.rows && rw.first + row / Gq > rw.cap) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
-    }
+    for (int k = 0; k < NR; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = rt * RT + 8 * k + 2 * q + e;
+        lim[k][e] = row < rw.rows ? max(0, min(rw.first + row / Gq, rw.cap)) : 0x7fffffff;
+        if (row < rw.rows && rw.first + row / Gq > rw.cap) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
+      }
     const int row_last = min(rw.rows, (rt + 1) * RT) - 1;
-    // every row of the group sees the tiles before this one whole
-    const int whole = row_last - rt * RT + 1 == RT ? min(rw.first + rt * RT / Gq, rw.cap) / kKvTile : 0;
+    const int whole = min(rw.first + rt * RT / Gq, rw.cap) / kKvTile;  // every row of the group sees the tiles before this one
     const int seen_tiles = (max(0, min(rw.first + row_last / Gq, rw.cap)) + kKvTile - 1) / kKvTile;
 
     // This warp's tiles: t_begin + warp + 4 j.  Every 32 of them, lane j looks up the place of the j-th, and asks for it
@@ -143,9 +156,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 #pragma unroll 1
     for (int j = 0; j < S - 1; ++j) fetch(j);
 
-    // queries as A fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64, paired (c, c + 4) as the codes are
+    // queries as B fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64 of row r, paired (c, c + 4) as the
+    // codes are; [group], [2 + group]
     uint32_t qf[QS ? 1 : NM][4];
-    float qsum[NR][GK];
+    float qsum[NR][2][GK];
     if constexpr (QS) __syncthreads();  // the last piece's reads of s_q
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -172,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
           for (int e = 0; e < 16; ++e) s += x[e];
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
-          qsum[i < NR ? i : 0][g] = s;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) qsum[i < NR ? i : 0][e][g] = __shfl_sync(0xffffffffu, s, (2 * q + e) * 4);
         }
 #pragma unroll
         for (int term = 0; term < TQ; ++term) {
@@ -188,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
                 uint32_t* d = reinterpret_cast<uint32_t*>(s_q + ((g * 4 + m) * TQ + term) * 32 + lane);
                 d[i] = f0, d[2 + i] = f1;
               }
-            } else {
+            } else if (i < NR) {
               qf[g * 4 + m][i] = f0, qf[g * 4 + m][2 + i] = f1;
             }
           }
@@ -197,25 +212,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
     }
     if constexpr (QS) __syncthreads();
 
-    float o[CB][8][4];
-    float rs[F32 ? 1 : GV][4];  // sums of the rounded p_t s_t: the products carry the codes as 128 + c for bf16
-    float mx[NR], l[NR], ob[NR][GV];
+    float o[NR][CB][4][4];                   // [channels 8r + 2j, + 1 of each 64][two channels x two rows]
+    float rs[NR][F32 ? 1 : GV][4];           // sums of the rounded p_t s_t: bf16 io carries the codes as 128 + c
+    float mx[NR][2], l[NR][2], ob[NR][2][GV];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      mx[i] = -INFINITY, l[i] = 0.0f;
+    for (int k = 0; k < NR; ++k) {
 #pragma unroll
-      for (int g = 0; g < GV; ++g) ob[i][g] = 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        mx[k][e] = -INFINITY, l[k][e] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < GV; ++g) ob[k][e][g] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[k][cb][j][e] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < (F32 ? 1 : GV); ++g) rs[k][g][e] = 0.0f;
+      }
     }
-#pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[cb][j][e] = 0.0f;
-#pragma unroll
-    for (int g = 0; g < (F32 ? 1 : GV); ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) rs[g][e] = 0.0f;
 
     int done = count;  // tiles passed (fewer after a wait that ran out)
     for (int j = 0; j < count; ++j) {
@@ -233,176 +250,184 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
         done = j;
         break;
       }
-      if ((valid >> (j & 31)) & 1u) {
-        const int t = t_begin + warp + kWarps * j;
-        const unsigned char* tile = ring + stage * TB;
+      if (!((valid >> (j & 31)) & 1u)) continue;
+      const int t = t_begin + warp + kWarps * j;
+      const unsigned char* tile = ring + stage * TB;
+      const uint32_t* scales = reinterpret_cast<const uint32_t*>(tile + kv_scale_off(D)) + r;  // of keys r and r + 8
 
-        // scores of the tile's 16 tokens: two 8-token products, tokens 2q and 2q + 1 of each in this thread
-        float s[2][2 * NR];
+      // scores: [group][key r or r + 8][row 2q or 2q + 1]
+      float s[NR][2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int k = 0; k < NR; ++k)
 #pragma unroll
-          for (int e = 0; e < 2 * NR; ++e) s[i][e] = 0.0f;
+        for (int i = 0; i < 2; ++i) s[k][i][0] = s[k][i][1] = 0.0f;
 #pragma unroll
-        for (int g = 0; g < GK; ++g) {
-          float acc[2][4];
-          uint2 kw[2];
+      for (int g = 0; g < GK; ++g) {
+        float acc[NR][4];
+        uint2 kw[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            kw[i] = *reinterpret_cast<const uint2*>(tile + g * 512 + (8 * i + r) * 32 + q * 8);
+        for (int i = 0; i < 2; ++i) kw[i] = *reinterpret_cast<const uint2*>(tile + g * 512 + (8 * i + r) * 32 + q * 8);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int sh = 8 * (m & 1);
-            uint32_t b0[2], b1[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
-              b0[i] = F32 ? codes.c8(w >> sh) : codes.c128(w >> sh);
-              b1[i] = F32 ? codes.c8(w >> (sh + 4)) : codes.c128(w >> (sh + 4));
-            }
-#pragma unroll
-            for (int term = 0; term < TQ; ++term) {
-              uint4 f;
-              if constexpr (QS) f = s_q[((g * 4 + m) * TQ + term) * 32 + lane];
-              else f = make_uint4(qf[g * 4 + m][0], qf[g * 4 + m][1], qf[g * 4 + m][2], qf[g * 4 + m][3]);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (m == 0 && term == 0) mma0(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
-                else mma(acc[i], f.x, f.y, f.z, f.w, b0[i], b1[i]);
-              }
-            }
-          }
+        for (int m = 0; m < 4; ++m) {
+          const int sh = 8 * (m & 1);
+          uint32_t c0[2], c1[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint2 sw = *reinterpret_cast<const uint2*>(tile + kv_scale_off(D) + g * 64 + (8 * i + 2 * q) * 4);
-            const float s0 = lo_bf16(sw.x), s1 = lo_bf16(sw.y);
-            const float z0 = fmaf(F32 ? 8.0f : -128.0f, s0, hi_bf16(sw.x));
-            const float z1 = fmaf(F32 ? 8.0f : -128.0f, s1, hi_bf16(sw.y));
+            const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
+            c0[i] = F32 ? codes.c8(w >> sh) : codes.c128(w >> sh);
+            c1[i] = F32 ? codes.c8(w >> (sh + 4)) : codes.c128(w >> (sh + 4));
+          }
+#pragma unroll
+          for (int term = 0; term < TQ; ++term) {
+            uint32_t f[4];
+            if constexpr (QS) {
+              const uint4 v = s_q[((g * 4 + m) * TQ + term) * 32 + lane];
+              f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = qf[g * 4 + m][e];
+            }
 #pragma unroll
             for (int k = 0; k < NR; ++k) {
-              s[i][2 * k] = fmaf(s0, acc[i][2 * k], fmaf(z0, qsum[k][g], s[i][2 * k]));
-              s[i][2 * k + 1] = fmaf(s1, acc[i][2 * k + 1], fmaf(z1, qsum[k][g], s[i][2 * k + 1]));
+              if (m == 0 && term == 0) mma0(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
+              else mma(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
             }
           }
         }
-        // online softmax in powers of two.  The running maximum moves only when a score passes it by kSlack, which is
-        // rare after the first tiles; until then exponentials are at most 2^kSlack.
-        const bool masked = t >= whole;
-        bool over = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = scales[g * kKvTile + 8 * i];
+          const float sk = lo_bf16(w), z = fmaf(F32 ? 8.0f : -128.0f, sk, hi_bf16(w));
 #pragma unroll
-          for (int e = 0; e < 2 * NR; ++e) {
-            s[i][e] *= c_log2;
-          }
-        if (masked) {
-          __syncwarp();  // (keeps the branch a branch)
+          for (int k = 0; k < NR; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[k][i][e] = fmaf(sk, acc[k][2 * i + e], fmaf(z, qsum[k][e][g], s[k][i][e]));
+        }
+      }
+      // online softmax in powers of two.  The running maximum moves only when a score passes it by kSlack, which is
+      // rare after the first tiles; until then exponentials are at most 2^kSlack.
+      const bool masked = t >= whole;
+      const int key = t * kKvTile + r;
+#pragma unroll
+      for (int k = 0; k < NR; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[k][i][0] *= c_log2, s[k][i][1] *= c_log2;
+      if (masked) {
+        __syncwarp();  // (keeps the branch a branch)
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 2 * NR; ++e)
-              if (t * kKvTile + 8 * i + 2 * q + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
-        }
+            for (int e = 0; e < 2; ++e)
+              if (key + 8 * i >= lim[k][e]) s[k][i][e] = -INFINITY;
+      }
+      bool over = false;
+#pragma unroll
+      for (int k = 0; k < NR; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) over |= fmaxf(s[k][0][e], s[k][1][e]) > mx[k][e] + kSlack;
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int k = 0; k < NR; ++k)
-          over |= fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1])) > mx[k] + kSlack;
-        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-          for (int k = 0; k < NR; ++k) {
-            float m = fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = fmaxf(m, mx[k]);
-            const float f = m == mx[k] ? 1.0f : ex2(mx[k] - m);
-            mx[k] = m;
-            l[k] *= f;
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(s[k][0][e], s[k][1][e]);
 #pragma unroll
-            for (int g = 0; g < GV; ++g) ob[k][g] *= f;
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            m = fmaxf(m, mx[k][e]);
+            const float f = m == mx[k][e] ? 1.0f : ex2(mx[k][e] - m);
+            mx[k][e] = m;
+            l[k][e] *= f;
 #pragma unroll
-            for (int g = 0; g < (F32 ? 1 : GV); ++g) {
-              rs[g][2 * k] *= f;
-              if constexpr (NR == 1) rs[g][2] *= f;
-            }
+            for (int g = 0; g < GV; ++g) ob[k][e][g] *= f;
+#pragma unroll
+            for (int g = 0; g < (F32 ? 1 : GV); ++g) rs[k][g][e] *= f;
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-              for (int jj = 0; jj < 8; ++jj) {
-                o[cb][jj][2 * k] *= f, o[cb][jj][2 * k + 1] *= f;
-                if constexpr (NR == 1) o[cb][jj][2] *= f, o[cb][jj][3] *= f;  // the same row's low part
-              }
+              for (int x = 0; x < 4; ++x) o[k][cb][x][e] *= f, o[k][cb][x][2 + e] *= f;
           }
-        }
+      }
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const float m = mx[k] == -INFINITY ? 0.0f : mx[k];
+      for (int k = 0; k < NR; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float pe = F32 ? exp2f(s[i][2 * k + e] - m) : ex2(s[i][2 * k + e] - m);
-              s[i][2 * k + e] = pe;
-              l[k] += pe;
-            }
-        }
-        // values: p_t s_t against the codes around 8
-#pragma unroll
-        for (int gv = 0; gv < GV; ++gv) {
-          uint32_t ph[4], pl[4], pt[4];  // A fragments: (row r, row r + 8) x (tokens 2q.., tokens 2q + 8..)
+        for (int e = 0; e < 2; ++e) {
+          const float m = mx[k][e] == -INFINITY ? 0.0f : mx[k][e];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint2 sw = *reinterpret_cast<const uint2*>(tile + kv_scale_off(D) + (GK + gv) * 64 + (8 * i + 2 * q) * 4);
-            const float s0 = lo_bf16(sw.x), s1 = lo_bf16(sw.y);
-            const float z0 = F32 ? fmaf(8.0f, s0, hi_bf16(sw.x)) : hi_bf16(sw.x);
-            const float z1 = F32 ? fmaf(8.0f, s1, hi_bf16(sw.y)) : hi_bf16(sw.y);
+            const float pe = F32 ? exp2f(s[k][i][e] - m) : ex2(s[k][i][e] - m);
+            s[k][i][e] = pe;
+            l[k][e] += pe;
+          }
+        }
+      // values: p_t s_t, in parts and turned into B fragments, against the codes
 #pragma unroll
-            for (int k = 0; k < NR; ++k) {
-              float x0 = s[i][2 * k] * s0, x1 = s[i][2 * k + 1] * s1;
-              float y0 = s[i][2 * k] * z0, y1 = s[i][2 * k + 1] * z1;
-              if (masked) {  // what a row does not see may hold anything
-                const int tok = t * kKvTile + 8 * i + 2 * q;
-                if (tok >= lim[k]) x0 = y0 = 0.0f;
-                if (tok + 1 >= lim[k]) x1 = y1 = 0.0f;
-              }
-              ob[k][gv] += y0 + y1;
-              const uint32_t hi = bf16x2(x0, x1);
-              x0 -= lo_bf16(hi), x1 -= hi_bf16(hi);
-              const uint32_t lo = bf16x2(x0, x1);
-              if constexpr (NR == 1) {  // rows 8 .. 15 of the product carry the low parts of rows 0 .. 7
-                ph[2 * i] = hi, ph[2 * i + 1] = lo;
-              } else {
-                ph[2 * i + k] = hi, pl[2 * i + k] = lo;
-              }
-              if constexpr (F32) pt[2 * i + k] = bf16x2(x0 - lo_bf16(lo), x1 - hi_bf16(lo));
+      for (int gv = 0; gv < GV; ++gv) {
+        float sv[2], bv[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = scales[(GK + gv) * kKvTile + 8 * i];
+          sv[i] = lo_bf16(w);
+          bv[i] = F32 ? fmaf(8.0f, sv[i], hi_bf16(w)) : hi_bf16(w);
+        }
+        uint32_t f[NR][TP][2];
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x[2], y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[e] = s[k][i][e] * sv[i], y[e] = s[k][i][e] * bv[i];
+            if (masked) {  // what a row does not see may hold anything
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (key + 8 * i >= lim[k][e]) x[e] = y[e] = 0.0f;
+            }
+            ob[k][0][gv] += y[0], ob[k][1][gv] += y[1];
+#pragma unroll
+            for (int tp = 0; tp < TP; ++tp) {
+              const uint32_t w = bf16x2(x[0], x[1]);
+              f[k][tp][i] = transpose8x8(w);
+              x[0] -= lo_bf16(w), x[1] -= hi_bf16(w);
             }
           }
-          if constexpr (!F32) {
-            mma(rs[gv], ph[0], ph[1], ph[2], ph[3], 0x3f803f80u, 0x3f803f80u);
-            if constexpr (NR == 2) mma(rs[gv], pl[0], pl[1], pl[2], pl[3], 0x3f803f80u, 0x3f803f80u);
-          }
+        if constexpr (!F32) {
 #pragma unroll
-          for (int cb = gv * (CB / GV); cb < (gv + 1) * (CB / GV); ++cb) {
-            uint32_t w[4];
+          for (int k = 0; k < NR; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = *reinterpret_cast<const uint32_t*>(tile + kv_v_off(D) + cb * 512 + ((e >> 1) * 8 + (e & 1) * 4 + q) * 32 + r * 4);
+            for (int tp = 0; tp < TP; ++tp)
+              mma(rs[k][gv], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, f[k][tp][0], f[k][tp][1]);
+        }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t sel = half ? 0x7632 : 0x5410;
-              const uint32_t w01 = __byte_perm(w[0], w[1], sel), w23 = __byte_perm(w[2], w[3], sel);
+        for (int cb = gv * (CB / GV); cb < (gv + 1) * (CB / GV); ++cb) {
+          uint32_t w[4];
 #pragma unroll
-              for (int jj = 0; jj < 4; ++jj) {
-                const uint32_t b0 = F32 ? codes.c8(w01 >> (4 * jj)) : codes.c128(w01 >> (4 * jj));
-                const uint32_t b1 = F32 ? codes.c8(w23 >> (4 * jj)) : codes.c128(w23 >> (4 * jj));
-                float(&c)[4] = o[cb][half * 4 + jj];
-                mma(c, ph[0], ph[1], ph[2], ph[3], b0, b1);
-                if constexpr (NR == 2) mma(c, pl[0], pl[1], pl[2], pl[3], b0, b1);
-                if constexpr (F32) mma(c, pt[0], pt[1], pt[2], pt[3], b0, b1);
+          for (int e = 0; e < 4; ++e)
+            w[e] = *reinterpret_cast<const uint32_t*>(tile + kv_v_off(D) + cb * 512 + ((e >> 1) * 8 + (e & 1) * 4 + q) * 32 + r * 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7632 : 0x5410;
+            const uint32_t w01 = __byte_perm(w[0], w[1], sel), w23 = __byte_perm(w[2], w[3], sel);
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {  // channels 8r + 4 half + 2 jj and the next
+              uint32_t c[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                c[e] = F32 ? codes.c8(w01 >> (8 * jj + 4 * e)) : codes.c128(w01 >> (8 * jj + 4 * e));
+                c[2 + e] = F32 ? codes.c8(w23 >> (8 * jj + 4 * e)) : codes.c128(w23 >> (8 * jj + 4 * e));
               }
+#pragma unroll
+              for (int k = 0; k < NR; ++k)
+#pragma unroll
+                for (int tp = 0; tp < TP; ++tp)
+                  mma(o[k][cb][2 * half + jj], c[0], c[1], c[2], c[3], f[k][tp][0], f[k][tp][1]);
             }
           }
         }
-        __syncwarp();  // the stage is read before it is refilled
       }
+      __syncwarp();  // the stage is read before it is refilled
     }
     if (dead)  // the copies still in flight land before the ring is used for the join
       for (int j = done; j < min(count, done + S); ++j)
@@ -412,37 +437,33 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
     // the join: every warp's rows (unnormalised, bias added) into its ring, then all threads over rows and channels
     float* mine = reinterpret_cast<float*>(ring);
     constexpr int LD = D + 4;
+    static_assert(RT * LD * 4 <= S * TB, "the join uses the ring");
 #pragma unroll
-    for (int k = 0; k < NR; ++k) {
-      float sl = l[k];
-      sl += __shfl_xor_sync(0xffffffffu, sl, 1);
-      sl += __shfl_xor_sync(0xffffffffu, sl, 2);
+    for (int k = 0; k < NR; ++k)
 #pragma unroll
-      for (int g = 0; g < GV; ++g) {
-        ob[k][g] += __shfl_xor_sync(0xffffffffu, ob[k][g], 1);
-        ob[k][g] += __shfl_xor_sync(0xffffffffu, ob[k][g], 2);
-      }
-      if constexpr (!F32) {
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * k + 2 * q + e;
 #pragma unroll
-        for (int g = 0; g < GV; ++g) ob[k][g] = fmaf(-128.0f, rs[g][2 * k] + (NR == 1 ? rs[g][2] : 0.0f), ob[k][g]);
-      }
-      if (q == 0) s_ml[warp][r + 8 * k] = make_float2(mx[k], sl);
+        for (int x = 4; x < 32; x <<= 1) {
+          l[k][e] += __shfl_xor_sync(0xffffffffu, l[k][e], x);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
+          for (int g = 0; g < GV; ++g) ob[k][e][g] += __shfl_xor_sync(0xffffffffu, ob[k][e][g], x);
+        }
+        if constexpr (!F32) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)  // channels 16q + 8e + (0 .. 7)
+          for (int g = 0; g < GV; ++g) ob[k][e][g] = fmaf(-128.0f, rs[k][g][e], ob[k][e][g]);
+        }
+        if (r == 0) s_ml[warp][row] = make_float2(mx[k][e], l[k][e]);
 #pragma unroll
-          for (int jj = 0; jj < 8; jj += 4) {
-            float4 v;
-            float* f = &v.x;
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              f[x] = o[cb][jj + x][2 * k + e] + ob[k][cb * GV / CB];
-              if constexpr (NR == 1) f[x] += o[cb][jj + x][2 + e];
-            }
-            *reinterpret_cast<float4*>(mine + (r + 8 * k) * LD + cb * 64 + 16 * q + 8 * e + jj) = v;
+          for (int half = 0; half < 2; ++half) {
+            const float b = ob[k][e][cb * GV / CB];
+            *reinterpret_cast<float4*>(mine + row * LD + cb * 64 + 8 * r + 4 * half) =
+                make_float4(o[k][cb][2 * half][e] + b, o[k][cb][2 * half][2 + e] + b, o[k][cb][2 * half + 1][e] + b,
+                            o[k][cb][2 * half + 1][2 + e] + b);
           }
-    }
+      }
     __syncthreads();
     const bool from_start = t_begin == 0, to_end = t_end == walk.tiles;
     const int rows_here = row_last - rt * RT + 1;
@@ -490,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) attn_kernel(const 
 // One block per (split group, row, D / gridDim.z channels): joins the partial rows that the group's blocks have left.
 // Block x takes the x-th of the blocks that started a group and did not finish it.  Four channels a thread, the weights
 // 2^(m_i - m) of all parts first, so that the loads of the rows do not wait on one another.
-constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kMaxBlocks = 512;
+constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kMaxBlocks = 256 * kSplitPer;
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ float4 s_o[kCombineThreads];
@@ -505,10 +526,10 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   if (gr >= rw.rows) return;
   const int Gq = a.p.Hq / a.cache.Hkv, parts = sp.w - first + 1;
   auto slot_of_part = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * 16 + row; };
-  float2 ml[2];
+  float2 ml[kSplitPer];
   float m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kSplitPer; ++i) {
     const int x = i * kCombineThreads + threadIdx.x;
     ml[i] = x < parts ? a.ws.ml[slot_of_part(x)] : make_float2(-INFINITY, 0.0f);
     m = fmaxf(m, ml[i].x);
@@ -520,7 +541,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
 #pragma unroll
   for (int w = 0; w < kCombineWarps; ++w) m = fmaxf(m, s_m[w]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kSplitPer; ++i) {
     const bool none = ml[i].x == -INFINITY && ml[i].y == 0.0f;  // a part whose tokens the row does not see
     const float f = none ? -1.0f : exp2f(ml[i].x - m);
     if (!none) l = fmaf(f, ml[i].y, l);
@@ -561,8 +582,8 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   if (c == 0 && a.p.lse) a.p.lse[out] = sl == 0.0f ? -INFINITY : (m + log2f(sl)) * kLn2;
 }
 
-int grid_of(int D) { return kAttnSms * blocks_per_sm(D); }
-static_assert(kAttnSms * blocks_per_sm(64) <= kMaxBlocks, "split_group looks at two blocks a thread");
+int grid_of(int D, int RT) { return kAttnSms * blocks_per_sm(D, RT); }
+static_assert(kAttnSms * blocks_per_sm(64, 8) <= kMaxBlocks, "split_group looks at kSplitPer blocks a thread");
 
 struct WsLayout {
   size_t o, ml, split, total;
@@ -586,8 +607,8 @@ constexpr int kPrefillFrom = 64;
 
 template <typename T, int D, int RT>
 cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
-  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D), 16), ws), grid_of(D), status, 0};
-  constexpr int bytes = smem_bytes(D, sizeof(T) == 4 ? 3 : 1);
+  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D, RT), 16), ws), grid_of(D, RT), status, 0};
+  constexpr int bytes = smem_bytes(D, RT, sizeof(T) == 4 ? 3 : 1);
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   {
@@ -619,7 +640,7 @@ cudaError_t run_d(const AttnProblem& p, const KvCache& c, void* ws, int32_t* sta
 }  // namespace
 
 size_t attention_ws_bytes(int32_t T, int32_t, int32_t Hq, int32_t Hkv, int32_t D, bool bf16) {
-  size_t w = ws_layout(D, grid_of(D), 16).total;
+  size_t w = ws_layout(D, grid_of(D, 8), 16).total;  // the larger grid
   if (bf16 && D <= 128 && (int64_t)T * (Hq / Hkv) > kPrefillFrom)
     w = std::max(w, ws_layout(D, kAttnSms, kPrefillRows).total);
   return w;

@@ -161,20 +161,21 @@ struct AttnWalk {
   }
 };
 
-// the x-th block that started a group and did not finish it, or -1 (256 threads, up to 512 blocks)
+// the x-th block that started a group and did not finish it, or -1 (256 threads; s_count: a word a warp and round)
+constexpr int kSplitPer = 3;  // blocks a thread looks at: up to 768
 __device__ __forceinline__ int split_group(const AttnArgs& a, int x, int* s_count, int* s_first) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) *s_first = -1;
-  uint32_t ball[2];
+  uint32_t ball[kSplitPer];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kSplitPer; ++i) {
     const int b = i * 256 + threadIdx.x;
     ball[i] = __ballot_sync(0xffffffffu, b < a.G && a.ws.split[b].w >= 0);
     if (lane == 0) s_count[i * 8 + warp] = __popc(ball[i]);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kSplitPer; ++i) {
     int before = __popc(ball[i] & ((1u << lane) - 1u));
     for (int w = 0; w < i * 8 + warp; ++w) before += s_count[w];
     if (((ball[i] >> lane) & 1u) && before == x) *s_first = i * 256 + threadIdx.x;

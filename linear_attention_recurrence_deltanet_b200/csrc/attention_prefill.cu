@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 // A warp a row of a split group: joins the partial rows of its blocks.
 template <int D>
 __global__ void __launch_bounds__(256) attn_prefill_combine_kernel(const __grid_constant__ AttnArgs a) {
-  __shared__ int s_count[16], s_first;
+  __shared__ int s_count[8 * kSplitPer], s_first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = split_group(a, blockIdx.x, s_count, &s_first);
   if (first < 0) return;
