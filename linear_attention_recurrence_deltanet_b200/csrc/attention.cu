@@ -27,8 +27,8 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kGroupUnits = 12;  // what a group costs beside its tiles, in tiles
-constexpr int kMinUnits = 24;    // the least quota
+constexpr int kGroupUnits = 20;  // what a group costs beside its tiles, in tiles
+constexpr int kMinUnits = 20;    // the least quota
 constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 
 constexpr int stages(int D) { return D == 64 ? 8 : 4; }
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t s_full[kWarps][S];
   __shared__ int64_t s_warp[kWarps];
-  __shared__ int64_t s_found[2];           // sequence that holds the block's first unit, units before it
+  __shared__ int64_t s_found[4];
   __shared__ float2 s_ml[kWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
   unsigned char* ring = smem + warp * (S * TB);
@@ -113,16 +113,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
     if (walk.piece(a)) {
     const int n = walk.n, h = walk.h, rt = walk.rt, t_begin = walk.t0, t_end = walk.t1;
     const AttnRows rw = walk.rw;
-    // keys that this lane's rows see; a row that is none sees all and is not written
-    int lim[NR][2];
-#pragma unroll
-    for (int k = 0; k < NR; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = rt * RT + 8 * k + 2 * q + e;
-        lim[k][e] = row < rw.rows ? max(0, min(rw.first + row / Gq, rw.cap)) : 0x7fffffff;
-        if (row < rw.rows && rw.first + row / Gq > rw.cap) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
-      }
     const int row_last = min(rw.rows, (rt + 1) * RT) - 1;
     const int whole = min(rw.first + rt * RT / Gq, rw.cap) / kKvTile;  // every row of the group sees the tiles before this one
     const int seen_tiles = (max(0, min(rw.first + row_last / Gq, rw.cap)) + kKvTile - 1) / kKvTile;
@@ -156,6 +146,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll 1
     for (int j = 0; j < S - 1; ++j) fetch(j);
 
+    // keys that this lane's rows see; a row that is none sees all and is not written
+    int lim[NR][2];
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = rt * RT + 8 * k + 2 * q + e;
+        lim[k][e] = row < rw.rows ? max(0, min(rw.first + row / Gq, rw.cap)) : 0x7fffffff;
+        if (row < rw.rows && rw.first + row / Gq > rw.cap) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
+      }
     // queries as B fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64 of row r, paired (c, c + 4) as the
     // codes are; [group], [2 + group]
     uint32_t qf[QS ? 1 : NM][4];

@@ -84,53 +84,60 @@ struct AttnWalk {
   int t0, t1;                   // the piece's tiles
   AttnRows rw;
 
-  __device__ __forceinline__ int tiles_of(const AttnArgs& a, const AttnRows& r, int i) const {
+  __device__ __forceinline__ static int tiles_of(const AttnArgs& a, const AttnRows& r, int i) {
     const int last = min(r.rows, (i + 1) * RT) - 1;  // the tile's last row sees most
     const int seen = min(r.first + last / (a.p.Hq / a.cache.Hkv), r.cap);
     return max(1, (seen + TT - 1) / TT);  // at least one: somebody writes the rows
   }
-  __device__ __forceinline__ int64_t head_units(const AttnArgs& a, int i) const {  // of one head of sequence i
-    const AttnRows r = rows_of(a, i);
+  __device__ __forceinline__ static int64_t head_units(const AttnArgs& a, const AttnRows& r) {  // of one head
     int64_t x = 0;
     for (int j = 0; j * RT < r.rows; ++j) x += GU + tiles_of(a, r, j);
     return x;
   }
-  // Every thread of the block; false: nothing to do.  s_warp: a word a warp, s_found: two.
+  __device__ __forceinline__ static int64_t div(int64_t x, int64_t y) {  // of positive numbers; 64-bit division is slow
+    return ((x | y) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  }
+  // Every thread of the block; false: nothing to do.  s_warp: a word a warp, s_found: four (the sum; the sequence, the units before it, those of a head).  Up to as many sequences as
+  // threads are looked at once; more, in rounds, twice: for the sum, then for the sequence that holds u.
   __device__ __forceinline__ bool start(const AttnArgs& a, int threads, int64_t* s_warp, int64_t* s_found) {
     const int tid = threadIdx.x;
-    int64_t total = 0;
+    int64_t total = 0, own = 0, upto = 0, head = 0;
     for (int n0 = 0; n0 < a.p.N; n0 += threads) {
-      const int i = n0 + tid;
-      const int64_t s = block_scan(i < a.p.N ? head_units(a, i) * a.cache.Hkv : 0, s_warp);
-      __syncthreads();
-      if (tid == threads - 1) s_found[0] = s;
+      head = n0 + tid < a.p.N ? head_units(a, rows_of(a, n0 + tid)) : 0;
+      own = head * a.cache.Hkv;
+      upto = block_scan(own, s_warp);
+      if (tid == threads - 1) s_found[0] = upto;
       __syncthreads();
       total += s_found[0];
     }
-    quota = max((int64_t)MIN, (total + a.G - 1) / a.G);
+    quota = max((int64_t)MIN, div(total + a.G - 1, a.G));
     u = quota * blockIdx.x;
     u_end = min(total, u + quota);
     if (tid == 0) a.ws.split[blockIdx.x] = make_int4(0, 0, 0, -1);
     if (u >= u_end) return false;
-    int64_t before = 0;
-    for (int n0 = 0; n0 < a.p.N; n0 += threads) {
-      const int i = n0 + tid;
-      const int64_t own = i < a.p.N ? head_units(a, i) * a.cache.Hkv : 0;
-      const int64_t s = before + block_scan(own, s_warp);
+    if (a.p.N <= threads) {
+      if (upto - own <= u && u < upto) s_found[1] = tid, s_found[2] = upto - own, s_found[3] = head;
       __syncthreads();
-      if (i < a.p.N && s - own <= u && u < s) s_found[0] = i, s_found[1] = s - own;
-      if (tid == threads - 1) s_warp[0] = s;
-      __syncthreads();
-      before = s_warp[0];
-      __syncthreads();
-      if (before > u) break;
+    } else {
+      int64_t before = 0;
+      for (int n0 = 0; n0 < a.p.N; n0 += threads) {
+        head = n0 + tid < a.p.N ? head_units(a, rows_of(a, n0 + tid)) : 0;
+        own = head * a.cache.Hkv;
+        upto = before + block_scan(own, s_warp);
+        __syncthreads();
+        if (upto - own <= u && u < upto) s_found[1] = n0 + tid, s_found[2] = upto - own, s_found[3] = head;
+        if (tid == threads - 1) s_warp[0] = upto;
+        __syncthreads();
+        before = s_warp[0];
+        __syncthreads();
+        if (before > u) break;
+      }
     }
-    n = (int)s_found[0];
-    at = u - s_found[1];
+    n = (int)s_found[1];
+    at = u - s_found[2];
     rw = rows_of(a, n);
-    const int64_t per_head = head_units(a, n);
-    h = (int)(at / per_head), rt = 0;
-    at -= h * per_head;
+    h = (int)div(at, s_found[3]), rt = 0;
+    at -= h * s_found[3];
     for (int w; at >= (w = GU + tiles_of(a, rw, rt)); ++rt) at -= w;
     return true;
   }
@@ -142,7 +149,7 @@ struct AttnWalk {
     return t0 < t1;
   }
   __device__ __forceinline__ int rows_here() const { return min(RT, rw.rows - rt * RT); }
-  __device__ __forceinline__ int last_block() const { return (int)((u - at + GU + tiles - 1) / quota); }  // of the group
+  __device__ __forceinline__ int last_block() const { return (int)div(u - at + GU + tiles - 1, quota); }  // of the group
   __device__ __forceinline__ bool next(const AttnArgs& a) {
     u += GU + tiles - at;
     at = 0;

@@ -13,7 +13,7 @@
 // A block takes two tiles of 128 query rows (tokens x the heads that share a
 // key/value head) through the same keys.  Warps 0-3 and 4-7 are the softmax of
 // either tile, a thread a row; warps 8-15 expand, 16 keys each; warp 16 issues the
-// products.  While one tile's softmax runs the other's products do.  S is 128
+// products (17-19 fill its group up).  While one tile's softmax runs the other's products do.  S is 128
 // columns of TMEM, P overwrites its first 64 in fp16 and is the A operand of P V.
 // O stays in TMEM; the running maximum moves only when a score passes it by
 // kSlack, and only then is O rescaled.
@@ -30,7 +30,14 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = kPrefillRows, kKeys = 128;
-constexpr int kSoftWarps = 8, kExpandWarps = 8, kThreads = (kSoftWarps + kExpandWarps + 1) * 32;
+constexpr int kSoftWarps = 8, kExpandWarps = 8, kThreads = (kSoftWarps + kExpandWarps + 4) * 32;
+// Registers a thread after the start: 640 threads begin with 96, 61440 in all; these come to 60416.
+constexpr int kSoftRegs = 128, kExpandRegs = 80, kProductRegs = 56;
+static_assert((kSoftWarps * kSoftRegs + kExpandWarps * kExpandRegs + 4 * kProductRegs) * 32 <= kThreads * 96, "register split");
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 using Walk = AttnWalk<kRows, kKeys, 3, 6>;     // a group's queries and output cost about three tiles
 
@@ -47,23 +54,32 @@ struct alignas(16) Meta {
 };
 static_assert(offsetof(Meta, valid) % 8 == 0, "vector reads");
 
-// eight codes as s c + b, in the order 0 4 1 5 2 6 3 7 (nibbles 1, 3, .. are masked into 1024 + 16 c: no shift)
-__device__ __forceinline__ uint4 expand(uint32_t w, __half2 s, __half2 b) {
-  uint32_t o[4];
-  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k16 = __half2half2(__ushort_as_half(0x2c00)),
-                k64 = __half2half2(__ushort_as_half(0xd400));  // 1024, 1/16, -64
+// Eight codes as s c + b, in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
+// shift.  The masks sit in registers whose values the compiler does not know (a kernel argument that is 0 is in them),
+// so that one instruction takes a mask and the exponent.
+struct Expand {
+  uint32_t lo, hi, magic;
+  __device__ __forceinline__ explicit Expand(uint32_t zero)
+      : lo(0x000f000fu + zero), hi(0x00f000f0u + zero), magic(0x64006400u + zero) {}
+  __device__ __forceinline__ uint4 operator()(uint32_t w, __half2 s, __half2 b) const {
+    uint32_t o[4];
+    const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k16 = __half2half2(__ushort_as_half(0x2c00)),
+                  k64 = __half2half2(__ushort_as_half(0xd400));  // 1024, 1/16, -64
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 cl = __hsub2(*reinterpret_cast<const __half2*>(&lo), k1024);
-    const __half2 ch = __hfma2(*reinterpret_cast<const __half2*>(&hi), k16, k64);
-    const __half2 wl = __hfma2(cl, s, b), wh = __hfma2(ch, s, b);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&wl);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&wh);
-    w >>= 8;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x, y;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(lo), "r"(magic));  // (w & mask) | magic
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "r"(hi), "r"(magic));
+      const __half2 cl = __hsub2(*reinterpret_cast<const __half2*>(&x), k1024);
+      const __half2 ch = __hfma2(*reinterpret_cast<const __half2*>(&y), k16, k64);
+      const __half2 wl = __hfma2(cl, s, b), wh = __hfma2(ch, s, b);
+      o[2 * i] = *reinterpret_cast<const uint32_t*>(&wl);
+      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&wh);
+      w >>= 8;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
+};
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // exponent of a finite magnitude's bits, at least -100
 __device__ __forceinline__ int exponent(uint32_t bits) { return max(-100, (int)(bits >> 23) - 127); }
@@ -83,6 +99,41 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
+// 32 columns of this thread's lane, not waited for; ld_wait() ends all loads in flight
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// the wait names the registers that the load fills, so that no use moves before it
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// a b + c and a + b of two floats in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 w, x, y, z;\n"
+      "mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 w, x, y;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -100,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], kv_full[2], kv_free[2], drain;
   __shared__ Meta meta[2];
   __shared__ uint2 s_top[kExpandWarps];
-  __shared__ int64_t s_warp[kThreads / 32], s_found[2];
+  __shared__ int64_t s_warp[kThreads / 32], s_found[4];
   __shared__ uint32_t tslot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const AttnProblem& p = a.p;
@@ -128,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
+    more_regs<kSoftRegs>();
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kO + D * x;
@@ -207,18 +259,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             nan |= (w[i] & (k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0;
           }
         }
-        // the largest product, then the probabilities: S is read twice, 32 columns at a time
+        // S is read twice, 32 columns at a time and the next ones on their way: for the largest product, then for the
+        // probabilities
+        uint32_t raw[2][32];
+        tmem_ld32_async(ts, raw[0]);
         float top = -INFINITY;
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32) {
-          float v[32];
-          tmem_ld32(ts + c0, v);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&cur)[32] = raw[c & 1];
+          ld_wait(cur);
+          tmem_ld32_async(ts + 32 * ((c + 1) & 3), raw[(c + 1) & 1]);  // the last: the first again
           if (masked) {
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = seen(c0 + e) ? v[e] : -INFINITY;
+            for (int e = 0; e < 32; ++e) cur[e] = seen(32 * c + e) ? cur[e] : 0xff800000u;
           }
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(v[e], v[e + 1]));
+          for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])));
         }
         top = top == -INFINITY ? top : top * f;
         if (__any_sync(0xffffffffu, top > m + kSlack || v_step != 1.0f)) {
@@ -227,39 +284,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           l *= g;
           if (t > walk.t0) {  // the product of the last tile is done: S came after it
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              float v[32];
-              tmem_ld32(to + c0, v);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              float z[16];
+              uint32_t w[16];
+              tmem_ld16(to + c0, z);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= g * v_step;
-              tmem_st32(to + c0, v);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(z[e] * (g * v_step));
+              tmem_st16(to + c0, w);
             }
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : -m;
+        float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&cur)[32] = raw[c & 1];
+          ld_wait(cur);
+          if (c < 3) tmem_ld32_async(ts + 32 * (c + 1), raw[(c + 1) & 1]);
           float v[32];
-          tmem_ld32(ts + c0, v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 z = fma2(make_float2(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), make_float2(f, f),
+                                  make_float2(base, base));
+            v[e] = ex2(z.x), v[e + 1] = ex2(z.y);
+          }
+          if (masked) {
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = seen(32 * c + e) ? v[e] : 0.0f;
+          }
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], f, -base));
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = seen(c0 + e) ? v[e] : 0.0f;
-          }
-          float sum[4] = {};
-#pragma unroll
-          for (int e = 0; e < 32; ++e) sum[e & 3] += v[e];
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int e = 0; e < 32; e += 2) {
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], make_float2(v[e], v[e + 1]));
+            const __half2 h = __floats2half2_rn(v[e], v[e + 1]);
+            w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
           }
           __syncwarp();
-          tmem_st16(ts + c0 / 2, w);
+          tmem_st16(ts + 16 * c, w);
         }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         fence_before();
         __syncwarp();
@@ -309,9 +373,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } while (walk.next(a));
   } else if (warp < kSoftWarps + kExpandWarps) {
     // ------------------------------------------------------------- expansion
+    fewer_regs<kExpandRegs>();
     const int w = warp - kSoftWarps, half = lane & 1, tk = lane >> 1;
     const int tv = (tk & 8) | ((tk & 3) << 1) | ((tk >> 2) & 1);  // the token of V row tk (v_row's inverse)
     int k_ref = -100, v_ref = -100;                               // exponents of the largest values so far
+    const Expand expand(a.zero);
+    // where this lane's four chunks of 64 channels go, of keys and of values
+    const bool odd = (tv >> 2) & 1;  // pairs of words in turn: the eight lanes of a store then hit all banks
+    uint32_t at_k[4], at_v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      at_k[j] = 2 * TILE + kmaj_chunk(kKeys, 16 * w + tk, (half * 4 + j) * 8);
+      at_v[j] = 3 * TILE + mnmaj_chunk(kKeys, 16 * w + tv, (half * 4 + (j ^ (odd ? 1 : 0))) * 8);
+    }
     do {
       if (!walk.piece(a)) continue;
       const int n = walk.n, h = walk.h;
@@ -395,25 +469,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           mt.valid[w] = ok ? 1 : 0;
           mt.v_nan[w] = (uint16_t)nans;
         }
-        unsigned char* sk = sm + (2 + 2 * st) * TILE;
-        unsigned char* sv = sk + TILE;
+        unsigned char* stage = sm + 2 * st * TILE;
+        constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
           const __half2 s = __float2half2_rn(lo_bf16(ks[g]) * fk), b = __float2half2_rn(hi_bf16(ks[g]) * fk);
           const uint32_t c[4] = {kc[g].x, kc[g].y, kc[g].z, kc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(sk + kmaj_chunk(kKeys, 16 * w + tk, g * 64 + (half * 4 + j) * 8)) = expand(c[j], s, b);
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_k[j] + g * kBlock64) = expand(c[j], s, b);
         }
         const __half2 s = __float2half2_rn(lo_bf16(vs) * fv), b = __float2half2_rn(hi_bf16(vs) * fv);
-        const bool odd = (tv >> 2) & 1;  // pairs of words in turn: the eight lanes of a store then hit all banks
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
           const uint32_t c[4] = {odd ? vc[g].y : vc[g].x, odd ? vc[g].x : vc[g].y, odd ? vc[g].w : vc[g].z, odd ? vc[g].z : vc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(sv + mnmaj_chunk(kKeys, 16 * w + tv, g * 64 + (half * 4 + (j ^ (odd ? 1 : 0))) * 8)) =
-                expand(c[j], s, b);
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_v[j] + g * kBlock64) = expand(c[j], s, b);
         }
         fence_async_smem();
         bar_sync(3, 32 * kExpandWarps);
@@ -427,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } while (!bad && walk.next(a));
   } else {
     // ------------------------------------------------------------- products
+    fewer_regs<kProductRegs>();
+    if (warp == kSoftWarps + kExpandWarps) {
     const uint32_t id_s = idesc_f16(128, kKeys, false, false), id_o = idesc_f16(128, D, false, true);
     const uint64_t dq = desc_kmaj(smem_u32(sm), 128, 0), dk = desc_kmaj(smem_u32(sm) + 2 * TILE, kKeys, 0);
     const uint64_t dv = desc_mnmaj(smem_u32(sm) + 3 * TILE, kKeys, 0);
@@ -483,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     if (elect_one()) mma_commit(&drain);  // every product issued has finished before TMEM is released
     __syncwarp();
     mbar_wait_warp(&drain, 0, kWaitCycles);
+    }
   }
   if (sync_tc_any(bad) && tid == 0) set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));
   if (warp == kSoftWarps + kExpandWarps) tmem_dealloc(tbase, 512);
@@ -507,13 +580,17 @@ __global__ void __launch_bounds__(256) attn_prefill_combine_kernel(const __grid_
 #pragma unroll
     for (int c = 0; c < V; ++c) v[c] = 0.0f;
     for (int i = 0; i < parts; ++i) m = fmaxf(m, a.ws.ml[slot(i)].x);
+#pragma unroll 2
     for (int i = 0; i < parts; ++i) {
       const float2 ml = a.ws.ml[slot(i)];
       const float f = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : exp2f(ml.x - m);
-      const float* o = a.ws.o + slot(i) * D + lane * V;
+      const float2* o = reinterpret_cast<const float2*>(a.ws.o + slot(i) * D + lane * V);
       l = fmaf(f, ml.y, l);
 #pragma unroll
-      for (int c = 0; c < V; ++c) v[c] = fmaf(f, o[c], v[c]);
+      for (int c = 0; c < V / 2; ++c) {
+        const float2 y = o[c];
+        v[2 * c] = fmaf(f, y.x, v[2 * c]), v[2 * c + 1] = fmaf(f, y.y, v[2 * c + 1]);
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t out = (int64_t)(a.p.cu[sp.x] + gr / Gq) * a.p.Hq + sp.y * Gq + gr % Gq;
@@ -535,7 +612,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t stream) {
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   LaunchScope scope(GDN_K_ATTN_COMBINE, stream);
-  attn_prefill_combine_kernel<D><<<dim3((unsigned)a.G, 8), 256, 0, stream>>>(a);
+  attn_prefill_combine_kernel<D><<<dim3((unsigned)a.G, 16), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
