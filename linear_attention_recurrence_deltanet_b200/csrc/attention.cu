@@ -29,7 +29,6 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroupUnits = 20;  // what a group costs beside its tiles, in tiles
 constexpr int kMinUnits = 20;    // the least quota
-constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 
 constexpr int stages(int D) { return D == 64 ? 8 : 4; }
 constexpr int blocks_per_sm(int D, int RT) { return D == 256 ? (RT == 8 ? 3 : 2) : RT == 8 ? 4 : 3; }
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
       if ((j & 31) == 0) valid = valid_next;
       fetch(jf);
       const uint32_t stage = (used + j) & (S - 1);
-      if (!tc::mbar_wait_warp(&s_full[warp][stage], ((used + j) / S) & 1, kWaitCycles)) {
+      if (!tc::mbar_wait_warp(&s_full[warp][stage], ((used + j) / S) & 1)) {
         set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));
         dead = true;
         done = j;
@@ -431,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
     }
     if (dead)  // the copies still in flight land before the ring is used for the join
       for (int j = done; j < min(count, done + S); ++j)
-        tc::mbar_wait_warp(&s_full[warp][(used + j) & (S - 1)], ((used + j) / S) & 1, kWaitCycles / 100);
+        tc::mbar_wait_warp(&s_full[warp][(used + j) & (S - 1)], ((used + j) / S) & 1, tc::kWaitTries / 64);
     used += count;
 
     // the join: every warp's rows (unnormalised, bias added) into its ring, then all threads over rows and channels

@@ -19,8 +19,6 @@
 // kSlack, and only then is O rescaled.
 #include <cuda_fp16.h>
 
-#include <cstddef>
-
 #include "attention.cuh"
 #include "tc.cuh"
 
@@ -38,7 +36,6 @@ template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 using Walk = AttnWalk<kRows, kKeys, 3, 6>;     // a group's queries and output cost about three tiles
 
 constexpr int tile_bytes(int D) { return kKeys * D * 2; }
@@ -46,13 +43,13 @@ constexpr int smem_bytes(int D) { return 6 * tile_bytes(D) + 1024 < 120000 ? 120
 
 // what the expanding warps say of a key tile
 struct alignas(16) Meta {
-  uint16_t v_nan[8];     // by key: its value is NaN (read as one uint4)
-  uint8_t valid[8];      // 16 keys each: they have a page (read as one uint2)
   float k_unit;          // a key's value = its operand times this
   float v_unit;          // the same of the values, of this tile and all before
   float v_step;          // v_unit before / after this tile: O is rescaled by it
+  uint32_t rare;         // some keys have no page (1), some values are NaN (2); the four are read as one uint4
+  uint8_t valid[8];      // 16 keys each: they have a page
+  uint16_t v_nan[8];     // by key: its value is NaN
 };
-static_assert(offsetof(Meta, valid) % 8 == 0, "vector reads");
 
 // Eight codes as s c + b, in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
 // shift.  The masks sit in registers whose values the compiler does not know (a kernel argument that is 0 is in them),
@@ -86,13 +83,8 @@ __device__ __forceinline__ int exponent(uint32_t bits) { return max(-100, (int)(
 __device__ __forceinline__ bool finite_word(uint32_t w) {
   return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
 }
-// bits of the largest magnitude a scale word's codes stand for
-__device__ __forceinline__ uint32_t reach(uint32_t w) {
-  if (!finite_word(w)) return 0;
-  const float s = lo_bf16(w), b = hi_bf16(w);
-  const uint32_t m = max(__float_as_uint(b) & 0x7fffffffu, __float_as_uint(fmaf(15.0f, s, b)) & 0x7fffffffu);
-  return max(m, __float_as_uint(s) & 0x7fffffffu);
-}
+// bound of the magnitudes that a finite scale word's codes stand for (twice the largest at most)
+__device__ __forceinline__ float reach(uint32_t w) { return fmaf(15.0f, fabsf(lo_bf16(w)), fabsf(hi_bf16(w))); }
 
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -237,26 +229,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
       float m = -INFINITY, l = 0.0f, v_unit = 1.0f;
       bool nan = false;
       for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
-        if (!group_wait(1 + x, 128, (warp & 3) == 0, &s_full[x], ph_s, nullptr, 0, kWaitCycles)) {
+        if (!group_wait(1 + x, 128, (warp & 3) == 0, &s_full[x], ph_s, nullptr, 0)) {
           bad = true;
           break;
         }
         ph_s ^= 1;
         fence_after();
         const Meta& mt = meta[kt & 1];
-        const float f = unit * mt.k_unit * c_log2, v_step = mt.v_step;
-        v_unit = mt.v_unit;
-        const uint2 valid = *reinterpret_cast<const uint2*>(mt.valid);
-        const uint4 vn = *reinterpret_cast<const uint4*>(mt.v_nan);
+        const uint4 units = *reinterpret_cast<const uint4*>(&mt);
+        const float f = unit * __uint_as_float(units.x) * c_log2, v_step = __uint_as_float(units.z);
+        v_unit = __uint_as_float(units.y);
+        uint2 valid = make_uint2(0x01010101u, 0x01010101u);
         const int left = lim - t * kKeys;  // keys of this tile that the row sees
-        const bool masked = (t + 1) * kKeys > whole || (valid.x & valid.y) != 0x01010101u;
+        const bool masked = (t + 1) * kKeys > whole || (units.w & 1u);
+        if (units.w & 1u) valid = *reinterpret_cast<const uint2*>(mt.valid);
         auto seen = [&](int c) { return c < left && ((c < 64 ? valid.x >> (8 * (c >> 4)) : valid.y >> (8 * ((c >> 4) - 4))) & 1u); };
-        if (vn.x | vn.y | vn.z | vn.w) {
-          const uint32_t w[4] = {vn.x, vn.y, vn.z, vn.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = left - 32 * i;
-            nan |= (w[i] & (k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0;
+        if (units.w & 2u) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int k = left - 16 * i;
+            nan |= (mt.v_nan[i] & (k >= 16 ? 0xffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0;
           }
         }
         // S is read twice, 32 columns at a time and the next ones on their way: for the largest product, then for the
@@ -329,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], ph_o, nullptr, 0, kWaitCycles)) {
+      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], ph_o, nullptr, 0)) {
         bad = true;
         break;
       }
@@ -377,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     const int w = warp - kSoftWarps, half = lane & 1, tk = lane >> 1;
     const int tv = (tk & 8) | ((tk & 3) << 1) | ((tk >> 2) & 1);  // the token of V row tk (v_row's inverse)
     int k_ref = -100, v_ref = -100;                               // exponents of the largest values so far
+    float k_lim = -1.0f, v_lim = -1.0f, fk = 0.0f, fv = 0.0f;     // what they hold, and their scales
     const Expand expand(a.zero);
     // where this lane's four chunks of 64 channels go, of keys and of values
     const bool odd = (tv >> 2) & 1;  // pairs of words in turn: the eight lanes of a store then hit all banks
@@ -431,44 +424,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
       for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
         if (t + 1 < walk.t1) load(t + 1, kn, vnx, ksn, vsn, okn);
         const int st = kt & 1;
-        // the tile's largest key and value
-        uint32_t top_k = 0;
+        // Mostly the tile's keys and values stay within the references and are finite, and every key has a page: one
+        // barrier says so, which the wait for the stage needs anyway.
+        float rk = 0.0f;
 #pragma unroll
-        for (int g = 0; g < GK; ++g) top_k = max(top_k, reach(ks[g]));
-        top_k = __reduce_max_sync(0xffffffffu, top_k);
-        const uint32_t top_v = __reduce_max_sync(0xffffffffu, reach(vs));
+        for (int g = 0; g < GK; ++g) rk = fmaxf(rk, reach(ks[g]));
+        const float rv = reach(vs);
+        bool odd_k = false;
+#pragma unroll
+        for (int g = 0; g < GK; ++g) odd_k |= !finite_word(ks[g]);
         const bool v_bad = !finite_word(vs);
-        const uint32_t nans = __reduce_or_sync(0xffffffffu, v_bad ? 1u << tv : 0u);
-        if (v_bad) vs = 0;
-        if (lane == 0) s_top[w] = make_uint2(top_k, top_v);
-        // (the barrier in here publishes s_top)
-        if (kt >= 2) {
-          if (!group_wait(3, 32 * kExpandWarps, w == 0, &kv_free[st], ((kt >> 1) & 1) ^ 1, nullptr, 0, kWaitCycles)) {
+        const bool plain = rk <= k_lim && rv <= v_lim && !odd_k && !v_bad && ok;
+        bool waited = true;
+        if (kt >= 2 && w == 0) waited = mbar_wait_warp(&kv_free[st], ((kt >> 1) & 1) ^ 1);
+        if (bar_or(3, 32 * kExpandWarps, !plain || !waited)) {
+          // the rest of it: whether the wait ran out, the tile's largest finite key and value, what is odd
+          uint32_t top_k = 0;
+#pragma unroll
+          for (int g = 0; g < GK; ++g)
+            if (finite_word(ks[g])) top_k = max(top_k, __float_as_uint(reach(ks[g])));
+          top_k = __reduce_max_sync(0xffffffffu, top_k);
+          uint32_t top_v = __reduce_max_sync(0xffffffffu, v_bad ? 0u : __float_as_uint(rv));
+          const uint32_t nans = __reduce_or_sync(0xffffffffu, v_bad ? 1u << tv : 0u);
+          if (v_bad) vs = 0;
+          if (lane == 0) {
+            s_top[w] = make_uint2(top_k, top_v);
+            meta[st].valid[w] = ok ? 1 : 0;
+            meta[st].v_nan[w] = (uint16_t)nans;
+          }
+          if (bar_or(3, 32 * kExpandWarps, !waited)) {
             bad = true;
             break;
           }
-        } else {
-          bar_sync(3, 32 * kExpandWarps);
-        }
+          const bool no_page = bar_or(3, 32 * kExpandWarps, !ok), any_nan = bar_or(3, 32 * kExpandWarps, nans != 0);
 #pragma unroll
-        for (int i = 0; i < kExpandWarps; ++i) top_k = max(top_k, s_top[i].x);
-        uint32_t tv_all = top_v;
-#pragma unroll
-        for (int i = 0; i < kExpandWarps; ++i) tv_all = max(tv_all, s_top[i].y);
-        // a larger exponent than all before moves the reference, by three more
-        const int ek = exponent(top_k), ev = exponent(tv_all), v_old = v_ref;
-        if (ek > k_ref) k_ref = min(ek + 3, 127);
-        if (ev > v_ref) v_ref = min(ev + 3, 127);
-        const float fk = pow2(11 - k_ref), fv = pow2(11 - v_ref);
-        if (lane == 0) {
-          Meta& mt = meta[st];
-          if (w == 0) {
-            mt.k_unit = pow2(k_ref - 11), mt.v_unit = pow2(v_ref - 11);
-            mt.v_step = v_old == v_ref ? 1.0f : exp2f((float)(v_old - v_ref));
+          for (int i = 0; i < kExpandWarps; ++i) top_k = max(top_k, s_top[i].x), top_v = max(top_v, s_top[i].y);
+          // a larger exponent than all before moves the reference, by three more
+          const int ek = exponent(min(top_k, 0x7f7fffffu)), ev = exponent(min(top_v, 0x7f7fffffu)), v_old = v_ref;
+          if (ek > k_ref) k_ref = min(ek + 3, 127);
+          if (ev > v_ref) v_ref = min(ev + 3, 127);
+          fk = pow2(11 - k_ref), fv = pow2(11 - v_ref);
+          k_lim = k_ref >= 127 ? 3.0e38f : pow2(k_ref + 1) * 0.99f, v_lim = v_ref >= 127 ? 3.0e38f : pow2(v_ref + 1) * 0.99f;
+          if (w == 0 && lane == 0) {
+            meta[st].v_step = v_old == v_ref ? 1.0f : exp2f((float)(v_old - v_ref));
+            meta[st].rare = (no_page ? 1u : 0u) | (any_nan ? 2u : 0u);
           }
-          mt.valid[w] = ok ? 1 : 0;
-          mt.v_nan[w] = (uint16_t)nans;
+          bar_sync(3, 32 * kExpandWarps);  // s_top is read
+        } else if (w == 0 && lane == 0) {
+          meta[st].v_step = 1.0f, meta[st].rare = 0;
         }
+        if (w == 0 && lane == 0) meta[st].k_unit = pow2(k_ref - 11), meta[st].v_unit = pow2(v_ref - 11);
         unsigned char* stage = sm + 2 * st * TILE;
         constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
 #pragma unroll
@@ -521,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
       if (!walk.piece(a)) continue;
       const int both = walk.rows_here() > 128 ? 2 : 1;
       for (int x = 0; x < both && !bad; ++x) {
-        if (!mbar_wait_warp(&q_full[x], ph_q[x], kWaitCycles)) bad = true;
+        if (!mbar_wait_warp(&q_full[x], ph_q[x])) bad = true;
         ph_q[x] ^= 1;
       }
-      if (!bad && !mbar_wait_warp(&kv_full[kt & 1], (kt >> 1) & 1, kWaitCycles)) bad = true;
+      if (!bad && !mbar_wait_warp(&kv_full[kt & 1], (kt >> 1) & 1)) bad = true;
       if (bad) break;
       fence_after();
       if (elect_one()) {
@@ -535,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
       for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
         const bool more = t + 1 < walk.t1;
         for (int x = 0; x < both; ++x) {
-          if (!mbar_wait_warp(&p_full[x], ph_p[x], kWaitCycles) ||
-              (x == 0 && more && !mbar_wait_warp(&kv_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, kWaitCycles))) {
+          if (!mbar_wait_warp(&p_full[x], ph_p[x]) ||
+              (x == 0 && more && !mbar_wait_warp(&kv_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1))) {
             bad = true;
             break;
           }
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } while (!bad && walk.next(a));
     if (elect_one()) mma_commit(&drain);  // every product issued has finished before TMEM is released
     __syncwarp();
-    mbar_wait_warp(&drain, 0, kWaitCycles);
+    mbar_wait_warp(&drain, 0);
     }
   }
   if (sync_tc_any(bad) && tid == 0) set_status(a.status, kStatusWaitTimeout | (GDN_K_ATTENTION << 8));

@@ -99,7 +99,6 @@ struct Stream {
     tc::bulk_load(slot + scale_at, scales + (int64_t)g0 * kGroupBytes, ng * kGroupBytes, full);
   }
 };
-constexpr int64_t kWaitCycles = 4000000000ll;  // about two seconds
 constexpr int kSms = 148;
 
 // ------------------------------------------------------------------ few rows
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                 on ? f[t][pt][2 * j + 1] : 0u);
           }
     }
-    if (!tc::mbar_wait_warp(&s_full[warp][slot_i], phase, kWaitCycles)) {
+    if (!tc::mbar_wait_warp(&s_full[warp][slot_i], phase)) {
       set_status(status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
       break;
     }
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   // (after a wait that ran out) every copy has landed before the rings take the sums
   for (int i = 0; i < kSmallSlots; ++i) {
     const int mine = first < L.blocks ? (L.blocks - first + step - 1) / step : 0, uses = (mine - i + kSmallSlots - 1) / kSmallSlots;
-    if (uses > 0) tc::mbar_wait_warp(&s_full[warp][i], (uses & 1) ^ 1, kWaitCycles / 100);
+    if (uses > 0) tc::mbar_wait_warp(&s_full[warp][i], (uses & 1) ^ 1, tc::kWaitTries / 64);
   }
   __syncthreads();
 
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     for (int j = 0; piece(j, p) && !bad; ++j) {
       const unsigned char* src = a.xh + ((int64_t)p.k0 * a.mp + (p.tile % mt) * a.tn) * 128;
       for (int kb = p.k0; kb < p.k1; ++kb, ++i, src += (int64_t)a.mp * 128) {
-        if (i >= stages && !mbar_wait_warp(&empty[s], phase, kWaitCycles)) {
+        if (i >= stages && !mbar_wait_warp(&empty[s], phase)) {
           bad = true;
           break;
         }
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       }
     }
     if (bad)  // let the copies already issued land before the block exits
-      for (int j = max(0, i - stages); j < i; ++j) mbar_wait_warp(&full[j % stages], (j / stages) & 1, kWaitCycles / 100);
+      for (int j = max(0, i - stages); j < i; ++j) mbar_wait_warp(&full[j % stages], (j / stages) & 1, tc::kWaitTries / 64);
   } else if (warp == 1) {
     const uint32_t id = idesc_f16(kTile, a.tn, false, false);
     const uint64_t dw = desc_kmaj(smem_u32(sm), kTile, 0), dx = desc_kmaj(smem_u32(sm) + kWStage, a.tn, 0);
@@ -497,14 +496,14 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     uint32_t phase = 0;
     for (int j = 0; piece(j, p) && !bad; ++j) {
       const int ab = j & 1;
-      if (j >= 2 && !mbar_wait_warp(&acc_empty[ab], ((j >> 1) & 1) ^ 1, kWaitCycles)) {
+      if (j >= 2 && !mbar_wait_warp(&acc_empty[ab], ((j >> 1) & 1) ^ 1)) {
         bad = true;
         break;
       }
       fence_after();
       const uint32_t d = tbase + 256 * ab;
       for (int kb = p.k0; kb < p.k1; ++kb) {
-        if (!mbar_wait_warp(&full[s], phase, kWaitCycles)) {
+        if (!mbar_wait_warp(&full[s], phase)) {
           bad = true;
           break;
         }
@@ -523,14 +522,14 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     // every product issued has finished before TMEM is released
     if (elect_one()) mma_commit(&drain);
     __syncwarp();
-    mbar_wait_warp(&drain, 0, kWaitCycles);
+    mbar_wait_warp(&drain, 0);
   } else if (warp == 6) {
     int i = 0, c = 0;
     uint32_t phase = 1;
     for (int j = 0; piece(j, p) && !bad; ++j) {
       const Stream stream(a.packed, a.L, p.tile / mt, a.lg_group);
       for (int k0 = p.k0; k0 < p.k1; k0 += kBigB, ++i) {
-        if (i >= slots && !mbar_wait_warp(&free_c[c], phase, kWaitCycles)) {
+        if (i >= slots && !mbar_wait_warp(&free_c[c], phase)) {
           bad = true;
           break;
         }
@@ -540,7 +539,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       }
     }
     if (bad)  // let the copies already issued land before the block exits
-      for (int j = max(0, i - slots); j < i; ++j) mbar_wait_warp(&full_c[j % slots], (j / slots) & 1, kWaitCycles / 100);
+      for (int j = max(0, i - slots); j < i; ++j) mbar_wait_warp(&full_c[j % slots], (j / slots) & 1, tc::kWaitTries / 64);
   } else if (warp >= 7) {
     const int strip = (warp - 7) & 7, grp = (warp - 7) >> 3, r = lane >> 2, q = lane & 3;
     const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off) + strip * kStrip + r;
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         uint32_t re = round;
         if (se >= stages) se -= stages, ++re;
         if (!group_wait(2 + grp, 32 * kStrips, strip == 0, &full_c[c], slot_phase, here && re > 0 ? &empty[se] : nullptr,
-                        (re & 1) ^ 1, kWaitCycles)) {
+                        (re & 1) ^ 1)) {
           bad = true;
           break;
         }
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       const int ab = j & 1, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
       const bool split = p.k1 - p.k0 < a.L.blocks;
       const float wf = n < a.N ? 1.0f / __ldg(row_inv + n) : 0.0f;
-      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0, kWaitCycles)) {  // the four warps leave together
+      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0)) {  // the four warps leave together
         bad = true;
         break;
       }

@@ -180,16 +180,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, uint64_t
   }
 }
 
-// The wait of a whole warp, all lanes together, with the limit in SM clock cycles: true for all lanes or for none.  A
-// converged warp is suspended in the instruction until the phase ends (about 110 cycles from the arrival, 3900 cycles at
-// most); a lane that polls alone is not, and its polls take the issue slots of the warps that work.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int64_t limit) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(m, parity))) return true;
-  const int64_t t0 = clock64();
-  while (true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(m, parity))) return true;
-    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) return false;
-  }
+// The wait of a whole warp, all lanes together: true for all lanes or for none.  A converged warp is suspended in the
+// instruction until the phase ends (about 110 cycles from the arrival) or something else arrives, 3900 cycles at most; a
+// lane that polls alone is not, and its polls take the issue slots of the warps that work.  For the same reason the limit
+// counts tries, the loop's cheapest measure: 20 to 3900 cycles each, so kWaitTries are 50 ms at least, some seconds at most.
+constexpr int kWaitTries = 1 << 22;
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int tries = kWaitTries) {
+  bool ok = mbar_try_wait(m, parity);
+  while (!ok && --tries > 0) ok = mbar_try_wait(m, parity);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // A named barrier of n threads: whether any of them passed true.
@@ -206,10 +205,9 @@ __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync
 // A group of warps (n threads, barrier id) waits for up to two mbarriers: one warp polls, the others wait at the barrier.
 // An arrival at any mbarrier wakes every warp that polls one; with 20 of them polling, their tries took more issue
 // slots than the work (the 4-bit product of 2048 rows).  True for all threads or for none.
-__device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* m0, uint32_t p0, uint64_t* m1, uint32_t p1,
-                                           int64_t limit) {
+__device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* m0, uint32_t p0, uint64_t* m1, uint32_t p1) {
   bool ok = true;
-  if (polls) ok = mbar_wait_warp(m0, p0, limit) && (!m1 || mbar_wait_warp(m1, p1, limit));
+  if (polls) ok = mbar_wait_warp(m0, p0) && (!m1 || mbar_wait_warp(m1, p1));
   return !bar_or(id, n, !ok);
 }
 
