@@ -121,14 +121,21 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Channels 2i, 2i + 1 of a word as bf16: 128 + code, or code - 8 for fp32 io.  The mask and the exponent sit in registers
+// whose values the compiler does not know (a kernel argument that is 0 is in them), so that one instruction takes both.
 template <bool F32>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {  // channels 2i, 2i + 1 of a word
-  const uint32_t c = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  if constexpr (!F32) return c;
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x43084308u));
-  return r;
-}
+struct CodePair {
+  uint32_t mask, magic;
+  __device__ __forceinline__ explicit CodePair(uint32_t zero) : mask(0x000f000fu + zero), magic(0x43004300u + zero) {}
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, int i) const {
+    uint32_t c;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(c) : "r"(w >> (4 * i)), "r"(mask), "r"(magic));  // (w & mask) | magic
+    if constexpr (!F32) return c;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x43084308u));
+    return r;
+  }
+};
 
 __device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {  // C = 0
@@ -145,8 +152,9 @@ constexpr int kRedLd = kTile + 4;                                            // 
 template <typename T, int MT, int G>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     linear_small_kernel(const T* __restrict__ x, int M, int K, const unsigned char* __restrict__ packed, Q4Layout L,
-                        int N, T* __restrict__ y, int S, int32_t* status) {
+                        int N, T* __restrict__ y, int S, int32_t* status, uint32_t zero) {
   constexpr bool F32 = sizeof(T) == 4;
+  const CodePair<F32> code_pair(zero);
   constexpr int P = F32 ? 3 : 1;                 // bf16 parts of x
   constexpr int SUB = G == 32 ? 2 : 1;           // groups of a block
   constexpr int LG = G == 32 ? 5 : G == 64 ? 6 : 7;
@@ -238,8 +246,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       uint32_t a[8][2];  // pairs of the lane's 16 channels, rows r and r + 8
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        a[j][0] = code_pair<F32>(w[j >> 2], j & 3);
-        a[j][1] = code_pair<F32>(w[2 + (j >> 2)], j & 3);
+        a[j][0] = code_pair(w[j >> 2], j & 3);
+        a[j][1] = code_pair(w[2 + (j >> 2)], j & 3);
       }
 #pragma unroll
       for (int g = 0; g < SUB; ++g) {
@@ -352,6 +360,7 @@ struct BigArgs {
   __nv_bfloat16* y;
   int32_t M, N, mp, tn, lg_group, full, S;  // rounds of whole tiles; slices of a tile of the last round
   int32_t* status;
+  uint32_t zero;  // 0, unknown to the compiler
 };
 
 // one block a row of x: fp16 scaled to below 2^11, into the layout of the products' operand
@@ -397,24 +406,31 @@ __global__ void __launch_bounds__(256) x_half_kernel(const __nv_bfloat16* __rest
   }
 }
 
-// codes of a word -> eight fp16 weights s code + b (one rounding).  Nibbles 0, 2 (and 4, 6) are masked into 1024 + c,
-// nibbles 1, 3 into 1024 + 16 c, which saves their shift.
-__device__ __forceinline__ uint4 expand(uint32_t w, __half2 s, __half2 b) {
-  uint32_t o[4];
-  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k16 = __half2half2(__ushort_as_half(0x2c00)),
-                k64 = __half2half2(__ushort_as_half(0xd400));  // 1024, 1/16, -64
+// Codes of a word -> eight fp16 weights s code + b (one rounding).  Nibbles 0, 2 (and 4, 6) are masked into 1024 + c,
+// nibbles 1, 3 into 1024 + 16 c, which saves their shift; masks and exponent as in CodePair.
+struct Expand {
+  uint32_t lo, hi, magic;
+  __device__ __forceinline__ explicit Expand(uint32_t zero)
+      : lo(0x000f000fu + zero), hi(0x00f000f0u + zero), magic(0x64006400u + zero) {}
+  __device__ __forceinline__ uint4 operator()(uint32_t w, __half2 s, __half2 b) const {
+    uint32_t o[4];
+    const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k16 = __half2half2(__ushort_as_half(0x2c00)),
+                  k64 = __half2half2(__ushort_as_half(0xd400));  // 1024, 1/16, -64
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 cl = __hsub2(*reinterpret_cast<const __half2*>(&lo), k1024);
-    const __half2 ch = __hfma2(*reinterpret_cast<const __half2*>(&hi), k16, k64);
-    const __half2 wl = __hfma2(cl, s, b), wh = __hfma2(ch, s, b);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&wl);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&wh);
-    w >>= 8;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x, y;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(lo), "r"(magic));
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "r"(hi), "r"(magic));
+      const __half2 cl = __hsub2(*reinterpret_cast<const __half2*>(&x), k1024);
+      const __half2 ch = __hfma2(*reinterpret_cast<const __half2*>(&y), k16, k64);
+      const __half2 wl = __hfma2(cl, s, b), wh = __hfma2(ch, s, b);
+      o[2 * i] = *reinterpret_cast<const uint32_t*>(&wl);
+      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&wh);
+      w >>= 8;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
+};
 
 __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid_constant__ BigArgs a) {
   using namespace tc;
@@ -541,6 +557,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     if (bad)  // let the copies already issued land before the block exits
       for (int j = max(0, i - slots); j < i; ++j) mbar_wait_warp(&full_c[j % slots], (j / slots) & 1, tc::kWaitTries / 64);
   } else if (warp >= 7) {
+    const Expand expand(a.zero);
     const int strip = (warp - 7) & 7, grp = (warp - 7) >> 3, r = lane >> 2, q = lane & 3;
     const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off) + strip * kStrip + r;
     const unsigned char* code_at = chunks + grp * kBlockBytes + strip * 512 + lane * 16;
@@ -706,7 +723,7 @@ cudaError_t run_small(const T* x, int32_t M, int32_t K, const unsigned char* pac
   cudaError_t e = cudaFuncSetAttribute(linear_small_kernel<T, MT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
   if (e != cudaSuccess) return e;
   LaunchScope scope(GDN_K_LINEAR_Q4, stream);
-  return cudaLaunchKernelEx(&cfg, linear_small_kernel<T, MT, G>, x, M, K, packed, L, N, y, S, status);
+  return cudaLaunchKernelEx(&cfg, linear_small_kernel<T, MT, G>, x, M, K, packed, L, N, y, S, status, 0u);
 }
 template <typename T, int MT>
 cudaError_t run_small_g(const T* x, int32_t M, int32_t K, const unsigned char* packed, const Q4Layout& L, int32_t N,
@@ -785,7 +802,7 @@ cudaError_t launch_linear_q4(bool bf16, const void* x, int32_t M, int32_t K, con
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(linear_big_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBigSmem)) != cudaSuccess) return e;
   const BigArgs a{w, L, xh, xf, (float*)(xh + bw.part), count, (__nv_bfloat16*)y, M, N, b.mp, b.tn,
-                  group == 32 ? 5 : group == 64 ? 6 : 7, b.full, b.S, status};
+                  group == 32 ? 5 : group == 64 ? 6 : 7, b.full, b.S, status, 0};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)b.grid);
   cfg.blockDim = dim3(kBigThreads);
