@@ -436,3 +436,131 @@ def test_outputs_past_the_last_token_are_left_alone():
     gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, big_o, big_l, ws)
     c.check(big_o[:c.T], big_l[:c.T])
     assert (big_o[c.T:] == 7.0).all() and (big_l[c.T:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------- the long row tiles (bf16, D up to 128)
+@pytest.mark.parametrize("d,hq,hkv,page", [(64, 4, 2, 32), (128, 6, 2, 64)])
+def test_long_tiles_masked_nan_values_reach_only_their_readers(d, hq, hkv, page):
+    """A token whose value is NaN is seen by the queries from its position on and by no other."""
+    new, ctx, at = 90, 37, 80
+    c = Case([new], [ctx], hq, hkv, d, page, "bf16", seed=31)
+    c.v[0][at, 0, 5] = math.nan  # the whole group stands for NaN
+    c.fill()
+    o, lse = c.attention()
+    group = hq // hkv
+    sees = torch.arange(new) + ctx >= at
+    assert torch.isnan(o[sees.cuda(), :group]).all()
+    assert torch.isfinite(o[~sees.cuda()]).all() and torch.isfinite(o[:, group:]).all() and torch.isfinite(lse).all()
+    # the others are what they are without it
+    clean = Case([new], [ctx], hq, hkv, d, page, "bf16", seed=31).fill()
+    o2, l2 = clean.attention()
+    assert torch.equal(o[~sees.cuda()], o2[~sees.cuda()]) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("k_scale,v_scale,q_scale", [(1e5, 1e-6, 1e-5), (1e-8, 3e6, 1e7), (1e-20, 1e-20, 1.0), (3e4, 1e30, 1e-4)])
+def test_long_tiles_magnitudes_past_fp16(k_scale, v_scale, q_scale):
+    """Keys, values and queries far outside fp16's range: powers of two over the operands keep them."""
+    c = Case([70, 3], [200, 500], 4, 2, 128, 32, "bf16", seed=32)
+    c.k = [(t.float() * k_scale).bfloat16() for t in c.k]
+    c.v = [(t.float() * v_scale).bfloat16() for t in c.v]
+    c.q = (c.q.float() * q_scale).bfloat16()
+    c.d_q = c.q.cuda()
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+def test_long_tiles_values_that_grow_along_the_context():
+    """Each 128 tokens ten times the last: the references of keys and values move while rows run."""
+    c = Case([80], [1000], 2, 1, 128, 64, "bf16", seed=33, outlier=False)
+    grow = 10.0 ** (torch.arange(1080) // 128).float()[:, None, None]
+    c.v = [(c.v[0].float() * grow * 1e-4).bfloat16()]
+    c.k = [(c.k[0].float() * (1 + torch.arange(1080).float()[:, None, None] / 300)).bfloat16()]
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 2.0])
+def test_long_tiles_other_scales(scale):
+    c = Case([66], [300], 2, 2, 64, 16, "bf16", seed=34, outlier=False)
+    c.cfg = gdn.make_attn_config(2, 2, 64, page_size=16, softmax_scale=scale)
+    c.scale = scale
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+def test_long_tiles_batches_of_many_and_empty_sequences():
+    """More groups than blocks, groups cut between blocks, sequences without new tokens, one that sees nothing."""
+    new = [0, 70, 1, 65, 0, 260, 3, 128, 129] * 3
+    ctx = [5, 0, 100, 64, 0, 300, 40, 1, 0] * 3
+    c = Case(new, ctx, 4, 4, 64, 16, "bf16", seed=35).fill()
+    c.d_lens[2] = 0
+    o, lse = c.attention()
+    a = int(c.cu[2])
+    assert (o[a] == 0).all() and (lse[a] == -math.inf).all()
+    c.check(o, lse, skip=(2,))
+    assert torch.equal(o, c.attention()[0])
+
+
+def test_long_tiles_captured_and_on_two_streams():
+    cases = [Case([300, 17], [100, 900], 6, 2, 128, 64, "bf16", seed=s).fill() for s in (41, 42)]
+    want = [c.attention() for c in cases]
+    outs = [c.outputs() for c in cases]
+    graphs = []
+    for c, (o, l, ws) in zip(cases, outs):
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=st):
+            gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, o, l, ws)
+        graphs.append((g, st))
+    for _ in range(4):
+        for (o, l, ws) in outs:
+            o.fill_(0)
+        torch.cuda.synchronize()
+        for g, st in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, l, ws), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_attention_many_sequences():
+    """More sequences than a block has threads, with and without new tokens."""
+    n = 700
+    new = [i % 3 == 0 for i in range(n)]
+    c = Case([int(x) for x in new], [1 + (7 * i) % 50 for i in range(n)], 2, 1, 64, 16, "bf16", seed=36).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    c = Case([66] + [int(x) for x in new], [3] + [1 + (7 * i) % 50 for i in range(n)], 2, 1, 64, 16, "bf16", seed=37).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1184, 2368, 4736, 4737])
+def test_rope_at_the_steps_of_its_block_size(io, T):
+    """Tokens a block change with T; in place, odd pair counts and a ragged last block."""
+    g = torch.Generator().manual_seed(T)
+    for H, D, rot in ((3, 64, 64), (5, 80, 60)):
+        x = torch.randn(T, H, D, generator=g).to(DT[io])
+        pos = torch.randint(0, 300000, (T,), generator=g, dtype=torch.int32)
+        plan = gdn.rope_plan(rot, 1e6)
+        f, ax = frequencies(rot, 1e6, None, "sections")
+        ref = rotate64(x, cos_sin(pos.view(1, -1).numpy(), f, ax))
+        out = x.cuda()
+        gdn.rope(plan, out, pos.cuda(), out)
+        mag = torch.cat((x.double().abs()[..., :rot // 2] + x.double().abs()[..., rot // 2:rot],) * 2 + (x.double().abs()[..., rot:],), -1)
+        assert ((out.cpu().double() - ref).abs() <= U[io] * ref.abs() + 6 * 2.0 ** -24 * mag).all()
+
+
+@pytest.mark.parametrize("n", [1000, 1100])
+def test_append_many_sequences(n):
+    """Sequences are found by a look at all of them, or by bisection where there are more than 1024."""
+    c = Case([i % 2 for i in range(n)], [3 + i % 7 for i in range(n)], 1, 1, 64, 16, "bf16", seed=38)
+    k, v = torch.randn(c.T, 1, 64).bfloat16().cuda(), torch.randn(c.T, 1, 64).bfloat16().cuda()
+    gdn.kv_append(c.cfg, None, None, k, v, None, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, None)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, ko, vo)
+    assert torch.equal(vo.cpu(), quantise(v.cpu(), 64)[3].bfloat16()) and torch.equal(ko.cpu(), quantise(k.cpu(), 64)[3].bfloat16())

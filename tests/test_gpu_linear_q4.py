@@ -160,3 +160,85 @@ def test_layer_decode_steps_together():
             assert ((o[n:n + 1].cpu().double() - want).abs() <= tol).all()
         ref, mag, _ = product(o.view(N, -1).cpu(), co, so, bo, 128)
         assert ((y.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+@pytest.mark.parametrize("w_scale,x_scale", [(1e-9, 1e6), (1e8, 1e-8), (1.0, 1e35), (1e30, 1e-30)])
+def test_linear_q4_magnitudes_past_fp16(M, w_scale, x_scale):
+    """Weights and rows of x far outside fp16's range, and rows of one call that differ by 2^40."""
+    N, K, group = 150, 200, 64
+    g = torch.Generator().manual_seed(7)
+    G = -(-K // group)
+    code = torch.randint(0, 16, (N, G * group), generator=g, dtype=torch.uint8)
+    scale = ((0.5 + torch.rand(N, G, generator=g)) * 0.05 * w_scale).bfloat16()
+    bias = (scale.float() * (-7.5 + torch.randn(N, G, generator=g))).bfloat16()
+    scale[::3] *= 2.0 ** -40
+    bias[::3] *= 2.0 ** -40
+    w = gdn.q4_pack((code[:, 0::2] | (code[:, 1::2] << 4)).cuda(), scale.cuda(), bias.cuda(), K, group)
+    x = torch.randn(M, K, generator=g) * x_scale
+    x[1::2] *= 2.0 ** -40
+    x = x.bfloat16()
+    y = run(x.cuda(), w)
+    code, s, b = code[:, :K].double(), scale.double(), bias.double()
+    ref, mag, _ = product(x, code, s, b, group)
+    tol = 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag
+    if M > 16:
+        se, be = (t.repeat_interleave(group, 1)[:, :K] for t in (s, b))
+        w64 = (se * code + be).abs().t()
+        tol += 2.0 ** -11 * (x.double().abs() @ w64) + 2.0 ** -35 * x.double().abs().amax(1, keepdim=True) * w64.sum(0)
+    assert ((y.cpu().double() - ref).abs() <= tol + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("M,N,K,group", [(40, 20000, 128, 32), (2000, 2100, 192, 64), (17, 8, 8, 128), (700, 1300, 1024, 128)])
+def test_linear_q4_rounds_and_slices(M, N, K, group):
+    """Whole rounds of tiles and a last one cut along K, for calls that share one workspace."""
+    code, scale, bias, w = weight(N, K, group, M)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).bfloat16()
+    ws = torch.full((gdn.linear_q4_workspace_size(M, N, K, group),), 0xFF, dtype=torch.uint8, device="cuda")
+    y = [torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for t in y:
+        gdn.linear_q4(x.cuda(), w, t, ws)
+    assert torch.equal(y[0], y[1])
+    ref, mag, _ = product(x, code, scale, bias, group)
+    se, be = (t.repeat_interleave(group, 1)[:, :K] for t in (scale, bias))
+    w64 = (se * code + be).abs().t()
+    tol = 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag + 2.0 ** -11 * (x.double().abs() @ w64)
+    tol += 2.0 ** -35 * x.double().abs().amax(1, keepdim=True) * w64.sum(0)
+    assert ((y[0].cpu().double() - ref).abs() <= tol).all()
+
+
+def test_linear_q4_many_rows_on_two_streams_and_captured():
+    _, _, _, w = weight(700, 512, 64, 8)
+    xs = [torch.randn(90, 512, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(2)]
+    want = [run(x, w) for x in xs]
+    ys = [torch.empty_like(t) for t in want]
+    ws = [torch.empty(gdn.linear_q4_workspace_size(90, 700, 512, 64), dtype=torch.uint8, device="cuda") for _ in xs]
+    graphs = []
+    for x, y, s in zip(xs, ys, ws):
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=st):
+            gdn.linear_q4(x, w, y, s)
+        graphs.append((g, st))
+    for _ in range(5):
+        for y in ys:
+            y.fill_(0)
+        torch.cuda.synchronize()
+        for g, st in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, t) for y, t in zip(ys, want))
+
+
+def test_linear_q4_weights_that_are_not_finite_stay_in_their_column():
+    for M in (2, 40):
+        code, scale, bias, w = weight(130, 128, 64, 9)
+        x = torch.randn(M, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
+        clean = run(x.cuda(), w)
+        scale = scale.float().bfloat16()
+        scale[77, 1] = float("nan")
+        packed = gdn.q4_pack((code.to(torch.uint8)[:, 0::2] | (code.to(torch.uint8)[:, 1::2] << 4)).cuda(), scale.cuda(),
+                             bias.bfloat16().cuda(), 128, 64)
+        y = run(x.cuda(), packed)
+        keep = torch.arange(130) != 77
+        assert torch.isnan(y[:, 77]).all() and torch.equal(y[:, keep.cuda()], clean[:, keep.cuda()])
