@@ -4,7 +4,7 @@
 //
 // The codes go to the tensor cores as they are, as small integers, and the
 // scales and biases of their groups are applied outside the products:
-//   q . k_t = sum_g s_tg (q_g . c_tg) + b_tg sum(q_g),
+//   q . k_t = sum_g s_tg (q_g . (c_tg - 8)) + (b_tg + 8 s_tg) sum(q_g),
 //   o = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (b_t + 8 s_t),
 // so that nothing is rounded but p_t s_t, which goes in two bf16 parts (three
 // for fp32 io, whose queries go in three as well).  A 4-bit code becomes a bf16
@@ -38,19 +38,17 @@ constexpr int smem_bytes(int D, int RT, int TQ) {
   return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, RT, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
-// Two codes (bits 0-3 and 16-19) as bf16: 128 + code, or code - 8.  The mask and the exponent sit in registers whose
-// values the compiler does not know (a kernel argument that is 0 is in them), so that one instruction takes both.
+// Two codes (bits 0-3 and 16-19) as bf16 code - 8.  The mask and the exponent sit in registers whose values the compiler
+// does not know (a kernel argument that is 0 is in them), so that one instruction takes both.  (128 + code as it is, with
+// the 128 taken out of the sums, is no faster, and costs the log of the sum three bits.)
 struct Codes {
   uint32_t mask, magic;
   __device__ __forceinline__ explicit Codes(uint32_t zero) : mask(0x000f000fu + zero), magic(0x43004300u + zero) {}
-  __device__ __forceinline__ uint32_t c128(uint32_t w) const {
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));  // (w & mask) | magic
-    return r;
-  }
-  __device__ __forceinline__ uint32_t c8(uint32_t w) const {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c128(w)), "r"(0x43084308u));
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, %2, %3, 0xEA;\nsub.rn.bf16x2 %0, t, %4;\n}\n"  // ((w & mask) | magic) - 136
+        : "=r"(r)
+        : "r"(w), "r"(mask), "r"(magic), "r"(0x43084308u));
     return r;
   }
 };
@@ -212,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
     if constexpr (QS) __syncthreads();
 
     float o[NR][CB][4][4];                   // [channels 8r + 2j, + 1 of each 64][two channels x two rows]
-    float rs[NR][F32 ? 1 : GV][4];           // sums of the rounded p_t s_t: bf16 io carries the codes as 128 + c
     float mx[NR][2], l[NR][2], ob[NR][2][GV];
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
@@ -228,8 +225,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[k][cb][j][e] = 0.0f;
-#pragma unroll
-        for (int g = 0; g < (F32 ? 1 : GV); ++g) rs[k][g][e] = 0.0f;
       }
     }
 
@@ -273,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
-            c0[i] = F32 ? codes.c8(w >> sh) : codes.c128(w >> sh);
-            c1[i] = F32 ? codes.c8(w >> (sh + 4)) : codes.c128(w >> (sh + 4));
+            c0[i] = codes(w >> sh);
+            c1[i] = codes(w >> (sh + 4));
           }
 #pragma unroll
           for (int term = 0; term < TQ; ++term) {
@@ -296,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t w = scales[g * kKvTile + 8 * i];
-          const float sk = lo_bf16(w), z = fmaf(F32 ? 8.0f : -128.0f, sk, hi_bf16(w));
+          const float sk = lo_bf16(w), z = fmaf(8.0f, sk, hi_bf16(w));
 #pragma unroll
           for (int k = 0; k < NR; ++k)
 #pragma unroll
@@ -341,8 +336,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
             for (int g = 0; g < GV; ++g) ob[k][e][g] *= f;
 #pragma unroll
-            for (int g = 0; g < (F32 ? 1 : GV); ++g) rs[k][g][e] *= f;
-#pragma unroll
             for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
               for (int x = 0; x < 4; ++x) o[k][cb][x][e] *= f, o[k][cb][x][2 + e] *= f;
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
         for (int i = 0; i < 2; ++i) {
           const uint32_t w = scales[(GK + gv) * kKvTile + 8 * i];
           sv[i] = lo_bf16(w);
-          bv[i] = F32 ? fmaf(8.0f, sv[i], hi_bf16(w)) : hi_bf16(w);
+          bv[i] = fmaf(8.0f, sv[i], hi_bf16(w));
         }
         uint32_t f[NR][TP][2];
 #pragma unroll
@@ -392,13 +385,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
               x[0] -= lo_bf16(w), x[1] -= hi_bf16(w);
             }
           }
-        if constexpr (!F32) {
-#pragma unroll
-          for (int k = 0; k < NR; ++k)
-#pragma unroll
-            for (int tp = 0; tp < TP; ++tp)
-              mma(rs[k][gv], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, f[k][tp][0], f[k][tp][1]);
-        }
 #pragma unroll
         for (int cb = gv * (CB / GV); cb < (gv + 1) * (CB / GV); ++cb) {
           uint32_t w[4];
@@ -414,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
               uint32_t c[4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                c[e] = F32 ? codes.c8(w01 >> (8 * jj + 4 * e)) : codes.c128(w01 >> (8 * jj + 4 * e));
-                c[2 + e] = F32 ? codes.c8(w23 >> (8 * jj + 4 * e)) : codes.c128(w23 >> (8 * jj + 4 * e));
+                c[e] = codes(w01 >> (8 * jj + 4 * e));
+                c[2 + e] = codes(w23 >> (8 * jj + 4 * e));
               }
 #pragma unroll
               for (int k = 0; k < NR; ++k)
@@ -447,10 +433,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
           l[k][e] += __shfl_xor_sync(0xffffffffu, l[k][e], x);
 #pragma unroll
           for (int g = 0; g < GV; ++g) ob[k][e][g] += __shfl_xor_sync(0xffffffffu, ob[k][e][g], x);
-        }
-        if constexpr (!F32) {
-#pragma unroll
-          for (int g = 0; g < GV; ++g) ob[k][e][g] = fmaf(-128.0f, rs[k][g][e], ob[k][e][g]);
         }
         if (r == 0) s_ml[warp][row] = make_float2(mx[k][e], l[k][e]);
 #pragma unroll

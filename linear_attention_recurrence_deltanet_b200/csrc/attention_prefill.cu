@@ -2,13 +2,17 @@
 // prefill; bf16 io, heads of 64 or 128 channels), on tcgen05:
 //   S = Q K^T, P = 2^(S - m) and O = P V on tiles of 128 rows x 128 keys.
 //
-// Operands are fp16.  Codes are expanded to s c + b with a power of two over them
-// that brings the largest value so far of the block's keys (values) below 2^12,
-// and query rows are brought below 2^11 by one of their own (exactly, but for
-// elements 2^-25 of the row's largest): keys, values and probabilities are off by
-// half a step of fp16, 2^-11, against 2^-8 in bf16, at the same rate.  A value
-// group that stands for NaN is expanded as zeros and noted by token, so that it
-// reaches the rows that see it and no other.
+// Operands are fp16, with powers of two over them: query rows are brought below 2^8
+// (exactly, but for elements 2^-22 of the row's largest), keys and values below
+// 2^12 by the largest of the block so far.  Keys go as s (c - 8), which is exact in
+// 11 bits, and the rest, b + 8 s by group, times the sums of the query's groups, as
+// 16 more channels in high and low parts:
+//   q . k_t = sum_g q_g . s_tg (c_tg - 8) + (b_tg + 8 s_tg) sum(q_g),
+// so that scores, and the log of their sum, are those of fp32.  (Keys as s c + b
+// in fp16 put 2^-12 of a score into the log of a short row's sum.)  Values,
+// s c + b, and probabilities are off by half a step of fp16, 2^-11, against 2^-8
+// in bf16, at the same rate.  A value group that stands for NaN is expanded as
+// zeros and noted by token, so that it reaches the rows that see it and no other.
 //
 // A block takes two tiles of 128 query rows (tokens x the heads that share a
 // key/value head) through the same keys.  Warps 0-3 and 4-7 are the softmax of
@@ -39,7 +43,20 @@ __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync
 using Walk = AttnWalk<kRows, kKeys, 3, 6>;     // a group's queries and output cost about three tiles
 
 constexpr int tile_bytes(int D) { return kKeys * D * 2; }
-constexpr int smem_bytes(int D) { return 6 * tile_bytes(D) + 1024 < 120000 ? 120000 : 6 * tile_bytes(D) + 1024; }
+constexpr int kSide = kKeys * 32;  // the 16 more channels of a tile: 32 bytes a row, 32-byte swizzle
+constexpr int smem_bytes(int D) {  // one block an SM, which takes all of its TMEM
+  return 6 * tile_bytes(D) + 4 * kSide + 1024 < 120000 ? 120000 : 6 * tile_bytes(D) + 4 * kSide + 1024;
+}
+// byte offset of eight of a row's 16 more channels, and the descriptor of such a tile (K-major, 8 rows a 256-byte group)
+__device__ __forceinline__ uint32_t side_chunk(int row, int i) { return (uint32_t)(row * 32 + ((i ^ (row >> 2)) & 1) * 16); }
+__device__ __forceinline__ uint64_t desc_side(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | (1ull << 16) | (16ull << 32) | (1ull << 46) | (6ull << 61);
+}
+// x in two halves: its fp16 and the fp16 of the rest
+__device__ __forceinline__ uint32_t high_low(float x) {
+  const __half h = __float2half_rn(x), l = __float2half_rn(x - __half2float(h));
+  return (uint32_t)__half_as_ushort(h) | ((uint32_t)__half_as_ushort(l) << 16);
+}
 
 // what the expanding warps say of a key tile
 struct alignas(16) Meta {
@@ -51,30 +68,35 @@ struct alignas(16) Meta {
   uint16_t v_nan[8];     // by key: its value is NaN
 };
 
-// Eight codes as s c + b, in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
+// Eight codes as values s c + b or keys s (c - 8), in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
 // shift.  The masks sit in registers whose values the compiler does not know (a kernel argument that is 0 is in them),
 // so that one instruction takes a mask and the exponent.
 struct Expand {
   uint32_t lo, hi, magic;
   __device__ __forceinline__ explicit Expand(uint32_t zero)
       : lo(0x000f000fu + zero), hi(0x00f000f0u + zero), magic(0x64006400u + zero) {}
-  __device__ __forceinline__ uint4 operator()(uint32_t w, __half2 s, __half2 b) const {
+  template <typename F>
+  __device__ __forceinline__ uint4 by(uint32_t w, float off, const F& f) const {  // f of the codes less `off`
     uint32_t o[4];
-    const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k16 = __half2half2(__ushort_as_half(0x2c00)),
-                  k64 = __half2half2(__ushort_as_half(0xd400));  // 1024, 1/16, -64
+    const __half2 kl = __float2half2_rn(-1024.0f - off), k16 = __float2half2_rn(0.0625f), kh = __float2half2_rn(-64.0f - off);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t x, y;
       asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(lo), "r"(magic));  // (w & mask) | magic
       asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "r"(hi), "r"(magic));
-      const __half2 cl = __hsub2(*reinterpret_cast<const __half2*>(&x), k1024);
-      const __half2 ch = __hfma2(*reinterpret_cast<const __half2*>(&y), k16, k64);
-      const __half2 wl = __hfma2(cl, s, b), wh = __hfma2(ch, s, b);
+      const __half2 wl = f(__hadd2(*reinterpret_cast<const __half2*>(&x), kl));
+      const __half2 wh = f(__hfma2(*reinterpret_cast<const __half2*>(&y), k16, kh));
       o[2 * i] = *reinterpret_cast<const uint32_t*>(&wl);
       o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&wh);
       w >>= 8;
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  __device__ __forceinline__ uint4 value(uint32_t w, __half2 s, __half2 b) const {
+    return by(w, 0.0f, [&](__half2 c) { return __hfma2(c, s, b); });
+  }
+  __device__ __forceinline__ uint4 key(uint32_t w, __half2 s) const {
+    return by(w, 8.0f, [&](__half2 c) { return __hmul2(c, s); });
   }
 };
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -212,16 +234,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           }
         }
         const int e = exponent(top);
-        unit = pow2(e - 10);
-        const float f = p.scale < 0.0f ? -pow2(10 - e) : pow2(10 - e);
+        unit = pow2(e - 7);
+        const float f = p.scale < 0.0f ? -pow2(7 - e) : pow2(7 - e);
+        float sum[GK];
+#pragma unroll
+        for (int g = 0; g < GK; ++g) sum[g] = 0.0f;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float v[8], z[8];
           Vec16<__nv_bfloat16>::unpack(on ? src[c] : make_uint4(0, 0, 0, 0), v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = v[(j >> 1) + 4 * (j & 1)] * f;  // channels in the order of expand
+          for (int j = 0; j < 8; ++j) z[j] = v[(j >> 1) + 4 * (j & 1)] * f, sum[c / 8] += z[j];  // channels in the order of Expand
           *reinterpret_cast<uint4*>(sq + kmaj_chunk(128, r, c * 8)) = pack8h(z);
         }
+        uint32_t side[4] = {0, 0, 0, 0};  // high, low, high, low by group
+#pragma unroll
+        for (int g = 0; g < GK; ++g) side[2 * g] = side[2 * g + 1] = high_low(sum[g]);
+        unsigned char* row_side = sm + 6 * TILE + x * kSide;
+        *reinterpret_cast<uint4*>(row_side + side_chunk(r, 0)) = make_uint4(side[0], side[1], side[2], side[3]);
+        *reinterpret_cast<uint4*>(row_side + side_chunk(r, 1)) = make_uint4(0, 0, 0, 0);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
@@ -476,19 +507,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         if (w == 0 && lane == 0) meta[st].k_unit = pow2(k_ref - 11), meta[st].v_unit = pow2(v_ref - 11);
         unsigned char* stage = sm + 2 * st * TILE;
         constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
+        uint32_t side[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
-          const __half2 s = __float2half2_rn(lo_bf16(ks[g]) * fk), b = __float2half2_rn(hi_bf16(ks[g]) * fk);
+          const float sk = lo_bf16(ks[g]) * fk;
+          const uint32_t z = high_low(fmaf(8.0f, sk, hi_bf16(ks[g]) * fk));
+          side[2 * g] = __byte_perm(z, z, 0x1010), side[2 * g + 1] = __byte_perm(z, z, 0x3232);  // high, high, low, low
+          const __half2 s = __float2half2_rn(sk);
           const uint32_t c[4] = {kc[g].x, kc[g].y, kc[g].z, kc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_k[j] + g * kBlock64) = expand(c[j], s, b);
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_k[j] + g * kBlock64) = expand.key(c[j], s);
         }
+        *reinterpret_cast<uint4*>(sm + 6 * TILE + (2 + st) * kSide + side_chunk(16 * w + tk, half)) =
+            half ? make_uint4(0, 0, 0, 0) : make_uint4(side[0], side[1], side[2], side[3]);
         const __half2 s = __float2half2_rn(lo_bf16(vs) * fv), b = __float2half2_rn(hi_bf16(vs) * fv);
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
           const uint32_t c[4] = {odd ? vc[g].y : vc[g].x, odd ? vc[g].x : vc[g].y, odd ? vc[g].w : vc[g].z, odd ? vc[g].z : vc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_v[j] + g * kBlock64) = expand(c[j], s, b);
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_v[j] + g * kBlock64) = expand.value(c[j], s, b);
         }
         fence_async_smem();
         bar_sync(3, 32 * kExpandWarps);
@@ -507,12 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     const uint32_t id_s = idesc_f16(128, kKeys, false, false), id_o = idesc_f16(128, D, false, true);
     const uint64_t dq = desc_kmaj(smem_u32(sm), 128, 0), dk = desc_kmaj(smem_u32(sm) + 2 * TILE, kKeys, 0);
     const uint64_t dv = desc_mnmaj(smem_u32(sm) + 3 * TILE, kKeys, 0);
+    const uint64_t dqs = desc_side(smem_u32(sm) + 6 * TILE), dks = desc_side(smem_u32(sm) + 6 * TILE + 2 * kSide);
     auto scores = [&](int x, int st) {
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;  // 64 channels a block of the operands
         mma_f16(tbase + 128 * x, dq + (uint32_t)((x * TILE >> 4) + off), dk + (uint32_t)((2 * st * TILE >> 4) + off), id_s, s > 0);
       }
+      mma_f16(tbase + 128 * x, dqs + (uint32_t)(x * kSide >> 4), dks + (uint32_t)(st * kSide >> 4), id_s, 1u);
       mma_commit(&s_full[x]);
     };
     auto values = [&](int x, int st, bool more) {

@@ -92,20 +92,19 @@ def attention_bound(q, k_parts, v_parts, o, scale, new, io, long=False):
 
     Scores: products of the io type and small integers are exact, sums lose at most 2^-23 of the running magnitude a
     step; a warp's chain of a score has fewer than 8 steps that see the whole sum, so 2^-20 of the sum of magnitudes
-    covers them (offset codes: up to 144 steps of the scale for bf16, 8 for fp32).  A score off by e changes p by a
-    factor within e^{+-2e}.  Probabilities enter the value product in parts that keep 16 bits (bf16 io) or 24, values
-    as codes around 8; sums as for scores.  The output rounds once.
+    (codes around 8, the bias moved there) covers them.  A score off by e changes p by a factor within e^{+-2e}.
+    Probabilities enter the value product in parts that keep 16 bits (bf16 io) or 24, values as codes around 8; sums as
+    for scores.  The output rounds once.
 
-    long: the long row tiles (bf16 io).  Keys, values and probabilities are fp16 operands, half a step 2^-11 each.  Keys
-    and values have their largest so far between 2^8 and 2^12 and queries between 2^10 and 2^11, so that the half step
-    below fp16's normal numbers, 2^-25, is 2^-33 of the largest key and 2^-35 of the row's largest query element; a
-    probability under 2^-14 is off by 2^-25 where the largest is 1 at least."""
+    long: the long row tiles (bf16 io).  Key products are exact in fp16 too; the moved bias and the sums of the query's
+    groups go in two parts of 11 bits each, 2^-22 of either, within the 2^-20.  Keys and values have their largest so far
+    between 2^7 and 2^12 and queries between 2^7 and 2^8, so that the half step below fp16's normal numbers, 2^-25, is
+    2^-32 of the largest key and of the row's largest query element.  Values and probabilities are off by half a step of
+    fp16, 2^-11 each; a probability under 2^-14 is off by 2^-25 where the largest is 1 at least."""
     n, hq, d = q.shape
     (_, ks, kb, _), (_, vs, vb, _) = k_parts, v_parts
     length, hkv = ks.shape[:2]
-    top = 144.0 if io == "bf16" else 8.0
-    kb_m = kb.abs() if io == "bf16" else (kb + 8 * ks).abs()
-    k_mag = (top * ks + kb_m).repeat_interleave(64, -1)
+    k_mag = (8 * ks + (kb + 8 * ks).abs()).repeat_interleave(64, -1)
     v_mag = (8 * vs + (vb + 8 * vs).abs()).amax(-1)  # [length, hkv]
     eo, el = torch.zeros(n, hq, dtype=torch.float64), torch.zeros(n, hq, dtype=torch.float64)
     for i in range(n):
@@ -118,12 +117,11 @@ def attention_bound(q, k_parts, v_parts, o, scale, new, io, long=False):
             ds = abs(scale) * 2.0 ** -20 * (k_mag[:seen, kh] @ qa).max()
             if long:
                 kv = k_parts[3].abs()[:, kh]
-                ds = ds + abs(scale) * ((2.0 ** -11 * (kv[:seen] @ qa)).max() + 2.0 ** -33 * kv.max() * qa.sum()
-                                        + 2.0 ** -35 * qa.max() * kv[:seen].sum(-1).max())
+                ds = ds + abs(scale) * (2.0 ** -32 * kv.max() * qa.sum() + 2.0 ** -32 * qa.max() * kv[:seen].sum(-1).max())
             el[i, h] = ds
             eo[i, h] = (2 * ds + (2.0 ** -16 if io == "bf16" else 2.0 ** -20) + 2.0 ** -20) * v_mag[:seen, kh].max()
             if long:
-                eo[i, h] += (2 * 2.0 ** -11 + 2.0 ** -33 + seen * 2.0 ** -25) * v_mag[:, kh].max()
+                eo[i, h] += (2 * 2.0 ** -11 + 2.0 ** -32 + seen * 2.0 ** -25) * v_mag[:, kh].max()
     return U[io] * o.abs() + eo.unsqueeze(-1), el
 
 
