@@ -102,7 +102,7 @@ struct Stream {
 constexpr int kSms = 148;
 
 // ------------------------------------------------------------------ few rows
-// Up to 8 MT rows of x a block: the codes go to the tensor cores as bf16
+// Eight rows of x a block: the codes go to the tensor cores as bf16
 // integers (A: 16 weight rows, B: 8 rows of x), each group's products are scaled
 // in fp32, so nothing but the sums is rounded.  bf16 io takes 128 + code (one
 // mask a pair), fp32 io code - 8 and three bf16 parts of x.
@@ -149,12 +149,13 @@ constexpr int kSmallSlots = 2, kSmallSlot = kBlockBytes + 2 * kGroupBytes;  // g
 constexpr int kSmallSmem = kSmallWarps * kSmallSlots * kSmallSlot;           // 80 KB: two blocks an SM
 constexpr int kRedLd = kTile + 4;                                            // floats between columns of the join
 
-template <typename T, int MT, int G>
+template <typename T, int G>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     linear_small_kernel(const T* __restrict__ x, int M, int K, const unsigned char* __restrict__ packed, Q4Layout L,
                         int N, T* __restrict__ y, int S, int32_t* status, uint32_t zero) {
   constexpr bool F32 = sizeof(T) == 4;
   const CodePair<F32> code_pair(zero);
+  constexpr int MT = 1;
   constexpr int P = F32 ? 3 : 1;                 // bf16 parts of x
   constexpr int SUB = G == 32 ? 2 : 1;           // groups of a block
   constexpr int LG = G == 32 ? 5 : G == 64 ? 6 : 7;
@@ -324,8 +325,196 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   tc::cluster_sync();  // the leader has read the others' sums
 }
 
+// 9 to 32 rows of bf16 io (8 MT).  A warp takes SPW of the tile's eight strips, so that its sums stay in registers, and
+// every KW-th 64-channel block; the block copies x of KW blocks at a time, in the order of B fragments, some steps ahead
+// (5120 x 6144, 16 rows: 16 us, with x read by each warp 26).
+constexpr int strips_per_warp(int MT) { return MT == 2 ? 8 : 4; }
+constexpr int rows_slots(int MT) { return MT == 2 ? 2 : 4; }
+constexpr int rows_kw(int MT) { return strips_per_warp(MT); }  // eight warps / (8 / SPW)
+constexpr int rows_stages(int MT) { return MT == 2 ? 2 : 3; }
+constexpr int rows_slot_bytes(int MT, int G) { return strips_per_warp(MT) * (512 + 64 * (G == 32 ? 2 : 1)); }
+constexpr int rows_smem(int MT, int G) {
+  const int rings = kSmallWarps * rows_slots(MT) * rows_slot_bytes(MT, G) + rows_stages(MT) * rows_kw(MT) * MT * 1024;
+  const int join = (rows_kw(MT) * MT * 8 * kRedLd + MT * 8 * kTile) * 4;
+  return rings > join ? rings : join;
+}
+constexpr int rows_blocks(int MT, int G) { return 2 * (rows_smem(MT, G) + 2048) <= 232448 && MT == 2 ? 2 : 1; }  // an SM
+
+template <int MT, int G>
+__global__ void __launch_bounds__(kSmallThreads, rows_blocks(MT, G))
+    linear_rows_kernel(const __nv_bfloat16* __restrict__ x, int M, int K, const unsigned char* __restrict__ packed, Q4Layout L,
+                       int N, __nv_bfloat16* __restrict__ y, int S, int32_t* status, uint32_t zero) {
+  constexpr int SPW = strips_per_warp(MT), SG = kStrips / SPW, KW = kSmallWarps / SG, SLOTS = rows_slots(MT);
+  constexpr int SUB = G == 32 ? 2 : 1, LG = G == 32 ? 5 : G == 64 ? 6 : 7;
+  constexpr int STAGES = rows_stages(MT), SLOT = rows_slot_bytes(MT, G), STAGE = KW * MT * 1024;
+  static_assert(KW == rows_kw(MT), "warps");
+  const CodePair<false> code_pair(zero);
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t s_full[kSmallWarps][SLOTS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  const int sg = warp % SG, kw = warp / SG;
+  const int rank = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
+  const int steps = (L.blocks + S * KW - 1) / (S * KW);  // step i: blocks (i S + rank) KW ..
+  if (threadIdx.x < kSmallWarps * SLOTS) tc::mbar_init(&s_full[threadIdx.x / SLOTS][threadIdx.x % SLOTS], 1);
+  tc::mbar_init_fence();
+  __syncthreads();
+
+  unsigned char* ring = smem + warp * SLOTS * SLOT;
+  unsigned char* xs_base = smem + kSmallWarps * SLOTS * SLOT;
+  const unsigned char* codes = packed + (int64_t)tile * L.blocks * kBlockBytes + sg * SPW * 512;
+  const unsigned char* scales = packed + L.scale_off + (int64_t)tile * L.row_groups * kGroupBytes + sg * SPW * 64;
+  auto fetch = [&](int step, int slot) {  // one lane: this warp's strips of its block
+    const int b = (step * S + rank) * KW + kw;
+    if (b >= L.blocks) return;
+    uint64_t* m = &s_full[warp][slot];
+    unsigned char* d = ring + slot * SLOT;
+    tc::mbar_expect_tx(m, SPW * 512 + SUB * SPW * 64);
+    tc::bulk_load(d, codes + (int64_t)b * kBlockBytes, SPW * 512, m);
+#pragma unroll
+    for (int g = 0; g < SUB; ++g)
+      tc::bulk_load(d + SPW * 512 + g * SPW * 64, scales + (int64_t)(((b * kBlock) >> LG) + g) * kGroupBytes, SPW * 64, m);
+  };
+  // x of a step's blocks: chunk c (eight channels) of row m of block k goes to lane (m % 8, c / 2), half c % 2
+  auto copy_x = [&](int step) {
+    if (step < steps)
+      for (int i = threadIdx.x; i < KW * MT * 64; i += kSmallThreads) {
+        const int c = i & 7, m = (i >> 3) % (MT * 8), k = (i >> 3) / (MT * 8);
+        const int ch = ((step * S + rank) * KW + k) * kBlock + c * 8;
+        const bool on = m < M && ch < K;
+        tc::cp_async16(xs_base + (step % STAGES) * STAGE + k * MT * 1024 +
+                           ((((m >> 3) * 2 + (c & 1)) * 32) + (m & 7) * 4 + (c >> 1)) * 16,
+                       on ? x + (int64_t)m * K + ch : x, on ? 16 : 0);
+      }
+    tc::cp_async_commit();
+  };
+  if (lane == 0)
+    for (int i = 0; i < SLOTS && i < steps; ++i) fetch(i, i);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) copy_x(i);
+
+  float acc[SPW][MT][4];
+#pragma unroll
+  for (int i = 0; i < SPW; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.0f;
+
+  int slot_i = 0;
+  uint32_t phase = 0;
+  bool dead = false;
+  for (int step = 0; step < steps; ++step) {
+    tc::cp_async_wait<STAGES - 2>();
+    __syncthreads();  // everybody's copies of this step have landed, and the stage of the last one is read
+    copy_x(step + STAGES - 1);
+    const bool here = (step * S + rank) * KW + kw < L.blocks && !dead;
+    if (here && !tc::mbar_wait_warp(&s_full[warp][slot_i], phase)) {
+      set_status(status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
+      dead = true;
+    }
+    if (here && !dead) {
+      const uint4* xs = reinterpret_cast<const uint4*>(xs_base + (step % STAGES) * STAGE + kw * MT * 1024) + lane;
+      uint32_t f[MT][8];
+      float sum[SUB][MT][4];  // x over the groups, as the product with ones
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint4 v0 = xs[(2 * t) * 32], v1 = xs[(2 * t + 1) * 32];
+        f[t][0] = v0.x, f[t][1] = v0.y, f[t][2] = v0.z, f[t][3] = v0.w;
+        f[t][4] = v1.x, f[t][5] = v1.y, f[t][6] = v1.z, f[t][7] = v1.w;
+#pragma unroll
+        for (int g = 0; g < SUB; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // groups of 32: lanes q < 2 hold the first, q >= 2 the second
+            const bool on = SUB == 1 || (q >> 1) == g;
+            const uint32_t f0 = on ? f[t][2 * j] : 0u, f1 = on ? f[t][2 * j + 1] : 0u;
+            if (j == 0) mma0(sum[g][t], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, f0, f1);
+            else mma(sum[g][t], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, f0, f1);
+          }
+      }
+      const unsigned char* slot = ring + slot_i * SLOT;
+      const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + SPW * 512) + r;
+#pragma unroll
+      for (int i = 0; i < SPW; ++i) {
+        const uint4 cw = *reinterpret_cast<const uint4*>(slot + i * 512 + lane * 16);
+        const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+        uint32_t a[8][2];  // pairs of the lane's 16 channels, rows r and r + 8
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j][0] = code_pair(w[j >> 2], j & 3), a[j][1] = code_pair(w[2 + (j >> 2)], j & 3);
+#pragma unroll
+        for (int g = 0; g < SUB; ++g) {
+          float s[2], z[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sw = sc[g * SPW * 16 + i * kStrip + 8 * h];
+            s[h] = lo_bf16(sw), z[h] = fmaf(-128.0f, s[h], hi_bf16(sw));
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            float p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool on = SUB == 1 || (q >> 1) == g;
+              const uint32_t f0 = on ? f[t][2 * j] : 0u, f1 = on ? f[t][2 * j + 1] : 0u;
+              if (j == 0) mma0(p, a[0][0], a[0][1], a[1][0], a[1][1], f0, f1);
+              else mma(p, a[2 * j][0], a[2 * j][1], a[2 * j + 1][0], a[2 * j + 1][1], f0, f1);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                acc[i][t][2 * h + e] = fmaf(s[h], p[2 * h + e], fmaf(z[h], sum[g][t][e], acc[i][t][2 * h + e]));
+          }
+        }
+      }
+      __syncwarp();  // the slot is read before lane 0 refills it
+    }
+    if (lane == 0 && !dead && step + SLOTS < steps) fetch(step + SLOTS, slot_i);
+    if (++slot_i == SLOTS) slot_i = 0, phase ^= 1;
+  }
+  tc::cp_async_wait<0>();
+  if (dead)  // the copies still in flight land before the block goes on
+    for (int i = 0; i < SLOTS; ++i)
+      for (uint32_t ph = 0; ph < 2; ++ph) tc::mbar_wait_warp(&s_full[warp][i], ph, tc::kWaitTries / 64);
+  __syncthreads();
+
+  float* red = reinterpret_cast<float*>(smem);  // [K part][column of x][row]
+  float* s_sum = red + KW * MT * 8 * kRedLd;
+#pragma unroll
+  for (int i = 0; i < SPW; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(kw * MT * 8 + t * 8 + 2 * q + (e & 1)) * kRedLd + (sg * SPW + i) * kStrip + r + 8 * (e >> 1)] = acc[i][t][e];
+  __syncthreads();
+  auto put = [&](int i, float v) {
+    const int n = tile * kTile + i % kTile;
+    if (n < N) y[(int64_t)(i / kTile) * N + n] = __float2bfloat16_rn(v);
+  };
+  for (int i = threadIdx.x; i < M * kTile; i += kSmallThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += red[(w * MT * 8 + i / kTile) * kRedLd + i % kTile];
+    if (S == 1) put(i, v);
+    else s_sum[i] = v;
+  }
+  if (S == 1) return;
+  tc::cluster_sync();
+  // each block of the cluster adds up its share of the rows
+  for (int i = rank * kSmallThreads + threadIdx.x; i < M * kTile; i += S * kSmallThreads) {
+    float v = 0.0f;
+    for (int o = 0; o < S; ++o) {
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(tc::mapa_shared(tc::smem_u32(&s_sum[i]), o)));
+      v += f;
+    }
+    put(i, v);
+  }
+  tc::cluster_sync();  // the others have read this block's sums
+}
+
 // ------------------------------------------------------------------ many rows
-// Rows past kSmallRows (bf16 io): tcgen05 products of 128 weight rows (A) and
+// More rows (bf16 io): tcgen05 products of 128 weight rows (A) and
 // `tn` rows of x (B), in fp16.  Weights are expanded to fp16 tiles in shared
 // memory by eight warps, one of the tile's 16-row strips each; scaled by a power of two a row (q4_pack) so that
 // the row's largest value is below 2^11, a weight is off by half a step, 2^-11,
@@ -702,35 +891,71 @@ cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* bi
 
 namespace {
 
-constexpr int kSmallFill = 250;
-constexpr int kSmallRows = 16;  // bf16 io: more rows run linear_big_kernel
 
-template <typename T, int MT, int G>
+// bf16 io: whether the products go by linear_rows_kernel.  17 to 32 rows do where the weight is small (1024 x 2048: 5.9
+// against 12 us; 5120 x 6144: 27 us against 22).
+bool few_rows(int32_t M, const Q4Layout& L) { return M <= 16 || (M <= 32 && (int64_t)L.tiles * L.blocks <= 1500); }
+  // bf16 io: more rows run linear_big_kernel
+
+// Blocks a tile: a block for each SM, while every warp keeps two blocks of K.  (Twice as many put 320 blocks of 5120 x
+// 6144 in two rounds: one row 11.9 us against 9.3.)
+int cluster_blocks(int64_t tiles, int blocks, int kw) {
+  int S = 1;
+  while (S < 8 && tiles * S < kSms + 2 && blocks >= 2 * S * kw) S *= 2;
+  return S;
+}
+cudaLaunchConfig_t cluster_config(dim3 grid, int S, int smem, cudaStream_t stream, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = (unsigned)S, at->val.clusterDim.y = 1, at->val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = S > 1 ? 1 : 0;
+  return cfg;
+}
+
+template <typename T, int G>
 cudaError_t run_small(const T* x, int32_t M, int32_t K, const unsigned char* packed, const Q4Layout& L, int32_t N, T* y,
                       int32_t* status, cudaStream_t stream) {
-  const int mg = (M + MT * 8 - 1) / (MT * 8);
-  int S = 1;  // blocks a tile: enough for two an SM, while every warp keeps a block of K
-  while (S < 8 && (int64_t)L.tiles * mg * S < kSmallFill && L.blocks >= 2 * S * kSmallWarps) S *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(L.tiles * S), (unsigned)mg);
-  cfg.blockDim = dim3(kSmallThreads);
-  cfg.dynamicSmemBytes = kSmallSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = S, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-  cfg.attrs = at, cfg.numAttrs = S > 1 ? 1 : 0;
-  cudaError_t e = cudaFuncSetAttribute(linear_small_kernel<T, MT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+  const int mg = (M + 7) / 8, S = cluster_blocks((int64_t)L.tiles * mg, L.blocks, kSmallWarps);
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(L.tiles * S), (unsigned)mg), S, kSmallSmem, stream, &at);
+  cudaError_t e = cudaFuncSetAttribute(linear_small_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
   if (e != cudaSuccess) return e;
   LaunchScope scope(GDN_K_LINEAR_Q4, stream);
-  return cudaLaunchKernelEx(&cfg, linear_small_kernel<T, MT, G>, x, M, K, packed, L, N, y, S, status, 0u);
+  return cudaLaunchKernelEx(&cfg, linear_small_kernel<T, G>, x, M, K, packed, L, N, y, S, status, 0u);
 }
-template <typename T, int MT>
-cudaError_t run_small_g(const T* x, int32_t M, int32_t K, const unsigned char* packed, const Q4Layout& L, int32_t N,
-                        int32_t group, T* y, int32_t* status, cudaStream_t stream) {
-  if (group == 32) return run_small<T, MT, 32>(x, M, K, packed, L, N, y, status, stream);
-  if (group == 64) return run_small<T, MT, 64>(x, M, K, packed, L, N, y, status, stream);
-  return run_small<T, MT, 128>(x, M, K, packed, L, N, y, status, stream);
+template <int MT, int G>
+cudaError_t run_rows(const __nv_bfloat16* x, int32_t M, int32_t K, const unsigned char* packed, const Q4Layout& L, int32_t N,
+                     __nv_bfloat16* y, int32_t* status, cudaStream_t stream) {
+  constexpr int smem = rows_smem(MT, G);
+  static_assert((smem + 2048) * rows_blocks(MT, G) <= 232448, "shared memory of an SM");
+  const int S = cluster_blocks(L.tiles, L.blocks, rows_kw(MT));
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(L.tiles * S)), S, smem, stream, &at);
+  cudaError_t e = cudaFuncSetAttribute(linear_rows_kernel<MT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  LaunchScope scope(GDN_K_LINEAR_Q4, stream);
+  return cudaLaunchKernelEx(&cfg, linear_rows_kernel<MT, G>, x, M, K, packed, L, N, y, S, status, 0u);
+}
+template <int G>
+cudaError_t run_few(bool bf16, const void* x, int32_t M, int32_t K, const unsigned char* w, const Q4Layout& L, int32_t N, void* y,
+                    int32_t* status, cudaStream_t stream) {
+  if (!bf16) {
+    for (int32_t m0 = 0; m0 < M; m0 += 65535 * 8) {  // grid.y
+      const cudaError_t e = run_small<float, G>((const float*)x + (int64_t)m0 * K, std::min(M - m0, 65535 * 8), K, w, L, N,
+                                       (float*)y + (int64_t)m0 * N, status, stream);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
+  const __nv_bfloat16* xb = (const __nv_bfloat16*)x;
+  __nv_bfloat16* yb = (__nv_bfloat16*)y;
+  if (M <= 8) return run_small<__nv_bfloat16, G>(xb, M, K, w, L, N, yb, status, stream);
+  if (M <= 16) return run_rows<2, G>(xb, M, K, w, L, N, yb, status, stream);
+  return run_rows<4, G>(xb, M, K, w, L, N, yb, status, stream);
 }
 
 struct BigPlan {
@@ -769,8 +994,8 @@ BigWs big_ws(const BigPlan& b, const Q4Layout& L) {
 }  // namespace
 
 size_t linear_q4_ws_bytes(int32_t M, int32_t N, int32_t K, int32_t group, bool bf16) {
-  if (!bf16 || M <= kSmallRows || N == 0) return 0;
   const Q4Layout L = q4_layout(N, K, group);
+  if (!bf16 || N == 0 || few_rows(M, L)) return 0;
   return big_ws(big_plan(M, L), L).total;
 }
 
@@ -778,16 +1003,10 @@ cudaError_t launch_linear_q4(bool bf16, const void* x, int32_t M, int32_t K, con
                              int32_t group, void* y, void* ws, int32_t* status, cudaStream_t stream) {
   const Q4Layout L = q4_layout(N, K, group);
   const unsigned char* w = (const unsigned char*)packed;
-  if (!bf16 || M <= kSmallRows) {
-    for (int32_t m0 = 0; m0 < M; m0 += 65535 * 8) {  // grid.y
-      const int32_t m = std::min(M - m0, 65535 * 8);
-      cudaError_t e;
-      if (!bf16) e = run_small_g<float, 1>((const float*)x + (int64_t)m0 * K, m, K, w, L, N, group, (float*)y + (int64_t)m0 * N, status, stream);
-      else if (M <= 8) e = run_small_g<__nv_bfloat16, 1>((const __nv_bfloat16*)x, M, K, w, L, N, group, (__nv_bfloat16*)y, status, stream);
-      else e = run_small_g<__nv_bfloat16, 2>((const __nv_bfloat16*)x, M, K, w, L, N, group, (__nv_bfloat16*)y, status, stream);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+  if (!bf16 || few_rows(M, L)) {
+    if (group == 32) return run_few<32>(bf16, x, M, K, w, L, N, y, status, stream);
+    if (group == 64) return run_few<64>(bf16, x, M, K, w, L, N, y, status, stream);
+    return run_few<128>(bf16, x, M, K, w, L, N, y, status, stream);
   }
   const BigPlan b = big_plan(M, L);
   const BigWs bw = big_ws(b, L);
