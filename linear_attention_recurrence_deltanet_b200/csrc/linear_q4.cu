@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
   __shared__ uint64_t full_c[kMaxSlots], free_c[kMaxSlots];
   __shared__ uint64_t full[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tslot;
-  __shared__ int s_last;
+  __shared__ int s_last;  // this block's slice came last: it adds the tile up
   bool bad = false;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int xbytes = a.tn * 128, stage_bytes = kWStage + xbytes;
@@ -667,6 +667,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     }
     mbar_init(&drain, 1);
     mbar_init_fence();
+    s_last = 0;
   }
   if (warp == 0) tmem_alloc(&tslot, 512);
   sync_tc();
@@ -821,25 +822,8 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
           for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * kTile, v[e]);
         }
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        bar_sync(1, 128);
         if (tid == 64) s_last = atomicAdd(a.count + blockIdx.x / a.S, 1) == a.S - 1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (!s_last) break;
-        __threadfence();
-        const float* parts = a.part + (int64_t)(blockIdx.x / a.S) * a.S * a.tn * kTile + row;
-#pragma unroll 1
-        for (int c = 0; c < a.tn && m0 + c < a.M; c += 16) {
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __ldcg(parts + (c + e) * kTile);
-          for (int o = 1; o < a.S; ++o)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += __ldcg(parts + ((int64_t)o * a.tn + c + e) * kTile);
-          if (n < a.N)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (m0 + c + e < a.M) a.y[(int64_t)(m0 + c + e) * a.N + n] = __float2bfloat16_rn(v[e] * wf * a.xf[m0 + c + e]);
-        }
         break;
       }
 #pragma unroll 1
@@ -856,8 +840,28 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
     }
   }
-  if (sync_tc_any(bad) && tid == 0) set_status(a.status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
+  const bool any_bad = sync_tc_any(bad);
+  if (any_bad && tid == 0) set_status(a.status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
   if (warp == 0) tmem_dealloc(tbase, 512);
+  if (!s_last) return;
+  // the slices' sums in their order, by all threads: neighbours take neighbouring weight rows
+  __threadfence();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tile = a.full * (int)gridDim.x + (int)blockIdx.x / a.S, m0 = tile % mt * a.tn, n0 = tile / mt * kTile;
+  const float* parts = a.part + (int64_t)(blockIdx.x / a.S) * a.S * a.tn * kTile;
+  const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off);
+  const int cols = min(a.tn, a.M - m0), rows = min(kTile, a.N - n0);
+#pragma unroll 4
+  for (int i = tid; i < cols * kTile; i += kBigThreads) {
+    const int c = i / kTile, r = i % kTile;
+    float p[8];
+#pragma unroll
+    for (int o = 0; o < 8; ++o) p[o] = o < a.S ? __ldcg(parts + (int64_t)o * a.tn * kTile + i) : 0.0f;
+    float v = p[0];
+#pragma unroll
+    for (int o = 1; o < 8; ++o) v += p[o];
+    if (r < rows) a.y[(int64_t)(m0 + c) * a.N + n0 + r] = __float2bfloat16_rn(v * (1.0f / __ldg(row_inv + n0 + r)) * a.xf[m0 + c]);
+  }
 }
 
 }  // namespace
