@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       for (int j = max(0, i - stages); j < i; ++j) mbar_wait_warp(&full[j % stages], (j / stages) & 1, tc::kWaitTries / 64);
   } else if (warp == 1) {
     const uint32_t id = idesc_f16(kTile, a.tn, false, false);
-    const uint64_t dw = desc_kmaj(smem_u32(sm), kTile, 0), dx = desc_kmaj(smem_u32(sm) + kWStage, a.tn, 0);
+    const uint32_t dw = (uint32_t)desc_kmaj(smem_u32(sm), kTile, 0), dx = (uint32_t)desc_kmaj(smem_u32(sm) + kWStage, a.tn, 0);
     const int stage16 = stage_bytes >> 4;  // addresses count in 16 bytes
     int s = 0;
     uint32_t phase = 0;
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kBlock / 16; ++kk)  // 32 bytes further in each row
-            mma_f16(d, dw + (uint32_t)(s * stage16 + 2 * kk), dx + (uint32_t)(s * stage16 + 2 * kk), id, (kb > p.k0 || kk > 0) ? 1u : 0u);
+            mma_f16_low(d, dw + (uint32_t)(s * stage16 + 2 * kk), dx + (uint32_t)(s * stage16 + 2 * kk), id, (kb > p.k0 || kk > 0) ? 1u : 0u);
           mma_commit(&empty[s]);
           if (kb + 1 == p.k1) mma_commit(&acc_full[ab]);
         }
