@@ -6,9 +6,11 @@
 // scales and biases of their groups are applied outside the products:
 //   q . k_t = sum_g s_tg (q_g . (c_tg - 8)) + (b_tg + 8 s_tg) sum(q_g),
 //   o = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (b_t + 8 s_t),
-// so that nothing is rounded but p_t s_t, which goes in two bf16 parts (three
-// for fp32 io, whose queries go in three as well).  A 4-bit code becomes a bf16
-// by masking it into the low mantissa bits of 128.
+// with the codes less 8 exact in 16 bits.  bf16 io: fp16 operands, query rows brought
+// below 2^8 by a power of two each (exactly, but for elements 2^-22 of the row's
+// largest), and nothing rounded but p_t s_t, to fp16 under a power of two of the
+// warp's largest s_t: 2^-11 of it.  fp32 io: bf16 operands, queries and p_t s_t in
+// three parts.
 //
 // Keys and values are the A operand (16 keys x 16 channels, 16 channels x 16
 // keys), eight query rows the B operand: a lane then scales two keys for all rows,
@@ -38,34 +40,67 @@ constexpr int smem_bytes(int D, int RT, int TQ) {
   return kWarps * stages(D) * kv_tile_bytes(D) + (q_in_smem(D, RT, TQ) ? D / 16 * TQ * 512 : 0);
 }
 
-// Two codes (bits 0-3 and 16-19) as bf16 code - 8.  The mask and the exponent sit in registers whose values the compiler
-// does not know (a kernel argument that is 0 is in them), so that one instruction takes both.  (128 + code as it is, with
-// the 128 taken out of the sums, is no faster, and costs the log of the sum three bits.)
+// Codes less 8 of a word's nibbles 0 and 4 (lo) and 1 and 5 (hi), as pairs of bf16 or fp16.  A mask and an exponent turn a
+// nibble into the low mantissa bits of 128 (bf16) or 1024 (fp16, nibble 1 as 16 c, which saves its shift).  They sit in
+// registers whose values the compiler does not know (a kernel argument that is 0 is in them), so that one instruction
+// takes both.
+template <bool F32>
 struct Codes {
-  uint32_t mask, magic;
-  __device__ __forceinline__ explicit Codes(uint32_t zero) : mask(0x000f000fu + zero), magic(0x43004300u + zero) {}
-  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
+  uint32_t mask_lo, mask_hi, magic;
+  __device__ __forceinline__ explicit Codes(uint32_t zero)
+      : mask_lo(0x000f000fu + zero), mask_hi(0x00f000f0u + zero), magic((F32 ? 0x43004300u : 0x64006400u) + zero) {}
+  __device__ __forceinline__ uint32_t lo(uint32_t w) const {
     uint32_t r;
-    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, %2, %3, 0xEA;\nsub.rn.bf16x2 %0, t, %4;\n}\n"  // ((w & mask) | magic) - 136
+    if constexpr (F32)
+      asm("{\n.reg .b32 t;\nlop3.b32 t, %1, %2, %3, 0xEA;\nsub.rn.bf16x2 %0, t, %4;\n}\n"  // ((w & mask) | magic) - 136
+          : "=r"(r)
+          : "r"(w), "r"(mask_lo), "r"(magic), "r"(0x43084308u));
+    else
+      asm("{\n.reg .b32 t;\nlop3.b32 t, %1, %2, %3, 0xEA;\nadd.rn.f16x2 %0, t, %4;\n}\n"  // ((w & mask) | magic) - 1032
+          : "=r"(r)
+          : "r"(w), "r"(mask_lo), "r"(magic), "r"(0xe408e408u));
+    return r;
+  }
+  __device__ __forceinline__ uint32_t hi(uint32_t w) const {
+    if constexpr (F32) return lo(w >> 4);
+    uint32_t r;
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, %2, %3, 0xEA;\nfma.rn.f16x2 %0, t, %4, %5;\n}\n"  // (1024 + 16 c) / 16 - 72
         : "=r"(r)
-        : "r"(w), "r"(mask), "r"(magic), "r"(0x43084308u));
+        : "r"(w), "r"(mask_hi), "r"(magic), "r"(0x2c002c00u), "r"(0xd480d480u));
     return r;
   }
 };
+template <bool F32>
+__device__ __forceinline__ uint32_t pair(float lo, float hi) {  // the operand type
+  if constexpr (F32) return bf16x2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+template <bool F32>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F32)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
+template <bool F32>
 __device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {  // C = 0
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  if constexpr (F32)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {  // of bf16: lane (r, q) has row r, columns 2q, 2q + 1
@@ -77,8 +112,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {  // of bf16: lane
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(const __grid_constant__ AttnArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int TQ = F32 ? 3 : 1;          // bf16 parts of a query
-  constexpr int TP = F32 ? 3 : 2;          // bf16 parts of p_t s_t
+  constexpr int TQ = F32 ? 3 : 1;          // parts of a query
+  constexpr int TP = F32 ? 3 : 1;          // parts of p_t s_t
   constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, NM = D / 16;
   constexpr int S = stages(D), TB = kv_tile_bytes(D);
   constexpr bool QS = q_in_smem(D, RT, TQ);
@@ -102,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
   AttnWalk<RT, kKvTile, kGroupUnits, kMinUnits> walk;
   if (!walk.start(a, kThreads, s_warp, s_found)) return;
   const float c_log2 = p.scale * kLog2e;
-  const Codes codes(a.zero);
+  const Codes<F32> codes(a.zero);
   uint32_t used = 0;  // tiles this warp has passed: stage used % S, phase used / S
   bool dead = false;
 
@@ -156,13 +191,37 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
     // queries as B fragments: lane (r, q) holds channels 16q .. 16q+15 of each 64 of row r, paired (c, c + 4) as the
     // codes are; [group], [2 + group]
     uint32_t qf[QS ? 1 : NM][4];
-    float qsum[NR][2][GK];
-    if constexpr (QS) __syncthreads();  // the last piece's reads of s_q
+    float qsum[NR][2][GK], unit[NR][2];  // sums of the row as it went into the operand; what that is a multiple of
+    if constexpr (QS) __syncthreads();   // the last piece's reads of s_q
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = rt * RT + r + 8 * i;
       const bool on = i < NR && row < rw.rows;
       const T* src = (const T*)p.q + (int64_t)(p.cu[n] + (on ? row / Gq : 0)) * p.ldq + (int64_t)(h * Gq + (on ? row % Gq : 0)) * D;
+      float scale = 1.0f;
+      if constexpr (!F32) {
+        if (i < NR) {
+          uint32_t top = 0;  // largest finite magnitude of the row, as bits
+#pragma unroll
+          for (int c = 0; c < 2 * GK; ++c) {
+            const uint4 v = on ? ld16_rw(src + (c >> 1) * 64 + q * 16 + (c & 1) * 8) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = (w[e] << 16) & 0x7fff0000u, hi = w[e] & 0x7fff0000u;
+              if (lo < 0x7f800000u) top = max(top, lo);
+              if (hi < 0x7f800000u) top = max(top, hi);
+            }
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = max(-100, (int)(top >> 23) - 127);
+          scale = pow2(7 - e);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (i < NR) unit[i < NR ? i : 0][e] = F32 ? 1.0f : 1.0f / __shfl_sync(0xffffffffu, scale, (2 * q + e) * 4);
 #pragma unroll
       for (int g = 0; g < GK; ++g) {
         float x[16];
@@ -172,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
           float y[8];
           load8(src + g * 64 + q * 16, y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = y[e];
+          for (int e = 0; e < 8; ++e) x[e] = F32 ? y[e] : y[e] * scale;
           load8(src + g * 64 + q * 16 + 8, y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[8 + e] = y[e];
+          for (int e = 0; e < 8; ++e) x[8 + e] = F32 ? y[e] : y[e] * scale;
         }
         if (i < NR) {
           float s = 0.0f;
@@ -191,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int e = 8 * (m >> 1) + 2 * (m & 1);
-            const uint32_t f0 = bf16x2(x[e], x[e + 4]), f1 = bf16x2(x[e + 1], x[e + 5]);
+            const uint32_t f0 = pair<F32>(x[e], x[e + 4]), f1 = pair<F32>(x[e + 1], x[e + 5]);
             if constexpr (F32) {
               x[e] -= lo_bf16(f0), x[e + 4] -= hi_bf16(f0), x[e + 1] -= lo_bf16(f1), x[e + 5] -= hi_bf16(f1);
             }
@@ -207,10 +266,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
         }
       }
     }
+#pragma unroll
+    for (int k = 0; k < NR; ++k) unit[k][0] *= c_log2, unit[k][1] *= c_log2;
     if constexpr (QS) __syncthreads();
 
     float o[NR][CB][4][4];                   // [channels 8r + 2j, + 1 of each 64][two channels x two rows]
     float mx[NR][2], l[NR][2], ob[NR][2][GV];
+    // bf16 io: p_t s_t times v_scale = 2^(6 - v_ref), where s_t < v_lim = 2^(v_ref + 1)
+    int v_ref = -100;
+    float v_scale = F32 ? 1.0f : 0.0f, v_lim = 0.0f;
+    const int seen_all = min(rw.first + row_last / Gq, rw.cap);  // keys that some row sees
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
 #pragma unroll
@@ -267,9 +332,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
           uint32_t c0[2], c1[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = m < 2 ? kw[i].x : kw[i].y;
-            c0[i] = codes(w >> sh);
-            c1[i] = codes(w >> (sh + 4));
+            const uint32_t w = (m < 2 ? kw[i].x : kw[i].y) >> sh;
+            c0[i] = codes.lo(w), c1[i] = codes.hi(w);
           }
 #pragma unroll
           for (int term = 0; term < TQ; ++term) {
@@ -283,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
             }
 #pragma unroll
             for (int k = 0; k < NR; ++k) {
-              if (m == 0 && term == 0) mma0(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
-              else mma(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
+              if (m == 0 && term == 0) mma0<F32>(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
+              else mma<F32>(acc[k], c0[0], c0[1], c1[0], c1[1], f[k], f[2 + k]);
             }
           }
         }
@@ -305,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
       for (int k = 0; k < NR; ++k)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s[k][i][0] *= c_log2, s[k][i][1] *= c_log2;
+        for (int i = 0; i < 2; ++i) s[k][i][0] *= unit[k][0], s[k][i][1] *= unit[k][1];
       if (masked) {
         __syncwarp();  // (keeps the branch a branch)
 #pragma unroll
@@ -316,12 +380,46 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
             for (int e = 0; e < 2; ++e)
               if (key + 8 * i >= lim[k][e]) s[k][i][e] = -INFINITY;
       }
+      float sv[GV][2], bv[GV][2];  // of the values of keys r and r + 8: scale, and bias moved to code 8
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = scales[(GK + gv) * kKvTile + 8 * i];
+          sv[gv][i] = lo_bf16(w), bv[gv][i] = fmaf(8.0f, sv[gv][i], hi_bf16(w));
+        }
       bool over = false;
+      if constexpr (!F32) {
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) over |= fabsf(sv[gv][i]) >= v_lim && (!masked || key + 8 * i < seen_all);
+      }
 #pragma unroll
       for (int k = 0; k < NR; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) over |= fmaxf(s[k][0][e], s[k][1][e]) > mx[k][e] + kSlack;
       if (__any_sync(0xffffffffu, over)) {
+        float fv = 1.0f;
+        if constexpr (!F32) {  // a larger scale than all before moves the reference, by three powers of two more
+          uint32_t top = 0;
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (!masked || key + 8 * i < seen_all) {
+                const uint32_t bits = __float_as_uint(fabsf(sv[gv][i]));
+                if (bits < 0x7f800000u) top = max(top, bits);  // (NaN reaches the rows that see it by itself)
+              }
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int e = max(-100, (int)(top >> 23) - 127);
+          if (e > v_ref || v_lim == 0.0f) {
+            const int before = v_ref;
+            v_ref = min(e + 3, 120);
+            fv = exp2f((float)(before - v_ref));
+            v_scale = pow2(6 - v_ref), v_lim = pow2(v_ref + 1);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < NR; ++k)
 #pragma unroll
@@ -338,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) o[k][cb][x][e] *= f, o[k][cb][x][2 + e] *= f;
+              for (int x = 0; x < 4; ++x) o[k][cb][x][e] *= f * fv, o[k][cb][x][2 + e] *= f * fv;
           }
       }
 #pragma unroll
@@ -356,13 +454,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
       // values: p_t s_t, in parts and turned into B fragments, against the codes
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv) {
-        float sv[2], bv[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w = scales[(GK + gv) * kKvTile + 8 * i];
-          sv[i] = lo_bf16(w);
-          bv[i] = fmaf(8.0f, sv[i], hi_bf16(w));
-        }
         uint32_t f[NR][TP][2];
 #pragma unroll
         for (int k = 0; k < NR; ++k)
@@ -370,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
           for (int i = 0; i < 2; ++i) {
             float x[2], y[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) x[e] = s[k][i][e] * sv[i], y[e] = s[k][i][e] * bv[i];
+            for (int e = 0; e < 2; ++e) x[e] = s[k][i][e] * (F32 ? sv[gv][i] : sv[gv][i] * v_scale), y[e] = s[k][i][e] * bv[gv][i];
             if (masked) {  // what a row does not see may hold anything
               __syncwarp();
 #pragma unroll
@@ -380,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
             ob[k][0][gv] += y[0], ob[k][1][gv] += y[1];
 #pragma unroll
             for (int tp = 0; tp < TP; ++tp) {
-              const uint32_t w = bf16x2(x[0], x[1]);
+              const uint32_t w = pair<F32>(x[0], x[1]);
               f[k][tp][i] = transpose8x8(w);
-              x[0] -= lo_bf16(w), x[1] -= hi_bf16(w);
+              if constexpr (F32) x[0] -= lo_bf16(w), x[1] -= hi_bf16(w);
             }
           }
 #pragma unroll
@@ -400,14 +491,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
               uint32_t c[4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                c[e] = codes(w01 >> (8 * jj + 4 * e));
-                c[2 + e] = codes(w23 >> (8 * jj + 4 * e));
+                c[e] = e ? codes.hi(w01 >> (8 * jj)) : codes.lo(w01 >> (8 * jj));
+                c[2 + e] = e ? codes.hi(w23 >> (8 * jj)) : codes.lo(w23 >> (8 * jj));
               }
 #pragma unroll
               for (int k = 0; k < NR; ++k)
 #pragma unroll
                 for (int tp = 0; tp < TP; ++tp)
-                  mma(o[k][cb][2 * half + jj], c[0], c[1], c[2], c[3], f[k][tp][0], f[k][tp][1]);
+                  mma<F32>(o[k][cb][2 * half + jj], c[0], c[1], c[2], c[3], f[k][tp][0], f[k][tp][1]);
             }
           }
         }
@@ -439,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, RT)) attn_kernel(co
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float b = ob[k][e][cb * GV / CB];
+            const float b = ob[k][e][cb * GV / CB], u = F32 ? 1.0f : pow2(v_ref - 6);
             *reinterpret_cast<float4*>(mine + row * LD + cb * 64 + 8 * r + 4 * half) =
-                make_float4(o[k][cb][2 * half][e] + b, o[k][cb][2 * half][2 + e] + b, o[k][cb][2 * half + 1][e] + b,
-                            o[k][cb][2 * half + 1][2 + e] + b);
+                make_float4(fmaf(u, o[k][cb][2 * half][e], b), fmaf(u, o[k][cb][2 * half][2 + e], b),
+                            fmaf(u, o[k][cb][2 * half + 1][e], b), fmaf(u, o[k][cb][2 * half + 1][2 + e], b));
           }
       }
     __syncthreads();

@@ -90,17 +90,19 @@ def attention64(q, k, v, scale, new):
 def attention_bound(q, k_parts, v_parts, o, scale, new, io, long=False):
     """What rounding allows: (|o error|, |lse error|) per query and head.
 
-    Scores: products of the io type and small integers are exact, sums lose at most 2^-23 of the running magnitude a
-    step; a warp's chain of a score has fewer than 8 steps that see the whole sum, so 2^-20 of the sum of magnitudes
-    (codes around 8, the bias moved there) covers them.  A score off by e changes p by a factor within e^{+-2e}.
-    Probabilities enter the value product in parts that keep 16 bits (bf16 io) or 24, values as codes around 8; sums as
+    Scores: products of the operands are exact, sums lose at most 2^-23 of the running magnitude a step; a warp's chain
+    of a score has fewer than 8 steps that see the whole sum, so 2^-20 of the sum of magnitudes (codes around 8, the bias
+    moved there) covers them.  A score off by e changes p by a factor within e^{+-2e}.  Values are codes around 8; sums as
     for scores.  The output rounds once.
 
+    fp32 io: queries and p times the value's scale go in three bf16 parts, 2^-20 covers them.
+    bf16 io: queries are fp16 between 2^7 and 2^8 at their row's largest, so that the half step below fp16's normal
+    numbers, 2^-25, is 2^-32 of it.  p times the scale is off by half a step of fp16, 2^-11, or, where it is under 2^-14,
+    by 2^-25 where the largest scale stands at 2^3 at least: 2^-25 of the largest value for each key.
     long: the long row tiles (bf16 io).  Key products are exact in fp16 too; the moved bias and the sums of the query's
     groups go in two parts of 11 bits each, 2^-22 of either, within the 2^-20.  Keys and values have their largest so far
-    between 2^7 and 2^12 and queries between 2^7 and 2^8, so that the half step below fp16's normal numbers, 2^-25, is
-    2^-32 of the largest key and of the row's largest query element.  Values and probabilities are off by half a step of
-    fp16, 2^-11 each; a probability under 2^-14 is off by 2^-25 where the largest is 1 at least."""
+    between 2^7 and 2^12: half a step below the normal numbers is 2^-32 of the largest key.  Values and probabilities are
+    off by half a step of fp16, 2^-11 each; a probability under 2^-14 is off by 2^-25 where the largest is 1 at least."""
     n, hq, d = q.shape
     (_, ks, kb, _), (_, vs, vb, _) = k_parts, v_parts
     length, hkv = ks.shape[:2]
@@ -115,13 +117,12 @@ def attention_bound(q, k_parts, v_parts, o, scale, new, io, long=False):
             kh = h // (hq // hkv)
             qa = q[i, h].double().abs()
             ds = abs(scale) * 2.0 ** -20 * (k_mag[:seen, kh] @ qa).max()
-            if long:
-                kv = k_parts[3].abs()[:, kh]
-                ds = ds + abs(scale) * (2.0 ** -32 * kv.max() * qa.sum() + 2.0 ** -32 * qa.max() * kv[:seen].sum(-1).max())
+            if io == "bf16":
+                ds = ds + abs(scale) * 2.0 ** -32 * (qa.max() * k_mag[:seen, kh].sum(-1).max() + k_mag[:, kh].max() * qa.sum())
             el[i, h] = ds
-            eo[i, h] = (2 * ds + (2.0 ** -16 if io == "bf16" else 2.0 ** -20) + 2.0 ** -20) * v_mag[:seen, kh].max()
-            if long:
-                eo[i, h] += (2 * 2.0 ** -11 + 2.0 ** -32 + seen * 2.0 ** -25) * v_mag[:, kh].max()
+            eo[i, h] = (2 * ds + 2 * 2.0 ** -20) * v_mag[:seen, kh].max()
+            if io == "bf16":
+                eo[i, h] += ((2 if long else 1) * 2.0 ** -11 + 2.0 ** -32 + seen * 2.0 ** -25) * v_mag[:, kh].max()
     return U[io] * o.abs() + eo.unsqueeze(-1), el
 
 

@@ -564,3 +564,33 @@ def test_append_many_sequences(n):
     ko, vo = torch.empty_like(k), torch.empty_like(v)
     gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, ko, vo)
     assert torch.equal(vo.cpu(), quantise(v.cpu(), 64)[3].bfloat16()) and torch.equal(ko.cpu(), quantise(k.cpu(), 64)[3].bfloat16())
+
+
+@pytest.mark.parametrize("new", [1, 4])
+@pytest.mark.parametrize("k_scale,v_scale,q_scale", [(1e5, 1e-6, 1e-5), (1e-8, 3e6, 1e7), (1e-20, 1e-20, 1.0), (3e4, 1e30, 1e-4)])
+def test_short_tiles_magnitudes_past_fp16(new, k_scale, v_scale, q_scale):
+    c = Case([new, new], [200, 500], 4, 2, 128, 32, "bf16", seed=52)
+    c.k = [(t.float() * k_scale).bfloat16() for t in c.k]
+    c.v = [(t.float() * v_scale).bfloat16() for t in c.v]
+    c.q = (c.q.float() * q_scale).bfloat16()
+    c.d_q = c.q.cuda()
+    c.fill()
+    c.check(*c.attention())
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_short_tiles_values_that_grow_and_nan_in_a_draft(d):
+    """Scales of the values grow along the context; the last draft token's value is NaN and only its own rows see it."""
+    c = Case([3], [1000], 4, 2, d, 64, "bf16", seed=53, outlier=False)
+    grow = 10.0 ** (torch.arange(1003) // 128).float()[:, None, None]
+    c.v = [(c.v[0].float() * grow * 1e-4).bfloat16()]
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    n = Case([3], [1000], 4, 2, d, 64, "bf16", seed=53, outlier=False)
+    n.v = [c.v[0].clone()]
+    n.v[0][1002, 1, 0] = math.nan
+    n.fill()
+    o2, l2 = n.attention()
+    assert torch.isnan(o2[2, 2:, :min(d, 128)]).all() and torch.equal(o2[:2], o[:2]) and torch.equal(o2[2, :2], o[2, :2])
+    assert torch.equal(l2, lse)
