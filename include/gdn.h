@@ -426,7 +426,10 @@ GDN_API gdn_status gdn_project_out(const gdn_config* cfg, const void* o, int32_t
  *   reading key/value head h / (Hq / Hkv).  A query that sees no key gets o = 0.
  *   lse (fp32 [T, Hq], may be NULL): log of the sum of the exponentials, -inf
  *   where nothing is seen.  One token a sequence is a decode step, a few are a
- *   draft to verify, many a prefill chunk; sequences may mix.
+ *   draft to verify, many a prefill chunk; sequences may mix.  Scores are exact
+ *   but for fp32 sums; bf16 io rounds probabilities (times the values' scales) to
+ *   fp16, 2^-11, and, where a sequence has more than 64 rows (tokens x Hq / Hkv)
+ *   and D <= 128, the values too; fp32 io keeps 24 bits of everything.
  *   Workspace: gdn_attention_workspace_size() bytes for the same (cfg, total
  *   tokens, num_seqs), 256-byte aligned; it needs no initial contents and holds
  *   nothing between calls, so calls that may run at the same time need one each.
@@ -487,7 +490,9 @@ GDN_API gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int6
  * Scope; affine Q4 weights, issue #95, implementation comment):
  *   Y[m, n] = sum_k X[m, k] * w[n, k],  w[n, k] = scale[n, k / group] * code[n, k] + bias[n, k / group]
  * group is 32, 64 or 128; K a positive multiple of 8, M, N >= 0.  X [M, K] and
- * Y [M, N] are dense in io_dtype; sums are fp32.
+ * Y [M, N] are dense in io_dtype; sums are fp32.  Products are exact for fp32 io
+ * and for up to 16 rows of bf16 (32 for small weights); more rows round the
+ * weights to fp16, 2^-11 of each, with powers of two over rows of W and of X.
  *
  * gdn_q4_pack: lays a weight out once for gdn_linear_q4.  codes
  *   [N, G * group / 2] bytes (G = ceil(K / group)): channel 2i in the low half
