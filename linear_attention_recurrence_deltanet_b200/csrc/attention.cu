@@ -674,8 +674,9 @@ AttnWorkspace ws_at(const WsLayout& w, void* ws) {
   return AttnWorkspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)};
 }
 
-// bf16 io and heads of up to 128 channels: sequences with more rows a key/value head than this run the long row tiles
-constexpr int kPrefillFrom = 64;
+// bf16 io: sequences with more rows a key/value head than this run the long row tiles (16 / 2 heads of 256 over 20000
+// tokens: 72 rows 45 us here and 55 there, 136 rows 65 and 56)
+constexpr int prefill_from(int D) { return D <= 128 ? 64 : 128; }
 
 template <typename T, int D, int RT>
 cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
@@ -713,15 +714,14 @@ cudaError_t run_d(const AttnProblem& p, const KvCache& c, void* ws, int32_t* sta
 
 size_t attention_ws_bytes(int32_t T, int32_t, int32_t Hq, int32_t Hkv, int32_t D, bool bf16) {
   size_t w = ws_layout(D, grid_of(D, 8), 16).total;  // the larger grid
-  if (bf16 && D <= 128 && (int64_t)T * (Hq / Hkv) > kPrefillFrom)
-    w = std::max(w, ws_layout(D, kAttnSms, kPrefillRows).total);
+  if (bf16 && (int64_t)T * (Hq / Hkv) > prefill_from(D)) w = std::max(w, ws_layout(D, kAttnSms, prefill_rows(D)).total);
   return w;
 }
 
 cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
                              cudaStream_t stream) {
-  if (p.bf16 && p.D <= 128 && (int64_t)p.max_q * (p.Hq / cache.Hkv) > kPrefillFrom)
-    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, kPrefillRows), ws), kAttnSms, status, 0}, stream);
+  if (p.bf16 && (int64_t)p.max_q * (p.Hq / cache.Hkv) > prefill_from(p.D))
+    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, prefill_rows(p.D)), ws), kAttnSms, status, 0}, stream);
   if (p.D == 64) return run_d<64>(p, cache, ws, status, stream);
   if (p.D == 128) return run_d<128>(p, cache, ws, status, stream);
   return run_d<256>(p, cache, ws, status, stream);

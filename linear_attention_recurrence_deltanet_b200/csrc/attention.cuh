@@ -191,8 +191,8 @@ __device__ __forceinline__ int split_group(const AttnArgs& a, int x, int* s_coun
   return *s_first;
 }
 
-// attention_prefill.cu: bf16 io, head dims up to 128, long row tiles
-constexpr int kPrefillRows = 256;
+// attention_prefill.cu: bf16 io, long row tiles
+constexpr int prefill_rows(int D) { return D <= 128 ? 256 : 128; }  // a block's
 cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace gdn

@@ -1,5 +1,5 @@
 // Causal attention over the 4-bit paged cache for many query rows (chunked
-// prefill; bf16 io, heads of 64 or 128 channels), on tcgen05:
+// prefill; bf16 io), on tcgen05:
 //   S = Q K^T, P = 2^(S - m) and O = P V on tiles of 128 rows x 128 keys.
 //
 // Operands are fp16, with powers of two over them: query rows are brought below 2^8
@@ -14,13 +14,27 @@
 // in bf16, at the same rate.  A value group that stands for NaN is expanded as
 // zeros and noted by token, so that it reaches the rows that see it and no other.
 //
-// A block takes two tiles of 128 query rows (tokens x the heads that share a
-// key/value head) through the same keys.  Warps 0-3 and 4-7 are the softmax of
-// either tile, a thread a row; warps 8-15 expand, 16 keys each; warp 16 issues the
-// products (17-19 fill its group up).  While one tile's softmax runs the other's products do.  S is 128
-// columns of TMEM, P overwrites its first 64 in fp16 and is the A operand of P V.
-// O stays in TMEM; the running maximum moves only when a score passes it by
-// kSlack, and only then is O rescaled.
+// Heads of up to 128 channels: a block takes two tiles of 128 query rows (tokens x
+// the heads that share a key/value head) through the same keys.  Warps 0-3 and 4-7
+// are the softmax of either tile, a thread a row; eight warps expand, 16 keys each;
+// one warp issues the products (three more fill its group up).  While one tile's
+// softmax runs the other's products do.  S is 128 columns of TMEM, P overwrites its
+// first 64 in fp16 and is the A operand of P V.  O stays in TMEM; the running maximum
+// moves only when a score passes it by kSlack, and only then is O rescaled.
+//
+// Heads of 256: O of one tile is half of TMEM, and queries, keys and values of one
+// tile are 192 KB, so a block takes one tile of rows.  Two buffers of S alternate
+// from key tile to key tile: S of tile t + 1 is made while the softmax of t runs.
+// Keys and values have one stage each, filled in turn: keys of t + 1 once S of t is made,
+// values of t once P V of t - 1 is.
+//
+// Measured, 2048 tokens over 6144, 24 / 2 heads: D = 128 288 us (floor 107, by the
+// products), D = 256 487 us (floor 214; 2310 with attn_kernel).  D = 128: a tile's chain of
+// products, wake-ups, maximum and exponentials is longer than the other tile's work.
+// D = 256: the chain is a tile's expansion, with shared memory half taken by operands.
+// Tried there: two threads a row 497, the keys in two parts 515, sixteen warps that
+// expand half the channels each 494, eight for keys and eight for values 604 (products
+// and stores then meet in shared memory).
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
@@ -31,22 +45,34 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = kPrefillRows, kKeys = 128;
-constexpr int kSoftWarps = 8, kExpandWarps = 8, kThreads = (kSoftWarps + kExpandWarps + 4) * 32;
-// Registers a thread after the start: 640 threads begin with 96, 61440 in all; these come to 60416.
+constexpr int kKeys = 128;
+constexpr bool two_tiles(int D) { return D <= 128; }  // row tiles of a block: two, or one with two buffers of S
+constexpr int rows_of_block(int D) { return prefill_rows(D); }
+constexpr int soft_warps(int D) { return two_tiles(D) ? 8 : 4; }
+constexpr int kExpandWarps = 8;
+constexpr int threads_of(int D) { return (soft_warps(D) + kExpandWarps + 4) * 32; }
+// Registers a thread after the start, heads of up to 128: 640 threads begin with 96, 61440 in all; these come to 60416.
+// Heads of 256: 512 threads have 128 each and keep them.
 constexpr int kSoftRegs = 128, kExpandRegs = 80, kProductRegs = 56;
-static_assert((kSoftWarps * kSoftRegs + kExpandWarps * kExpandRegs + 4 * kProductRegs) * 32 <= kThreads * 96, "register split");
+static_assert((8 * kSoftRegs + kExpandWarps * kExpandRegs + 4 * kProductRegs) * 32 <= threads_of(128) * 96, "register split");
+static_assert(kSoftRegs >= 96 && kExpandRegs <= 96 && kProductRegs <= 96, "setmaxnreg.inc must not lower, .dec not raise");
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-using Walk = AttnWalk<kRows, kKeys, 3, 6>;     // a group's queries and output cost about three tiles
+template <int D>
+using Walk = AttnWalk<rows_of_block(D), kKeys, 3, 3>;  // a group's queries and output cost about three tiles; at least three a block (six: 64 tokens over 500 40 -> 55 us)
 
 constexpr int tile_bytes(int D) { return kKeys * D * 2; }
 constexpr int kSide = kKeys * 32;  // the 16 more channels of a tile: 32 bytes a row, 32-byte swizzle
+// shared memory, in tiles: queries 0 (and 1), then stages of keys and values in turn; in sides: queries, then stages of keys
+constexpr int q_tiles(int D) { return two_tiles(D) ? 2 : 1; }
+constexpr int stages_of(int D) { return two_tiles(D) ? 2 : 1; }
+constexpr int all_tiles(int D) { return q_tiles(D) + 2 * stages_of(D); }
 constexpr int smem_bytes(int D) {  // one block an SM, which takes all of its TMEM
-  return 6 * tile_bytes(D) + 4 * kSide + 1024 < 120000 ? 120000 : 6 * tile_bytes(D) + 4 * kSide + 1024;
+  return all_tiles(D) * tile_bytes(D) + 4 * kSide + 1024 < 120000 ? 120000 : all_tiles(D) * tile_bytes(D) + 4 * kSide + 1024;
 }
+static_assert(smem_bytes(256) <= 227 * 1024 - 2048, "shared memory of a block");
 // byte offset of eight of a row's 16 more channels, and the descriptor of such a tile (K-major, 8 rows a 256-byte group)
 __device__ __forceinline__ uint32_t side_chunk(int row, int i) { return (uint32_t)(row * 32 + ((i ^ (row >> 2)) & 1) * 16); }
 __device__ __forceinline__ uint64_t desc_side(uint32_t saddr) {
@@ -65,7 +91,7 @@ struct alignas(16) Meta {
   float v_step;          // v_unit before / after this tile: O is rescaled by it
   uint32_t rare;         // some keys have no page (1), some values are NaN (2); the four are read as one uint4
   uint8_t valid[8];      // 16 keys each: they have a page
-  uint16_t v_nan[8];     // by key: its value is NaN
+  uint16_t v_nan[2][8];  // by value group and key: its value is NaN
 };
 
 // Eight codes as values s c + b or keys s (c - 8), in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
@@ -157,13 +183,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int GK = D / kKGroup, CB = D / 64, TB = kv_tile_bytes(D), TILE = tile_bytes(D);
-  constexpr uint32_t kO = 256;  // TMEM: S of either tile at 0 and 128, O at 256 and 256 + D
+__global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, TILE = tile_bytes(D);
+  constexpr bool kTwo = two_tiles(D);
+  constexpr int kSoftWarps = soft_warps(D), kThreads = threads_of(D), kRows = rows_of_block(D);
+  constexpr int kKv = q_tiles(D) * TILE, kSides = all_tiles(D) * TILE;  // where stages and sides begin
+  constexpr int kMeta = kTwo ? 2 : 4;  // key tiles that are spoken of at a time
+  // TMEM: S of either row tile, or of either key tile in turn, at 0 and 128; O at 256 (and 256 + D).  P is in the first
+  // half of its S, which is made anew only when the product that reads P is done: products of different shapes or into
+  // different columns need not run in the order of their issue.  Heads of 64 leave columns for P apart from S, and
+  // nothing waits.
+  constexpr uint32_t kO = 256;
+  constexpr bool kPApart = D == 64;
+  constexpr uint32_t kP = kPApart ? kO + 2 * D : 0, kPStep = kPApart ? 64 : 128;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  // two row tiles: q, s, p, o by row tile, kv by stage.  One: s and p by key tile, kv_full of the keys and of the values.
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], kv_full[2], kv_free[2], drain;
-  __shared__ Meta meta[2];
+  __shared__ Meta meta[kMeta];
   __shared__ uint2 s_top[kExpandWarps];
   __shared__ int64_t s_warp[kThreads / 32], s_found[4];
   __shared__ uint32_t tslot;
@@ -171,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
   const AttnProblem& p = a.p;
   const int Gq = p.Hq / a.cache.Hkv;
 
-  Walk walk;
+  Walk<D> walk;
   if (!walk.start(a, kThreads, s_warp, s_found)) return;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -189,17 +226,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
   sync_tc();
   const uint32_t tbase = tslot;
   bool bad = false;
-  int kt = 0;  // key tiles before this one, over all pieces: stage kt & 1
+  int kt = 0;  // key tiles before this one, over all pieces
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
-    more_regs<kSoftRegs>();
-    const int x = warp >> 2, r = (warp & 3) * 32 + lane;
+    if constexpr (kTwo) more_regs<kSoftRegs>();
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kO + D * x;
+    const uint32_t to = tbase + lanes + kO + D * x;
     unsigned char* sq = sm + x * TILE;
     const float c_log2 = fabsf(p.scale) * kLog2e;
-    uint32_t ph_s = 0, ph_o = 0;
+    uint32_t ph_s = 0, o_done = 0;  // o_done: arrivals at o_full
+    bool late = false;  // a wait of this warp alone ran out
     do {
       if (!walk.piece(a)) continue;
       const int tiles = walk.t1 - walk.t0;
@@ -247,26 +285,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           for (int j = 0; j < 8; ++j) z[j] = v[(j >> 1) + 4 * (j & 1)] * f, sum[c / 8] += z[j];  // channels in the order of Expand
           *reinterpret_cast<uint4*>(sq + kmaj_chunk(128, r, c * 8)) = pack8h(z);
         }
-        uint32_t side[4] = {0, 0, 0, 0};  // high, low, high, low by group
+        uint32_t side[8] = {};  // high, low, high, low by group
 #pragma unroll
         for (int g = 0; g < GK; ++g) side[2 * g] = side[2 * g + 1] = high_low(sum[g]);
-        unsigned char* row_side = sm + 6 * TILE + x * kSide;
-        *reinterpret_cast<uint4*>(row_side + side_chunk(r, 0)) = make_uint4(side[0], side[1], side[2], side[3]);
-        *reinterpret_cast<uint4*>(row_side + side_chunk(r, 1)) = make_uint4(0, 0, 0, 0);
+        unsigned char* row_side = sm + kSides + x * kSide;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4*>(row_side + side_chunk(r, i)) =
+              make_uint4(side[4 * i], side[4 * i + 1], side[4 * i + 2], side[4 * i + 3]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
       }
       float m = -INFINITY, l = 0.0f, v_unit = 1.0f;
-      bool nan = false;
+      bool nan[GV] = {};
       for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
-        if (!group_wait(1 + x, 128, (warp & 3) == 0, &s_full[x], ph_s, nullptr, 0)) {
+        const int buf = kTwo ? x : kt & 1;
+        const uint32_t ts = tbase + lanes + 128 * buf, tp = tbase + lanes + kP + kPStep * buf;
+        if (!group_wait(1 + x, 128, (warp & 3) == 0, &s_full[buf], kTwo ? ph_s : (uint32_t)(kt >> 1) & 1u, nullptr, 0)) {
           bad = true;
           break;
         }
         ph_s ^= 1;
         fence_after();
-        const Meta& mt = meta[kt & 1];
+        const Meta& mt = meta[kt % kMeta];
         const uint4 units = *reinterpret_cast<const uint4*>(&mt);
         const float f = unit * __uint_as_float(units.x) * c_log2, v_step = __uint_as_float(units.z);
         v_unit = __uint_as_float(units.y);
@@ -279,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int k = left - 16 * i;
-            nan |= (mt.v_nan[i] & (k >= 16 ? 0xffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0;
+#pragma unroll
+            for (int g = 0; g < GV; ++g) nan[g] |= (mt.v_nan[g][i] & (k >= 16 ? 0xffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0;
           }
         }
         // S is read twice, 32 columns at a time and the next ones on their way: for the largest product, then for the
@@ -305,7 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           const float m2 = fmaxf(m, top), g = m2 == m ? 1.0f : ex2(m - m2);
           m = m2;
           l *= g;
-          if (t > walk.t0) {  // the product of the last tile is done: S came after it
+          if (t > walk.t0) {
+            // the product of the last tile is done: S came after it.  With one row tile S came before, and O is waited for.
+            if constexpr (!kTwo) {
+              late |= !mbar_wait_warp(&o_full[0], (uint32_t)(kt - 1) & 1u);
+              fence_after();
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
               float z[16];
@@ -344,28 +392,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
           }
           __syncwarp();
-          tmem_st16(ts + 16 * c, w);
+          tmem_st16(tp + 16 * c, w);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], ph_o, nullptr, 0)) {
+      o_done += kPApart ? 1 : tiles;
+      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], (o_done - 1) & 1u, nullptr, 0)) {
         bad = true;
         break;
       }
-      ph_o ^= 1;
       fence_after();
       // rows out: whole, or unnormalised to the workspace
       const bool from_start = walk.t0 == 0, to_end = walk.t1 == walk.tiles;
       const bool is_whole = from_start && to_end;
       const int64_t out = (int64_t)tok * p.Hq + head;
       const int64_t slot = ((int64_t)(2 * blockIdx.x + (from_start ? 1 : 0)) * kRows + x * 128 + r);
-      const float f = nan ? __int_as_float(0x7fc00000) : is_whole ? (l == 0.0f ? 0.0f : v_unit / l) : v_unit;
+      const float f_row = is_whole ? (l == 0.0f ? 0.0f : v_unit / l) : v_unit;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
+        const float f = (GV > 1 && c0 >= v_group(D) ? nan[GV - 1] : nan[0]) ? __int_as_float(0x7fc00000) : f_row;
         float v[32];
         tmem_ld32(to + c0, v);
         if (!on) continue;
@@ -394,32 +443,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         a.ws.split[blockIdx.x] = make_int4(walk.n, walk.h, walk.rt, walk.last_block());
       fence_before();  // O is read before the next piece's first product, which waits for p_full
     } while (walk.next(a));
+    bad |= late;
   } else if (warp < kSoftWarps + kExpandWarps) {
     // ------------------------------------------------------------- expansion
-    fewer_regs<kExpandRegs>();
-    const int w = warp - kSoftWarps, half = lane & 1, tk = lane >> 1;
+    if constexpr (kTwo) fewer_regs<kExpandRegs>();
+    const int w = warp - kSoftWarps, half = lane & 1, tk = lane >> 1;  // 16 keys a warp
+    constexpr int kGroup = 32 * kExpandWarps, kBar = 3;
     const int tv = (tk & 8) | ((tk & 3) << 1) | ((tk >> 2) & 1);  // the token of V row tk (v_row's inverse)
     int k_ref = -100, v_ref = -100;                               // exponents of the largest values so far
     float k_lim = -1.0f, v_lim = -1.0f, fk = 0.0f, fv = 0.0f;     // what they hold, and their scales
     const Expand expand(a.zero);
+    constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
     // where this lane's four chunks of 64 channels go, of keys and of values
     const bool odd = (tv >> 2) & 1;  // pairs of words in turn: the eight lanes of a store then hit all banks
     uint32_t at_k[4], at_v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      at_k[j] = 2 * TILE + kmaj_chunk(kKeys, 16 * w + tk, (half * 4 + j) * 8);
-      at_v[j] = 3 * TILE + mnmaj_chunk(kKeys, 16 * w + tv, (half * 4 + (j ^ (odd ? 1 : 0))) * 8);
+      at_k[j] = kKv + kmaj_chunk(kKeys, 16 * w + tk, (half * 4 + j) * 8);
+      at_v[j] = kKv + TILE + mnmaj_chunk(kKeys, 16 * w + tv, (half * 4 + (j ^ (odd ? 1 : 0))) * 8);
     }
     do {
       if (!walk.piece(a)) continue;
       const int n = walk.n, h = walk.h;
       const int all = max(0, min(walk.rw.first + (walk.rt * kRows + walk.rows_here() - 1) / Gq, walk.rw.cap));  // keys anybody sees
-      uint4 kc[CB], vc[CB], kn[CB], vnx[CB];
-      uint32_t ks[GK], vs, ksn[GK], vsn;
-      bool ok, okn;
       int64_t place = -1;
-      // this warp's 16 keys of tile t; every 32 tiles lane j looks the j-th of them up
-      auto load = [&](int t, uint4 (&k4)[CB], uint4 (&v4)[CB], uint32_t (&sk)[GK], uint32_t& sv, bool& there) {
+      // Where this warp's 16 keys of tile t are, -1: nowhere.  Every 32 tiles lane j looks the j-th of them up.
+      auto find = [&](int t) {
         if ((t - walk.t0) % 32 == 0) {
           const int pos = (t + lane) * kKeys + 16 * w;
           place = -1;
@@ -428,68 +477,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (place < 0) set_status(a.status, kStatusBadPage | (GDN_K_ATTENTION << 8));
           }
         }
-        const int64_t at = __shfl_sync(0xffffffffu, place, (t - walk.t0) % 32);
+        return __shfl_sync(0xffffffffu, place, (t - walk.t0) % 32);
+      };
+      auto load_codes = [&](int64_t at, int off, uint4 (&c)[CB]) {
+        const unsigned char* from = a.cache.pool + at + off + lane * 16;
+#pragma unroll
+        for (int g = 0; g < CB; ++g) c[g] = at >= 0 ? *reinterpret_cast<const uint4*>(from + g * 512) : make_uint4(0, 0, 0, 0);
+      };
+      auto load_scales = [&](int t, int64_t at, uint32_t (&sk)[GK], uint32_t (&sv)[GV], bool& there) {
         const int pos = t * kKeys + 16 * w;
         there = at >= 0 || pos >= all;
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(a.cache.pool + at + kv_scale_off(D));
+        const bool see_k = at >= 0 && pos + tk < all, see_v = at >= 0 && pos + tv < all;  // behind the last key they may be anything
 #pragma unroll
-        for (int g = 0; g < CB; ++g) k4[g] = v4[g] = make_uint4(0, 0, 0, 0);
+        for (int g = 0; g < GK; ++g) sk[g] = see_k ? sc[g * kKvTile + tk] : 0;
 #pragma unroll
-        for (int g = 0; g < GK; ++g) sk[g] = 0;
-        sv = 0;
-        if (at >= 0) {
-          const unsigned char* tile = a.cache.pool + at;
-          const uint32_t* sc = reinterpret_cast<const uint32_t*>(tile + kv_scale_off(D));
-#pragma unroll
-          for (int g = 0; g < CB; ++g) {
-            k4[g] = *reinterpret_cast<const uint4*>(tile + g * 512 + lane * 16);
-            v4[g] = *reinterpret_cast<const uint4*>(tile + kv_v_off(D) + g * 512 + lane * 16);
-          }
-          if (pos + tk < all) {  // behind the last key the codes may be anything
-#pragma unroll
-            for (int g = 0; g < GK; ++g) sk[g] = sc[g * kKvTile + tk];
-          }
-          if (pos + tv < all) sv = sc[GK * kKvTile + tv];
-        }
+        for (int g = 0; g < GV; ++g) sv[g] = see_v ? sc[(GK + g) * kKvTile + tv] : 0;
       };
-      load(walk.t0, kc, vc, ks, vs, ok);
-      for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
-        if (t + 1 < walk.t1) load(t + 1, kn, vnx, ksn, vsn, okn);
-        const int st = kt & 1;
-        // Mostly the tile's keys and values stay within the references and are finite, and every key has a page: one
-        // barrier says so, which the wait for the stage needs anyway.
-        float rk = 0.0f;
+      // Brings the references up to a tile's keys and values and fills mt; false: a wait ran out (a warp passes waited =
+      // false).  Mostly the tile stays within the references and is finite, and every key has a page: one barrier says
+      // so, which the wait for the stage needs anyway.  A value that is NaN gets the scale 0.
+      auto agree = [&](Meta& mt, bool waited, const uint32_t (&ks)[GK], uint32_t (&vs)[GV], bool ok) {
+        float rk = 0.0f, rv = 0.0f;
+        bool odd_k = false, odd_v = false;
 #pragma unroll
-        for (int g = 0; g < GK; ++g) rk = fmaxf(rk, reach(ks[g]));
-        const float rv = reach(vs);
-        bool odd_k = false;
+        for (int g = 0; g < GK; ++g) rk = fmaxf(rk, reach(ks[g])), odd_k |= !finite_word(ks[g]);
 #pragma unroll
-        for (int g = 0; g < GK; ++g) odd_k |= !finite_word(ks[g]);
-        const bool v_bad = !finite_word(vs);
-        const bool plain = rk <= k_lim && rv <= v_lim && !odd_k && !v_bad && ok;
-        bool waited = true;
-        if (kt >= 2 && w == 0) waited = mbar_wait_warp(&kv_free[st], ((kt >> 1) & 1) ^ 1);
-        if (bar_or(3, 32 * kExpandWarps, !plain || !waited)) {
+        for (int g = 0; g < GV; ++g) rv = fmaxf(rv, reach(vs[g])), odd_v |= !finite_word(vs[g]);
+        const bool plain = rk <= k_lim && rv <= v_lim && !odd_k && !odd_v && ok;
+        if (bar_or(kBar, kGroup, !plain || !waited)) {
           // the rest of it: whether the wait ran out, the tile's largest finite key and value, what is odd
-          uint32_t top_k = 0;
+          uint32_t top_k = 0, top_v = 0, nans[GV];
+          bool any = false;
 #pragma unroll
           for (int g = 0; g < GK; ++g)
             if (finite_word(ks[g])) top_k = max(top_k, __float_as_uint(reach(ks[g])));
+#pragma unroll
+          for (int g = 0; g < GV; ++g) {
+            const bool v_bad = !finite_word(vs[g]);
+            if (v_bad) vs[g] = 0;
+            else top_v = max(top_v, __float_as_uint(reach(vs[g])));
+            nans[g] = __reduce_or_sync(0xffffffffu, v_bad ? 1u << tv : 0u);
+            any |= nans[g] != 0;
+          }
           top_k = __reduce_max_sync(0xffffffffu, top_k);
-          uint32_t top_v = __reduce_max_sync(0xffffffffu, v_bad ? 0u : __float_as_uint(rv));
-          const uint32_t nans = __reduce_or_sync(0xffffffffu, v_bad ? 1u << tv : 0u);
-          if (v_bad) vs = 0;
+          top_v = __reduce_max_sync(0xffffffffu, top_v);
           if (lane == 0) {
             s_top[w] = make_uint2(top_k, top_v);
-            meta[st].valid[w] = ok ? 1 : 0;
-            meta[st].v_nan[w] = (uint16_t)nans;
-          }
-          if (bar_or(3, 32 * kExpandWarps, !waited)) {
-            bad = true;
-            break;
-          }
-          const bool no_page = bar_or(3, 32 * kExpandWarps, !ok), any_nan = bar_or(3, 32 * kExpandWarps, nans != 0);
+            mt.valid[w] = ok ? 1 : 0;
 #pragma unroll
-          for (int i = 0; i < kExpandWarps; ++i) top_k = max(top_k, s_top[i].x), top_v = max(top_v, s_top[i].y);
+            for (int g = 0; g < GV; ++g) mt.v_nan[g][w] = (uint16_t)nans[g];
+          }
+          if (bar_or(kBar, kGroup, !waited)) return false;
+          const bool no_page = bar_or(kBar, kGroup, !ok), any_nan = bar_or(kBar, kGroup, any);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top_k = max(top_k, s_top[i].x), top_v = max(top_v, s_top[i].y);
           // a larger exponent than all before moves the reference, by three more
           const int ek = exponent(min(top_k, 0x7f7fffffu)), ev = exponent(min(top_v, 0x7f7fffffu)), v_old = v_ref;
           if (ek > k_ref) k_ref = min(ek + 3, 127);
@@ -497,102 +539,223 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
           fk = pow2(11 - k_ref), fv = pow2(11 - v_ref);
           k_lim = k_ref >= 127 ? 3.0e38f : pow2(k_ref + 1) * 0.99f, v_lim = v_ref >= 127 ? 3.0e38f : pow2(v_ref + 1) * 0.99f;
           if (w == 0 && lane == 0) {
-            meta[st].v_step = v_old == v_ref ? 1.0f : exp2f((float)(v_old - v_ref));
-            meta[st].rare = (no_page ? 1u : 0u) | (any_nan ? 2u : 0u);
+            mt.v_step = v_old == v_ref ? 1.0f : exp2f((float)(v_old - v_ref));
+            mt.rare = (no_page ? 1u : 0u) | (any_nan ? 2u : 0u);
           }
-          bar_sync(3, 32 * kExpandWarps);  // s_top is read
+          bar_sync(kBar, kGroup);  // s_top is read
         } else if (w == 0 && lane == 0) {
-          meta[st].v_step = 1.0f, meta[st].rare = 0;
+          mt.v_step = 1.0f, mt.rare = 0;
         }
-        if (w == 0 && lane == 0) meta[st].k_unit = pow2(k_ref - 11), meta[st].v_unit = pow2(v_ref - 11);
-        unsigned char* stage = sm + 2 * st * TILE;
-        constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
-        uint32_t side[4] = {0, 0, 0, 0};
+        if (w == 0 && lane == 0) mt.k_unit = pow2(k_ref - 11), mt.v_unit = pow2(v_ref - 11);
+        return true;
+      };
+      auto put_keys = [&](int st, const uint4 (&kc)[CB], const uint32_t (&ks)[GK]) {
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
-          const float sk = lo_bf16(ks[g]) * fk;
-          const uint32_t z = high_low(fmaf(8.0f, sk, hi_bf16(ks[g]) * fk));
-          side[2 * g] = __byte_perm(z, z, 0x1010), side[2 * g + 1] = __byte_perm(z, z, 0x3232);  // high, high, low, low
-          const __half2 s = __float2half2_rn(sk);
+          const __half2 s = __float2half2_rn(lo_bf16(ks[g]) * fk);
           const uint32_t c[4] = {kc[g].x, kc[g].y, kc[g].z, kc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_k[j] + g * kBlock64) = expand.key(c[j], s);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(sm + 2 * st * TILE + at_k[j] + g * kBlock64) = expand.key(c[j], s);
         }
-        *reinterpret_cast<uint4*>(sm + 6 * TILE + (2 + st) * kSide + side_chunk(16 * w + tk, half)) =
-            half ? make_uint4(0, 0, 0, 0) : make_uint4(side[0], side[1], side[2], side[3]);
-        const __half2 s = __float2half2_rn(lo_bf16(vs) * fv), b = __float2half2_rn(hi_bf16(vs) * fv);
+        uint32_t side[8] = {};
+#pragma unroll
+        for (int g = 0; g < GK; ++g) {
+          const uint32_t z = high_low(fmaf(8.0f, lo_bf16(ks[g]) * fk, hi_bf16(ks[g]) * fk));
+          side[2 * g] = __byte_perm(z, z, 0x1010), side[2 * g + 1] = __byte_perm(z, z, 0x3232);  // high, high, low, low
+        }
+        *reinterpret_cast<uint4*>(sm + kSides + (q_tiles(D) + st) * kSide + side_chunk(16 * w + tk, half)) =
+            half ? make_uint4(side[4], side[5], side[6], side[7]) : make_uint4(side[0], side[1], side[2], side[3]);
+      };
+      auto put_values = [&](int st, const uint4 (&vc)[CB], const __half2 (&s)[GV], const __half2 (&b)[GV]) {
 #pragma unroll
         for (int g = 0; g < CB; ++g) {
           const uint32_t c[4] = {odd ? vc[g].y : vc[g].x, odd ? vc[g].x : vc[g].y, odd ? vc[g].w : vc[g].z, odd ? vc[g].z : vc[g].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + at_v[j] + g * kBlock64) = expand.value(c[j], s, b);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(sm + 2 * st * TILE + at_v[j] + g * kBlock64) = expand.value(c[j], s[g * GV / CB], b[g * GV / CB]);
         }
+      };
+      auto value_scales = [&](const uint32_t (&vs)[GV], __half2 (&s)[GV], __half2 (&b)[GV]) {
+#pragma unroll
+        for (int g = 0; g < GV; ++g) s[g] = __float2half2_rn(lo_bf16(vs[g]) * fv), b[g] = __float2half2_rn(hi_bf16(vs[g]) * fv);
+      };
+      auto full = [&](uint64_t* m) {  // what the warps have written may be read
         fence_async_smem();
-        bar_sync(3, 32 * kExpandWarps);
-        if (w == 0 && lane == 0) mbar_arrive(&kv_full[st]);
+        bar_sync(kBar, kGroup);
+        if (w == 0 && lane == 0) mbar_arrive(m);
+      };
+      uint4 kc[CB], vc[CB], kn[CB], vnx[CB];
+      uint32_t ks[GK], vs[GV], ksn[GK], vsn[GV];
+      __half2 v_s[GV], v_b[GV];
+      bool ok, okn;
+      int64_t at = find(walk.t0);
+      load_codes(at, 0, kc);
+      load_scales(walk.t0, at, ks, vs, ok);
+      if constexpr (kTwo) {
+        load_codes(at, kv_v_off(D), vc);
+        for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
+          if (t + 1 < walk.t1) {
+            at = find(t + 1);
+            load_codes(at, 0, kn);
+            load_codes(at, kv_v_off(D), vnx);
+            load_scales(t + 1, at, ksn, vsn, okn);
+          }
+          const int st = kt & 1;
+          bool waited = true;
+          if (kt >= 2 && w == 0) waited = mbar_wait_warp(&kv_free[st], ((kt >> 1) & 1) ^ 1);
+          if (!agree(meta[kt % kMeta], waited, ks, vs, ok)) {
+            bad = true;
+            break;
+          }
+          value_scales(vs, v_s, v_b);
+          put_keys(st, kc, ks);
+          put_values(st, vc, v_s, v_b);
+          full(&kv_full[st]);
 #pragma unroll
-        for (int g = 0; g < CB; ++g) kc[g] = kn[g], vc[g] = vnx[g];
+          for (int g = 0; g < CB; ++g) kc[g] = kn[g], vc[g] = vnx[g];
 #pragma unroll
-        for (int g = 0; g < GK; ++g) ks[g] = ksn[g];
-        vs = vsn, ok = okn;
+          for (int g = 0; g < GK; ++g) ks[g] = ksn[g];
+#pragma unroll
+          for (int g = 0; g < GV; ++g) vs[g] = vsn[g];
+          ok = okn;
+        }
+      } else {
+        // Keys of tile t, then values of tile t - 1 (kt: of tile t).  The waits say that the products which read the
+        // last ones are done: S of the tile before, O of the tile before.
+        for (int t = walk.t0; t <= walk.t1; ++t) {
+          const int64_t at_here = at;
+          if (t + 1 < walk.t1) {
+            at = find(t + 1);
+            load_codes(at, 0, kn);
+            load_scales(t + 1, at, ksn, vsn, okn);
+          }
+          if (t < walk.t1) load_codes(at_here, kv_v_off(D), vnx);
+          __half2 s_next[GV], b_next[GV];
+          if (t < walk.t1) {
+            bool waited = true;
+            if (kt >= 1 && w == 0) waited = mbar_wait_warp(&s_full[(kt - 1) & 1], (uint32_t)((kt - 1) >> 1) & 1u);
+            if (!agree(meta[kt % kMeta], waited, ks, vs, ok)) {
+              bad = true;
+              break;
+            }
+            value_scales(vs, s_next, b_next);
+            put_keys(0, kc, ks);
+            full(&kv_full[0]);
+          }
+          if (t > walk.t0) {
+            if (kt >= 2 && !group_wait(kBar, kGroup, w == 0, &o_full[0], (uint32_t)(kt - 2) & 1u, nullptr, 0)) {
+              bad = true;
+              break;
+            }
+            put_values(0, vc, v_s, v_b);
+            full(&kv_full[1]);
+          }
+          if (t == walk.t1) break;
+          ++kt;
+#pragma unroll
+          for (int g = 0; g < CB; ++g) kc[g] = kn[g], vc[g] = vnx[g];
+#pragma unroll
+          for (int g = 0; g < GK; ++g) ks[g] = ksn[g];
+#pragma unroll
+          for (int g = 0; g < GV; ++g) vs[g] = vsn[g], v_s[g] = s_next[g], v_b[g] = b_next[g];
+          ok = okn;
+        }
       }
     } while (!bad && walk.next(a));
   } else {
     // ------------------------------------------------------------- products
-    fewer_regs<kProductRegs>();
+    if constexpr (kTwo) fewer_regs<kProductRegs>();
     if (warp == kSoftWarps + kExpandWarps) {
     const uint32_t id_s = idesc_f16(128, kKeys, false, false), id_o = idesc_f16(128, D, false, true);
-    const uint64_t dq = desc_kmaj(smem_u32(sm), 128, 0), dk = desc_kmaj(smem_u32(sm) + 2 * TILE, kKeys, 0);
-    const uint64_t dv = desc_mnmaj(smem_u32(sm) + 3 * TILE, kKeys, 0);
-    const uint64_t dqs = desc_side(smem_u32(sm) + 6 * TILE), dks = desc_side(smem_u32(sm) + 6 * TILE + 2 * kSide);
-    auto scores = [&](int x, int st) {
+    const uint64_t dq = desc_kmaj(smem_u32(sm), 128, 0), dk = desc_kmaj(smem_u32(sm) + kKv, kKeys, 0);
+    const uint64_t dv = desc_mnmaj(smem_u32(sm) + kKv + TILE, kKeys, 0);
+    const uint64_t dqs = desc_side(smem_u32(sm) + kSides), dks = desc_side(smem_u32(sm) + kSides + q_tiles(D) * kSide);
+    auto scores = [&](int x, int st, int buf) {  // row tile, stage, buffer of S
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;  // 64 channels a block of the operands
-        mma_f16(tbase + 128 * x, dq + (uint32_t)((x * TILE >> 4) + off), dk + (uint32_t)((2 * st * TILE >> 4) + off), id_s, s > 0);
+        mma_f16(tbase + 128 * buf, dq + (uint32_t)((x * TILE >> 4) + off), dk + (uint32_t)((2 * st * TILE >> 4) + off), id_s, s > 0);
       }
-      mma_f16(tbase + 128 * x, dqs + (uint32_t)(x * kSide >> 4), dks + (uint32_t)(st * kSide >> 4), id_s, 1u);
-      mma_commit(&s_full[x]);
+      mma_f16(tbase + 128 * buf, dqs + (uint32_t)(x * kSide >> 4), dks + (uint32_t)(st * kSide >> 4), id_s, 1u);
+      mma_commit(&s_full[buf]);
     };
-    auto values = [&](int x, int st, bool more) {
+    auto values = [&](int x, int st, int buf, bool more) {
 #pragma unroll
       for (int s = 0; s < kKeys / 16; ++s)
-        mma_ts(tbase + kO + D * x, tbase + 128 * x + 8 * s, dv + (uint32_t)((2 * st * TILE >> 4) + s * 128), id_o,
+        mma_ts(tbase + kO + D * x, tbase + kP + kPStep * buf + 8 * s, dv + (uint32_t)((2 * st * TILE >> 4) + s * 128), id_o,
                more || s > 0 ? 1u : 0u);
     };
-    uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+    uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_o[2] = {0, 0};
     do {
       if (!walk.piece(a)) continue;
-      const int both = walk.rows_here() > 128 ? 2 : 1;
-      for (int x = 0; x < both && !bad; ++x) {
-        if (!mbar_wait_warp(&q_full[x], ph_q[x])) bad = true;
-        ph_q[x] ^= 1;
-      }
-      if (!bad && !mbar_wait_warp(&kv_full[kt & 1], (kt >> 1) & 1)) bad = true;
-      if (bad) break;
-      fence_after();
-      if (elect_one()) {
-        scores(0, kt & 1);
-        if (both == 2) scores(1, kt & 1);
-      }
-      __syncwarp();
-      for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
-        const bool more = t + 1 < walk.t1;
-        for (int x = 0; x < both; ++x) {
-          if (!mbar_wait_warp(&p_full[x], ph_p[x]) ||
-              (x == 0 && more && !mbar_wait_warp(&kv_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1))) {
+      if constexpr (kTwo) {
+        const int both = walk.rows_here() > 128 ? 2 : 1;
+        for (int x = 0; x < both && !bad; ++x) {
+          if (!mbar_wait_warp(&q_full[x], ph_q[x])) bad = true;
+          ph_q[x] ^= 1;
+        }
+        if (!bad && !mbar_wait_warp(&kv_full[kt & 1], (kt >> 1) & 1)) bad = true;
+        if (bad) break;
+        fence_after();
+        if (elect_one()) {
+          scores(0, kt & 1, 0);
+          if (both == 2) scores(1, kt & 1, 1);
+        }
+        __syncwarp();
+        for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
+          const bool more = t + 1 < walk.t1;
+          for (int x = 0; x < both; ++x) {
+            if (!mbar_wait_warp(&p_full[x], ph_p[x]) ||
+                (x == 0 && more && !mbar_wait_warp(&kv_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1))) {
+              bad = true;
+              break;
+            }
+            ph_p[x] ^= 1;
+            fence_after();
+            if (elect_one()) {
+              values(x, kt & 1, x, t > walk.t0);
+              if (x + 1 == both) mma_commit(&kv_free[kt & 1]);
+              if (kPApart && more) scores(x, (kt + 1) & 1, x);
+              if (!kPApart || !more) mma_commit(&o_full[x]);
+            }
+            __syncwarp();
+            if (!kPApart && more) {
+              if (!mbar_wait_warp(&o_full[x], ph_o[x])) {
+                bad = true;
+                break;
+              }
+              fence_after();
+              if (elect_one()) scores(x, (kt + 1) & 1, x);
+              __syncwarp();
+            }
+            if (!kPApart || !more) ph_o[x] ^= 1;
+          }
+        }
+      } else {
+        // S of two tiles ahead of the probabilities; a buffer is made anew once the product that reads P there is done
+        auto next_scores = [&](int k) {  // of key tile k (over all pieces)
+          if (!mbar_wait_warp(&kv_full[0], (uint32_t)k & 1u)) return false;
+          fence_after();
+          if (elect_one()) scores(0, 0, k & 1);
+          __syncwarp();
+          return true;
+        };
+        bad = !mbar_wait_warp(&q_full[0], ph_q[0]);
+        ph_q[0] ^= 1;
+        bad = bad || !next_scores(kt) || (walk.t0 + 1 < walk.t1 && !next_scores(kt + 1));
+        for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
+          if (!mbar_wait_warp(&p_full[kt & 1], (uint32_t)(kt >> 1) & 1u) || !mbar_wait_warp(&kv_full[1], (uint32_t)kt & 1u)) {
             bad = true;
             break;
           }
-          ph_p[x] ^= 1;
           fence_after();
           if (elect_one()) {
-            values(x, kt & 1, t > walk.t0);
-            if (x + 1 == both) mma_commit(&kv_free[kt & 1]);
-            if (more) scores(x, (kt + 1) & 1);
-            else mma_commit(&o_full[x]);
+            values(0, 0, kt & 1, t > walk.t0);
+            mma_commit(&o_full[0]);
           }
           __syncwarp();
+          if (t + 2 < walk.t1) bad = !mbar_wait_warp(&o_full[0], (uint32_t)kt & 1u) || !next_scores(kt + 2);
         }
       }
     } while (!bad && walk.next(a));
@@ -615,25 +778,45 @@ __global__ void __launch_bounds__(256) attn_prefill_combine_kernel(const __grid_
   const int4 sp = a.ws.split[first];
   const AttnRows rw = rows_of(a, sp.x);
   const int Gq = a.p.Hq / a.cache.Hkv, parts = sp.w - first + 1;
-  constexpr int V = D / 32;  // channels of a lane
+  constexpr int V = D / 32, kRows = rows_of_block(D);  // channels of a lane
+  constexpr int kParts = (kAttnSms + 31) / 32;         // parts of a lane
   for (int row = blockIdx.y * 8 + warp; row < kRows; row += gridDim.y * 8) {
     const int gr = sp.z * kRows + row;
     if (gr >= rw.rows) break;
     auto slot = [&](int i) { return (int64_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * kRows + row; };
+    // the weights 2^(m_i - m) of all parts first, a part a lane, so that the loads of the rows do not wait on one another
+    // (24 tokens over 20000, 16 / 2 heads of 256: 69 -> 56 us)
+    float2 ml[kParts];
     float m = -INFINITY, l = 0.0f, v[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) v[c] = 0.0f;
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, a.ws.ml[slot(i)].x);
-#pragma unroll 2
-    for (int i = 0; i < parts; ++i) {
-      const float2 ml = a.ws.ml[slot(i)];
-      const float f = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : exp2f(ml.x - m);
-      const float2* o = reinterpret_cast<const float2*>(a.ws.o + slot(i) * D + lane * V);
-      l = fmaf(f, ml.y, l);
+    for (int k = 0; k < kParts; ++k) {
+      const int i = 32 * k + lane;
+      ml[k] = i < parts ? a.ws.ml[slot(i)] : make_float2(-INFINITY, 0.0f);
+      m = fmaxf(m, ml[k].x);
+    }
 #pragma unroll
-      for (int c = 0; c < V / 2; ++c) {
-        const float2 y = o[c];
-        v[2 * c] = fmaf(f, y.x, v[2 * c]), v[2 * c + 1] = fmaf(f, y.y, v[2 * c + 1]);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      ml[k].x = ml[k].x == -INFINITY && ml[k].y == 0.0f ? 0.0f : exp2f(ml[k].x - m);
+      l = fmaf(ml[k].x, ml[k].y, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int c = 0; c < V; ++c) v[c] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const int here = min(32, parts - 32 * k);
+#pragma unroll 8
+      for (int i = 0; i < here; ++i) {
+        const float f = __shfl_sync(0xffffffffu, ml[k].x, i);
+        const float2* o = reinterpret_cast<const float2*>(a.ws.o + slot(32 * k + i) * D + lane * V);
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) {
+          const float2 y = o[c];
+          v[2 * c] = fmaf(f, y.x, v[2 * c]), v[2 * c + 1] = fmaf(f, y.y, v[2 * c + 1]);
+        }
       }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -652,7 +835,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   {
     LaunchScope scope(GDN_K_ATTENTION, stream);
-    attn_prefill_kernel<D><<<a.G, kThreads, bytes, stream>>>(a);
+    attn_prefill_kernel<D><<<a.G, threads_of(D), bytes, stream>>>(a);
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   LaunchScope scope(GDN_K_ATTN_COMBINE, stream);
@@ -663,7 +846,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t stream) {
-  return a.p.D == 64 ? run<64>(a, stream) : run<128>(a, stream);
+  return a.p.D == 64 ? run<64>(a, stream) : a.p.D == 128 ? run<128>(a, stream) : run<256>(a, stream);
 }
 
 }  // namespace gdn

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     s_seq[threadIdx.x] = seq_of(a.cu, a.N, t0 + threadIdx.x);
   }
   if (threadIdx.x < nt) {
-    const int n = s_seq[threadIdx.x];
+    // (a cu_seqlens that leaves a token out is not the host's copy: the token may go wrong, not the address)
+    const int n = s_seq[threadIdx.x] = min((uint32_t)s_seq[threadIdx.x], (uint32_t)a.N - 1u);
     s_at[threadIdx.x] = cache.lens[n] - (a.cu[n + 1] - (t0 + threadIdx.x));  // position in the cache; negative: not stored
   }
   if (!a.pos) __syncthreads();

@@ -184,7 +184,7 @@ class Case:
     def check(self, o, lse, skip=()):
         o, lse = o.cpu(), lse.cpu()
         assert torch.isfinite(o).all()
-        long = self.io == "bf16" and self.d <= 128 and max(self.new) * (self.hq // self.hkv) > 64
+        long = self.io == "bf16" and max(self.new) * (self.hq // self.hkv) > (64 if self.d <= 128 else 128)
         for n in range(self.N):
             a, b = int(self.cu[n]), int(self.cu[n + 1])
             if a == b or n in skip:

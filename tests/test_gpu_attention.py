@@ -438,7 +438,7 @@ def test_outputs_past_the_last_token_are_left_alone():
     assert (big_o[c.T:] == 7.0).all() and (big_l[c.T:] == 7.0).all()
 
 
-# ------------------------------------------------------------------------- the long row tiles (bf16, D up to 128)
+# ------------------------------------------------------------------------- the long row tiles (bf16)
 @pytest.mark.parametrize("d,hq,hkv,page", [(64, 4, 2, 32), (128, 6, 2, 64)])
 def test_long_tiles_masked_nan_values_reach_only_their_readers(d, hq, hkv, page):
     """A token whose value is NaN is seen by the queries from its position on and by no other."""
@@ -524,6 +524,68 @@ def test_long_tiles_captured_and_on_two_streams():
         torch.cuda.synchronize()
         for (o, l, ws), (wo, wl) in zip(outs, want):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+# heads of 256 channels: one row tile a block, two buffers of scores, two groups of values
+@pytest.mark.parametrize("new,ctx,hq,hkv,page", [([65], [0], 1, 1, 16), ([129, 1, 0, 70], [127, 300, 5, 0], 2, 2, 48),
+                                                 ([40], [1000], 16, 2, 64), ([300, 17], [2000, 900], 6, 2, 128),
+                                                 ([9, 33], [5000, 3], 8, 1, 32), ([128], [128], 1, 1, 128)])
+def test_wide_heads_against_float64(new, ctx, hq, hkv, page):
+    c = Case(new, ctx, hq, hkv, 256, page, "bf16", seed=61).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    assert torch.equal(o, c.attention()[0])
+
+
+@pytest.mark.parametrize("channel", [5, 200])
+def test_wide_heads_masked_nan_values_reach_only_their_readers(channel):
+    """A value group that stands for NaN is half of a head: the other half's outputs are numbers."""
+    new, ctx, at = 90, 37, 80
+    c = Case([new], [ctx], 6, 2, 256, 64, "bf16", seed=62)
+    c.v[0][at, 0, channel] = math.nan
+    c.fill()
+    o, lse = c.attention()
+    sees = (torch.arange(new) + ctx >= at).cuda()
+    half = slice(0, 128) if channel < 128 else slice(128, 256)
+    other = slice(128, 256) if channel < 128 else slice(0, 128)
+    assert torch.isnan(o[sees, :3, half]).all() and torch.isfinite(o[sees, :3, other]).all()
+    assert torch.isfinite(o[~sees]).all() and torch.isfinite(o[:, 3:]).all() and torch.isfinite(lse).all()
+    o2, l2 = Case([new], [ctx], 6, 2, 256, 64, "bf16", seed=62).fill().attention()
+    assert torch.equal(o[~sees], o2[~sees]) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("k_scale,v_scale,q_scale", [(1e5, 1e-6, 1e-5), (1e-8, 3e6, 1e7), (3e4, 1e30, 1e-4)])
+def test_wide_heads_magnitudes_past_fp16(k_scale, v_scale, q_scale):
+    c = Case([70, 3], [200, 500], 4, 2, 256, 32, "bf16", seed=63)
+    c.k = [(t.float() * k_scale).bfloat16() for t in c.k]
+    c.v = [(t.float() * v_scale).bfloat16() for t in c.v]
+    c.q = (c.q.float() * q_scale).bfloat16()
+    c.d_q = c.q.cuda()
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+def test_wide_heads_values_that_grow_along_the_context():
+    """The references move from tile to tile: every time the output is rescaled behind the product before it."""
+    c = Case([80], [1000], 2, 1, 256, 64, "bf16", seed=64, outlier=False)
+    grow = 10.0 ** (torch.arange(1080) // 128).float()[:, None, None]
+    c.v = [(c.v[0].float() * grow * 1e-4).bfloat16()]
+    c.k = [(c.k[0].float() * (1 + torch.arange(1080).float()[:, None, None] / 300)).bfloat16()]
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+
+def test_wide_heads_batches_of_many_and_empty_sequences():
+    new = [0, 70, 1, 65, 0, 260, 3, 128, 129] * 3
+    ctx = [5, 0, 100, 64, 0, 300, 40, 1, 0] * 3
+    c = Case(new, ctx, 4, 4, 256, 16, "bf16", seed=65).fill()
+    c.d_lens[2] = 0
+    o, lse = c.attention()
+    a = int(c.cu[2])
+    assert (o[a] == 0).all() and (lse[a] == -math.inf).all()
+    c.check(o, lse, skip=(2,))
 
 
 def test_attention_many_sequences():
