@@ -97,8 +97,9 @@ struct AttnWalk {
   __device__ __forceinline__ static int64_t div(int64_t x, int64_t y) {  // of positive numbers; 64-bit division is slow
     return ((x | y) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
   }
-  // Every thread of the block; false: nothing to do.  s_warp: a word a warp, s_found: four (the sum; the sequence, the units before it, those of a head).  Up to as many sequences as
-  // threads are looked at once; more, in rounds, twice: for the sum, then for the sequence that holds u.
+  // Every thread of the block; false: nothing to do.  s_warp: a word a warp, s_found: four (the sum; the sequence, the
+  // units before it, those of a head).  Up to as many sequences as threads are looked at once; more, in rounds, twice:
+  // for the sum, then for the sequence that holds u.
   __device__ __forceinline__ bool start(const AttnArgs& a, int threads, int64_t* s_warp, int64_t* s_found) {
     const int tid = threadIdx.x;
     int64_t total = 0, own = 0, upto = 0, head = 0;

@@ -28,7 +28,7 @@
 // Keys and values have one stage each, filled in turn: keys of t + 1 once S of t is made,
 // values of t once P V of t - 1 is.
 //
-// Measured, 2048 tokens over 6144, 24 / 2 heads: D = 128 288 us (floor 107, by the
+// Measured, 2048 tokens over 6144, 24 / 2 heads: D = 128 287 us (floor 107, by the
 // products), D = 256 487 us (floor 214; 2310 with attn_kernel).  D = 128: a tile's chain of
 // products, wake-ups, maximum and exponentials is longer than the other tile's work.
 // D = 256: the chain is a tile's expansion, with shared memory half taken by operands.
@@ -94,8 +94,8 @@ struct alignas(16) Meta {
   uint16_t v_nan[2][8];  // by value group and key: its value is NaN
 };
 
-// Eight codes as values s c + b or keys s (c - 8), in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into 1024 + 16 c, which saves their
-// shift.  The masks sit in registers whose values the compiler does not know (a kernel argument that is 0 is in them),
+// Eight codes as values s c + b or keys s (c - 8), in the order 0 4 1 5 2 6 3 7.  Nibbles 1, 3, .. are masked into
+// 1024 + 16 c, which saves their shift.  The masks sit in registers whose values the compiler does not know (a kernel argument that is 0 is in them),
 // so that one instruction takes a mask and the exponent.
 struct Expand {
   uint32_t lo, hi, magic;
@@ -188,10 +188,11 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
   constexpr bool kTwo = two_tiles(D);
   constexpr int kSoftWarps = soft_warps(D), kThreads = threads_of(D), kRows = rows_of_block(D);
   constexpr int kKv = q_tiles(D) * TILE, kSides = all_tiles(D) * TILE;  // where stages and sides begin
+  constexpr int kPSplit = kTwo ? 2 : 1;  // parts of P that are multiplied as they are written (2048 tokens over 6144: 300 -> 289 us)
   constexpr int kMeta = kTwo ? 2 : 4;  // key tiles that are spoken of at a time
   // TMEM: S of either row tile, or of either key tile in turn, at 0 and 128; O at 256 (and 256 + D).  P is in the first
   // half of its S, which is made anew only when the product that reads P is done: products of different shapes or into
-  // different columns need not run in the order of their issue.  Heads of 64 leave columns for P apart from S, and
+  // different columns need not run in the order of their issue (the wait costs 10 of 287 us; heads of 256 were wrong without).  Heads of 64 leave columns for P apart from S, and
   // nothing waits.
   constexpr uint32_t kO = 256;
   constexpr bool kPApart = D == 64;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   // two row tiles: q, s, p, o by row tile, kv by stage.  One: s and p by key tile, kv_full of the keys and of the values.
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], kv_full[2], kv_free[2], drain;
+  __shared__ uint64_t q_full[2], s_full[2], p_full[kPSplit][2], o_full[2], kv_full[2], kv_free[2], drain;
   __shared__ Meta meta[kMeta];
   __shared__ uint2 s_top[kExpandWarps];
   __shared__ int64_t s_warp[kThreads / 32], s_found[4];
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      for (int j = 0; j < kPSplit; ++j) mbar_init(&p_full[j][i], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
@@ -393,12 +394,14 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
           }
           __syncwarp();
           tmem_st16(tp + 16 * c, w);
+          if (c % (4 / kPSplit) == 4 / kPSplit - 1) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[c / (4 / kPSplit)][buf]);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       o_done += kPApart ? 1 : tiles;
       if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], (o_done - 1) & 1u, nullptr, 0)) {
@@ -680,9 +683,9 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
       mma_f16(tbase + 128 * buf, dqs + (uint32_t)(x * kSide >> 4), dks + (uint32_t)(st * kSide >> 4), id_s, 1u);
       mma_commit(&s_full[buf]);
     };
-    auto values = [&](int x, int st, int buf, bool more) {
+    auto values = [&](int x, int st, int buf, bool more, int part) {
 #pragma unroll
-      for (int s = 0; s < kKeys / 16; ++s)
+      for (int s = part * (8 / kPSplit); s < (part + 1) * (8 / kPSplit); ++s)
         mma_ts(tbase + kO + D * x, tbase + kP + kPStep * buf + 8 * s, dv + (uint32_t)((2 * st * TILE >> 4) + s * 128), id_o,
                more || s > 0 ? 1u : 0u);
     };
@@ -706,7 +709,15 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
         for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
           const bool more = t + 1 < walk.t1;
           for (int x = 0; x < both; ++x) {
-            if (!mbar_wait_warp(&p_full[x], ph_p[x]) ||
+#pragma unroll
+            for (int j = 0; j < kPSplit - 1; ++j) {
+              bad = bad || !mbar_wait_warp(&p_full[j][x], ph_p[x]);
+              if (bad) break;
+              fence_after();
+              if (elect_one()) values(x, kt & 1, x, t > walk.t0, j);
+              __syncwarp();
+            }
+            if (bad || !mbar_wait_warp(&p_full[kPSplit - 1][x], ph_p[x]) ||
                 (x == 0 && more && !mbar_wait_warp(&kv_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1))) {
               bad = true;
               break;
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
             ph_p[x] ^= 1;
             fence_after();
             if (elect_one()) {
-              values(x, kt & 1, x, t > walk.t0);
+              values(x, kt & 1, x, t > walk.t0, kPSplit - 1);
               if (x + 1 == both) mma_commit(&kv_free[kt & 1]);
               if (kPApart && more) scores(x, (kt + 1) & 1, x);
               if (!kPApart || !more) mma_commit(&o_full[x]);
@@ -745,13 +756,13 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
         ph_q[0] ^= 1;
         bad = bad || !next_scores(kt) || (walk.t0 + 1 < walk.t1 && !next_scores(kt + 1));
         for (int t = walk.t0; t < walk.t1 && !bad; ++t, ++kt) {
-          if (!mbar_wait_warp(&p_full[kt & 1], (uint32_t)(kt >> 1) & 1u) || !mbar_wait_warp(&kv_full[1], (uint32_t)kt & 1u)) {
+          if (!mbar_wait_warp(&p_full[0][kt & 1], (uint32_t)(kt >> 1) & 1u) || !mbar_wait_warp(&kv_full[1], (uint32_t)kt & 1u)) {
             bad = true;
             break;
           }
           fence_after();
           if (elect_one()) {
-            values(0, 0, kt & 1, t > walk.t0);
+            values(0, 0, kt & 1, t > walk.t0, 0);
             mma_commit(&o_full[0]);
           }
           __syncwarp();
