@@ -515,28 +515,44 @@ __global__ void __launch_bounds__(kSmallThreads, rows_blocks(MT, G))
 
 // ------------------------------------------------------------------ many rows
 // More rows (bf16 io): tcgen05 products of 128 weight rows (A) and
-// `tn` rows of x (B), in fp16.  Weights are expanded to fp16 tiles in shared
-// memory by eight warps, one of the tile's 16-row strips each; scaled by a power of two a row (q4_pack) so that
-// the row's largest value is below 2^11, a weight is off by half a step, 2^-11,
-// against 2^-8 in bf16.  x goes through x_half_kernel: fp16 with a power of two
-// a row, exact but for elements 2^-25 of the row's largest and smaller, laid out
-// as the tiles that the products read.
+// `tn` rows of x (B), in fp16.  Weights are expanded to fp16 into TMEM by eight
+// warps, one of the tile's 16-row strips each; scaled by a power of two a row
+// (q4_pack) so that the row's largest value is below 2^11, a weight is off by half a
+// step, 2^-11, against 2^-8 in bf16.  x goes through x_half_kernel: fp16 with a power
+// of two a row, exact but for elements 2^-25 of the row's largest and smaller, laid
+// out as the tiles that the products read, with the channels of a block in the order
+// in which a warp's TMEM store leaves the weights.
+//
+// Shared memory is what the products and the copies of x share: weights that went
+// through it as well took 96 KB a step of 256 rows, more than it moves in the
+// products' 512 cycles.  In TMEM they leave 256 columns: two accumulators of 128, so
+// that one tile's output overlaps the next one's products, or one of 256.
 //
 // Warp 0 loads x, warp 1 issues the products, warps 2-5 write the accumulator
-// out, warp 6 loads codes and scales, warps 7-30 expand: three groups of
+// out, warp 6 loads codes and scales, warps 8-31 expand: three groups of
 // eight, a warp each 16-row strip, take the blocks in turn, since a block's way
 // through a warp takes longer than its products.
-// Two accumulators, so that one tile's output overlaps the next one's products.
 // Rounds of whole tiles, then the remaining tiles in S slices of K each: their
 // sums go to the workspace, and the block that comes last adds them in the order
 // of the slices.
-constexpr int kGroups = 3, kExpandWarps = kGroups * kStrips, kBigThreads = (7 + kExpandWarps) * 32;
+//
+// Measured (x_half included): 2048 rows of 5120 -> 8192 150 us, 1150 TFLOP/s (weights in
+// shared memory 167, an output loop of nine instructions a value 175, rounds chosen
+// without the output's cost 164); 64 rows of 6144 -> 5120 23 us (25).  What is left:
+// output of the single accumulator 3 us a tile, x from L2 at 10 TB/s, the slices' join;
+// for few rows the handshake of a step and 9 us of start, x_half and join.  A pair of
+// blocks a tile, which halves the copies of x, took 250 us: its handshake is longer
+// than a step.
+constexpr int kGroups = 3, kExpandWarps = kGroups * kStrips, kBigThreads = (8 + kExpandWarps) * 32;
 constexpr int kBigB = kGroups, kMaxSlots = 4;  // blocks of a chunk, chunks ahead
 constexpr int kChunk = kBigB * kBlockBytes + 2 * kBigB * kGroupBytes;
-constexpr int kWStage = kTile * kBlock * 2, kMaxRing = 8;
+constexpr int kMaxRing = 8, kWAt = 256, kWCols = kBlock / 2;  // columns of TMEM where the weights begin, and of a stage of them
+// accumulators (of 128 columns, or one of 256) in front of the weights
+__host__ __device__ constexpr int big_accs(int tn) { return tn <= 128 ? 2 : 1; }
 constexpr int kBigRing = 229376, kBigSmem = kBigRing + 1024;  // chunks and stages: 224 KB
 static_assert(kBigSmem + 2048 <= 232448, "shared memory of a block");
-// chunks: many where tiles of x leave room (and weights come from memory), few beside four stages of 256 rows
+static_assert(kWAt + kMaxRing * kWCols == 512, "TMEM: accumulators, then the weights' stages");
+// chunks: many where tiles of x leave room (and weights come from memory), few beside six stages of 256 rows
 __host__ __device__ constexpr int big_slots(int tn) { return tn <= 128 ? kMaxSlots : 2; }
 
 struct BigArgs {
@@ -591,7 +607,12 @@ __global__ void __launch_bounds__(256) x_half_kernel(const __nv_bfloat16* __rest
     if (m < M && c * 8 < K) Vec16<__nv_bfloat16>::unpack(ld16(row + c * 8), v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= f;
-    *reinterpret_cast<uint4*>(xh + ((int64_t)(c >> 3) * mp + m) * 128 + (((c & 7) ^ (m & 7)) << 4)) = tc::pack8h(v);
+    // channels 16 q + 4 i .. + 3 of 64 go to 16 i + 4 q, where the weights have them
+    const uint4 h = tc::pack8h(v);
+    unsigned char* d = xh + ((int64_t)(c >> 3) * mp + m) * 128 + 8 * ((c >> 1) & 1);
+    const int at = 4 * (c & 1) + ((c >> 2) & 1);
+    *reinterpret_cast<uint2*>(d + ((at ^ (m & 7)) << 4)) = make_uint2(h.x, h.y);
+    *reinterpret_cast<uint2*>(d + (((at + 2) ^ (m & 7)) << 4)) = make_uint2(h.z, h.w);
   }
 }
 
@@ -621,6 +642,38 @@ struct Expand {
   }
 };
 
+// products with the weights (A) in TMEM; b: as in mma_f16_low
+__device__ __forceinline__ void mma_ts_low(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 y;\nmov.b64 y, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "n"(tc::kDescHigh));
+}
+// 16 TMEM lanes x 32 columns: lane (r, q) of the warp has lanes r (a, b) and r + 8 (c, d), columns 8 i + 2 q and the next
+// of each i < 4; waits until they are there
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, uint4 a, uint4 b, uint4 c, uint4 d) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(a.x), "r"(a.y), "r"(c.x), "r"(c.y), "r"(a.z), "r"(a.w), "r"(c.z), "r"(c.w), "r"(b.x), "r"(b.y), "r"(d.x), "r"(d.y),
+      "r"(b.z), "r"(b.w), "r"(d.z), "r"(d.w)
+      : "memory");
+}
+
+// 16 columns of this thread's TMEM lane, on their way until ld_wait, which names the registers that the load fills
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
 __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid_constant__ BigArgs a) {
   using namespace tc;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -628,10 +681,11 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
   __shared__ uint64_t full_c[kMaxSlots], free_c[kMaxSlots];
   __shared__ uint64_t full[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tslot;
+  __shared__ __align__(16) float s_xf[256];
   __shared__ int s_last;  // this block's slice came last: it adds the tile up
   bool bad = false;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int xbytes = a.tn * 128, stage_bytes = kWStage + xbytes;
+  const int stage_bytes = a.tn * 128, accs = big_accs(a.tn);
   const int slots = big_slots(a.tn), stages = min(kMaxRing, (kBigRing - slots * kChunk) / stage_bytes);
   unsigned char* chunks = sm + stages * stage_bytes;
   const int mt = a.mp / a.tn, tiles = mt * a.L.tiles;
@@ -685,8 +739,8 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
           break;
         }
         if (elect_one()) {
-          mbar_expect_tx(&full[s], xbytes);
-          bulk_load(sm + s * stage_bytes + kWStage, src, xbytes, &full[s]);
+          mbar_expect_tx(&full[s], stage_bytes);
+          bulk_load(sm + s * stage_bytes, src, stage_bytes, &full[s]);
         }
         __syncwarp();
         if (++s == stages) s = 0, phase ^= 1;
@@ -696,18 +750,18 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
       for (int j = max(0, i - stages); j < i; ++j) mbar_wait_warp(&full[j % stages], (j / stages) & 1, tc::kWaitTries / 64);
   } else if (warp == 1) {
     const uint32_t id = idesc_f16(kTile, a.tn, false, false);
-    const uint32_t dw = (uint32_t)desc_kmaj(smem_u32(sm), kTile, 0), dx = (uint32_t)desc_kmaj(smem_u32(sm) + kWStage, a.tn, 0);
+    const uint32_t dx = (uint32_t)desc_kmaj(smem_u32(sm), a.tn, 0);
     const int stage16 = stage_bytes >> 4;  // addresses count in 16 bytes
     int s = 0;
     uint32_t phase = 0;
     for (int j = 0; piece(j, p) && !bad; ++j) {
-      const int ab = j & 1;
-      if (j >= 2 && !mbar_wait_warp(&acc_empty[ab], ((j >> 1) & 1) ^ 1)) {
+      const int ab = j % accs;
+      if (j >= accs && !mbar_wait_warp(&acc_empty[ab], ((j / accs) & 1) ^ 1)) {
         bad = true;
         break;
       }
       fence_after();
-      const uint32_t d = tbase + 256 * ab;
+      const uint32_t d = tbase + 128 * ab;
       for (int kb = p.k0; kb < p.k1; ++kb) {
         if (!mbar_wait_warp(&full[s], phase)) {
           bad = true;
@@ -717,7 +771,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kBlock / 16; ++kk)  // 32 bytes further in each row
-            mma_f16_low(d, dw + (uint32_t)(s * stage16 + 2 * kk), dx + (uint32_t)(s * stage16 + 2 * kk), id, (kb > p.k0 || kk > 0) ? 1u : 0u);
+            mma_ts_low(d, tbase + kWAt + kWCols * s + 8 * kk, dx + (uint32_t)(s * stage16 + 2 * kk), id, (kb > p.k0 || kk > 0) ? 1u : 0u);
           mma_commit(&empty[s]);
           if (kb + 1 == p.k1) mma_commit(&acc_full[ab]);
         }
@@ -746,14 +800,15 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     }
     if (bad)  // let the copies already issued land before the block exits
       for (int j = max(0, i - slots); j < i; ++j) mbar_wait_warp(&full_c[j % slots], (j / slots) & 1, tc::kWaitTries / 64);
-  } else if (warp >= 7) {
+  } else if (warp >= 8) {
     const Expand expand(a.zero);
-    const int strip = (warp - 7) & 7, grp = (warp - 7) >> 3, r = lane >> 2, q = lane & 3;
+    // a warp writes the TMEM lanes of its number's remainder by four: two strips of 16 rows
+    const int grp = (warp - 8) >> 3, strip = 2 * (warp & 3) + ((warp >> 2) & 1), r = lane >> 2, q = lane & 3;
+    const bool polls = (warp & 7) == 0;
     const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off) + strip * kStrip + r;
     const unsigned char* code_at = chunks + grp * kBlockBytes + strip * 512 + lane * 16;
     const unsigned char* scale_at = chunks + kBigB * kBlockBytes + (strip * kStrip + r) * 4;
-    unsigned char* row = sm + strip * 2048 + r * 128;
-    const int c0 = ((2 * q) ^ r) << 4, c1 = ((2 * q + 1) ^ r) << 4;
+    const uint32_t w_at = tbase + kWAt + ((uint32_t)(16 * strip) << 16);
     int s = 0, c = 0;                    // stage of the next chunk's first block; chunk slot
     uint32_t round = 0, slot_phase = 0;  // rounds of the stages; phase of the slot
     for (int j = 0; piece(j, p) && !bad; ++j) {
@@ -765,7 +820,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         int se = s + grp;
         uint32_t re = round;
         if (se >= stages) se -= stages, ++re;
-        if (!group_wait(2 + grp, 32 * kStrips, strip == 0, &full_c[c], slot_phase, here && re > 0 ? &empty[se] : nullptr,
+        if (!group_wait(2 + grp, 32 * kStrips, polls, &full_c[c], slot_phase, here && re > 0 ? &empty[se] : nullptr,
                         (re & 1) ^ 1)) {
           bad = true;
           break;
@@ -781,15 +836,14 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
             sh[h] = __float2half2_rn(lo_bf16(v) * inv[h]);
             bh[h] = __float2half2_rn(hi_bf16(v) * inv[h]);
           }
-          unsigned char* d = row + se * stage_bytes;
-          *reinterpret_cast<uint4*>(d + c0) = expand(w.x, sh[0], bh[0]);
-          *reinterpret_cast<uint4*>(d + c1) = expand(w.y, sh[0], bh[0]);
-          *reinterpret_cast<uint4*>(d + 1024 + c0) = expand(w.z, sh[1], bh[1]);
-          *reinterpret_cast<uint4*>(d + 1024 + c1) = expand(w.w, sh[1], bh[1]);
-          fence_async_smem();
+          const uint4 o0 = expand(w.x, sh[0], bh[0]), o1 = expand(w.y, sh[0], bh[0]);  // row r, eight channels each
+          const uint4 o2 = expand(w.z, sh[1], bh[1]), o3 = expand(w.w, sh[1], bh[1]);  // row r + 8
+          fence_after();
+          tmem_st_16x8(w_at + kWCols * se, o0, o1, o2, o3);
+          fence_before();
         }
         bar_sync(2 + grp, 32 * kStrips);
-        if (strip == 0 && lane == 0) {
+        if (polls && lane == 0) {
           if (here) mbar_arrive(&full[se]);
           mbar_arrive(&free_c[c]);
         }
@@ -798,43 +852,68 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         if (++c == slots) c = 0, slot_phase ^= 1;
       }
     }
-  } else {  // warp w reads TMEM lanes 32 (w % 4) .. + 31: weight rows 32 q + lane
+  } else if (warp < 6) {  // warp w reads TMEM lanes 32 (w % 4) .. + 31: weight rows 32 q + lane
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int q = warp & 3, row = 32 * q + lane;
     const float* row_inv = reinterpret_cast<const float*>(a.packed + a.L.row_off);
     for (int j = 0; piece(j, p); ++j) {
-      const int ab = j & 1, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
+      const int ab = j % accs, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
       const bool split = p.k1 - p.k0 < a.L.blocks;
       const float wf = n < a.N ? 1.0f / __ldg(row_inv + n) : 0.0f;
-      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j >> 1) & 1, nullptr, 0)) {  // the four warps leave together
+      bar_sync(1, 128);  // the last tile's factors are read
+      for (int c = tid - 64; c < a.tn; c += 128) s_xf[c] = a.xf[m0 + c];
+      if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j / accs) & 1, nullptr, 0)) {  // the four warps leave together
         bad = true;
         break;
       }
       fence_after();
-      const uint32_t src = tbase + 256 * ab + ((uint32_t)(32 * q) << 16);
+      const uint32_t src = tbase + 128 * ab + ((uint32_t)(32 * q) << 16);
+      // 16 columns at a time, the next ones on their way
+      uint32_t raw[2][16];
+      const int cols = split ? a.tn : min(a.tn, (a.M - m0 + 15) & ~15);
+      tmem_ld16_async(src, raw[0]);
+      auto columns = [&](auto&& out) {
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = c + 16 * h;
+            if (at < cols) {
+              ld_wait(raw[h]);
+              if (at + 16 < cols) tmem_ld16_async(src + at + 16, raw[h ^ 1]);
+              out(at, raw[h]);
+            }
+          }
+        }
+      };
       if (split) {  // always a block's last piece: no other waits for the accumulator
         float* mine = a.part + (int64_t)blockIdx.x * a.tn * kTile + row;
-#pragma unroll 1
-        for (int c = 0; c < a.tn; c += 16) {
-          float v[16];
-          tmem_ld16(src + c, v);
+        columns([&](int c, const uint32_t (&v)[16]) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * kTile, v[e]);
-        }
+          for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * kTile, __uint_as_float(v[e]));
+        });
         __threadfence();
         bar_sync(1, 128);
         if (tid == 64) s_last = atomicAdd(a.count + blockIdx.x / a.S, 1) == a.S - 1;
         break;
       }
-#pragma unroll 1
-      for (int c = 0; c < a.tn && m0 + c < a.M; c += 16) {
-        float v[16];
-        tmem_ld16(src + c, v);
-        if (n < a.N)
+      __nv_bfloat16* y = a.y + (int64_t)m0 * a.N + n;
+      columns([&](int c, const uint32_t (&v)[16]) {
+        if (n >= a.N) return;
+        const int left = a.M - m0 - c;
+        auto put = [&](auto all) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (m0 + c + e < a.M) a.y[(int64_t)(m0 + c + e) * a.N + n] = __float2bfloat16_rn(v[e] * wf * a.xf[m0 + c + e]);
-      }
+          for (int e = 0; e < 16; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(&s_xf[c + e]);
+            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(v[e]) * wf * f.x, __uint_as_float(v[e + 1]) * wf * f.y);
+            if (all || e < left) y[0] = two.x;
+            if (all || e + 1 < left) y[a.N] = two.y;
+            y += 2 * (int64_t)a.N;
+          }
+        };
+        if (left >= 16) put(std::true_type{});
+        else put(std::false_type{});
+      });
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
@@ -966,7 +1045,9 @@ struct BigPlan {
   int tn, mp, full, S, grid, rem;
 };
 // Rows of x a tile, rounds of whole tiles and slices of the rest: the fewest cycles on the fullest SM.  A 64-channel
-// step takes 2 cycles a column in the products and about 300 for the expansion of its weights at least.
+// step takes 2 cycles a column in the products and about 300 for the expansion of its weights at least; the output
+// of a tile 4000 where there is one accumulator; the slices' join 16 a column and slice (1100 rows of 5120 -> 17408:
+// 167 us, with 8 of them 218).
 BigPlan big_plan(int32_t M, const Q4Layout& L) {
   const int64_t nt = L.tiles;
   BigPlan best{};
@@ -977,8 +1058,8 @@ BigPlan big_plan(int32_t M, const Q4Layout& L) {
     b.tn = tn, b.mp = (int)(mt * tn), b.full = (int)(tiles / kSms), b.rem = (int)(tiles % kSms), b.S = 1;
     if (b.rem) b.S = (int)std::min<int64_t>(std::min(kSms / b.rem, 8), std::max(1, L.blocks / 4));
     b.grid = b.full ? kSms : b.rem * b.S;
-    const double steps = b.full * (double)L.blocks + (b.rem ? (double)L.blocks / b.S + (b.S > 1 ? 4 : 0) : 0.0);
-    const double cost = steps * std::max(300, 2 * tn);
+    const double steps = b.full * (double)L.blocks + (b.rem ? (double)L.blocks / b.S : 0.0);
+    const double cost = steps * std::max(300, 2 * tn) + (big_accs(tn) == 1 ? 4000.0 * b.full : 0.0) + (b.S > 1 ? 1000.0 + 16.0 * b.S * tn : 0.0);
     if (cost < least * 0.995) least = cost, best = b;
   }
   return best;

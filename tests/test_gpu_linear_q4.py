@@ -242,3 +242,10 @@ def test_linear_q4_weights_that_are_not_finite_stay_in_their_column():
         y = run(x.cuda(), packed)
         keep = torch.arange(130) != 77
         assert torch.isnan(y[:, 77]).all() and torch.equal(y[:, keep.cuda()], clean[:, keep.cuda()])
+
+
+@pytest.mark.parametrize("M,N,K,group", [(129, 256, 512, 64), (256, 19200, 320, 32), (300, 9600, 640, 128), (600, 2500, 1288, 64),
+                                         (128, 18944, 64, 32), (255, 700, 4096, 64)])
+def test_products_with_one_and_two_accumulators(M, N, K, group):
+    """Tiles of up to 128 rows of x and of more; several tiles a block, ragged last rows and weight rows, slices."""
+    test_linear_q4_against_float64("bf16", group, M, N, K)
