@@ -538,9 +538,10 @@ __global__ void __launch_bounds__(kSmallThreads, rows_blocks(MT, G))
 //
 // Measured (x_half included): 2048 rows of 5120 -> 8192 150 us, 1150 TFLOP/s (weights in
 // shared memory 167, an output loop of nine instructions a value 175, rounds chosen
-// without the output's cost 164); 64 rows of 6144 -> 5120 23 us (25).  What is left:
-// output of the single accumulator 3 us a tile, x from L2 at 10 TB/s, the slices' join;
-// for few rows the handshake of a step and 9 us of start, x_half and join.  A pair of
+// without the output's cost 164); 64 rows of 6144 -> 5120 23 us (25).  What is left
+// beside the products, which keep the tensor pipe active for 66 %: the output of the
+// single accumulator, start, x_half and the slices' join; for few rows the handshake
+// of a step and 9 us of start, x_half and join.  A pair of
 // blocks a tile, which halves the copies of x, took 250 us: its handshake is longer
 // than a step.
 constexpr int kGroups = 3, kExpandWarps = kGroups * kStrips, kBigThreads = (8 + kExpandWarps) * 32;
