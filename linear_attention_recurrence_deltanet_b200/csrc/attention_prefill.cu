@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
   constexpr uint32_t kP = kPApart ? kO + 2 * D : 0, kPStep = kPApart ? 64 : 128;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
-  // two row tiles: q, s, p, o by row tile, kv by stage.  One: s and p by key tile, kv_full of the keys and of the values.
+  // two row tiles: q, s, p, o by row tile, kv by stage.  One: s and p by key tile, kv_full of the keys and of the values,
+  // o_full[0] of every key tile, o_full[1] of a piece's last.
   __shared__ uint64_t q_full[2], s_full[2], p_full[kPSplit][2], o_full[2], kv_full[2], kv_free[2], drain;
   __shared__ Meta meta[kMeta];
   __shared__ uint2 s_top[kExpandWarps];
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
     const uint32_t to = tbase + lanes + kO + D * x;
     unsigned char* sq = sm + x * TILE;
     const float c_log2 = fabsf(p.scale) * kLog2e;
-    uint32_t ph_s = 0, o_done = 0;  // o_done: arrivals at o_full
+    uint32_t ph_s = 0, o_done = 0;  // o_done: phases of the o_full that ends a piece
     bool late = false;  // a wait of this warp alone ran out
     do {
       if (!walk.piece(a)) continue;
@@ -403,8 +404,13 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      o_done += kPApart ? 1 : tiles;
-      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[x], (o_done - 1) & 1u, nullptr, 0)) {
+      // The products of the piece are done.  A parity tells a phase from the one before it only: with two row tiles the
+      // last S followed the product before the last (heads of 64: one phase a piece).  With one row tile it followed the
+      // product before that, whose successor may still run, and o_full[0] would pass for it; waiting for both phases in
+      // turn could miss the first, which the second may overtake once the last P is out.  So the last product of a piece
+      // completes o_full[1], one phase a piece, none of them passed over.
+      o_done += kTwo && !kPApart ? tiles : 1;
+      if (bad || !group_wait(1 + x, 128, (warp & 3) == 0, &o_full[kTwo ? x : 1], (o_done - 1) & 1u, nullptr, 0)) {
         bad = true;
         break;
       }
@@ -764,6 +770,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
           if (elect_one()) {
             values(0, 0, kt & 1, t > walk.t0, 0);
             mma_commit(&o_full[0]);
+            if (t + 1 == walk.t1) mma_commit(&o_full[1]);
           }
           __syncwarp();
           if (t + 2 < walk.t1) bad = !mbar_wait_warp(&o_full[0], (uint32_t)kt & 1u) || !next_scores(kt + 2);

@@ -656,3 +656,33 @@ def test_short_tiles_values_that_grow_and_nan_in_a_draft(d):
     o2, l2 = n.attention()
     assert torch.isnan(o2[2, 2:, :min(d, 128)]).all() and torch.equal(o2[:2], o[:2]) and torch.equal(o2[2, :2], o[2, :2])
     assert torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("new,ctx,hq,hkv", [
+    ([130], [0], 1, 1),                  # groups of one and of two key tiles
+    ([129], [127], 1, 1),                # two whole key tiles
+    ([140], [200], 2, 2),                # two and three
+    ([129, 150, 200], [40, 250, 300], 2, 1),
+    ([300], [2000], 16, 1),              # whole groups, and groups cut anywhere
+    ([20], [6000], 8, 1),                # one group over many blocks
+])
+def test_wide_heads_rows_have_all_their_products(new, ctx, hq, hkv):
+    """The rows that end a piece wait for its last product, whatever the loads beside it: copies on another stream take
+    the memory for some of the passes, and every pass has the first one's bits."""
+    c = Case(new, ctx, hq, hkv, 256, 64, "bf16", seed=66).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    side, a = torch.cuda.Stream(), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    b = torch.empty_like(a)
+    out, l2, ws = c.outputs()
+    torch.cuda.synchronize()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(300):
+        if i % 3 == 0:
+            with torch.cuda.stream(side):
+                b.copy_(a)
+        out.fill_(7.0)
+        gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, out, l2, ws)
+        differ += (out != o).sum() + (l2 != lse).sum()
+    torch.cuda.synchronize()
+    assert differ.item() == 0
