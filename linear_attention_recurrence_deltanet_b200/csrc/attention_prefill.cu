@@ -46,6 +46,7 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = 128;
+constexpr float kFar = 1048576.0f;  // a maximum whose rounding is a score's own: 2^-4 powers of two and more
 constexpr bool two_tiles(int D) { return D <= 128; }  // row tiles of a block: two, or one with two buffers of S
 constexpr int rows_of_block(int D) { return prefill_rows(D); }
 constexpr int soft_warps(int D) { return two_tiles(D) ? 8 : 4; }
@@ -182,6 +183,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int GK = D / kKGroup, GV = D / v_group(D), CB = D / 64, TILE = tile_bytes(D);
@@ -301,6 +308,12 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
       }
       float m = -INFINITY, l = 0.0f, v_unit = 1.0f;
       bool nan[GV] = {};
+      auto p_done = [&](uint64_t* full) {  // what this warp has written of P may be multiplied
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      };
       for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
         const int buf = kTwo ? x : kt & 1;
         const uint32_t ts = tbase + lanes + 128 * buf, tp = tbase + lanes + kP + kPStep * buf;
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
           for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])));
         }
         top = top == -INFINITY ? top : top * f;
-        if (__any_sync(0xffffffffu, top > m + kSlack || v_step != 1.0f)) {
+        if (__any_sync(0xffffffffu, top > m + kSlack || v_step != 1.0f || fabsf(m) >= kFar)) {
           const float m2 = fmaxf(m, top), g = m2 == m ? 1.0f : ex2(m - m2);
           m = m2;
           l *= g;
@@ -365,6 +378,34 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
               for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(z[e] * (g * v_step));
               tmem_st16(to + c0, w);
             }
+          }
+          // S f - m in one step keeps what the rounding of m left out.  That is the same for all keys of the row, and nothing
+          // beside scores of a few powers of two, but past the exponents' range where m is: from kFar on products are rounded
+          // as m was.
+          if (__any_sync(0xffffffffu, fabsf(m) >= kFar && m != -INFINITY)) {
+            ld_wait(raw[0]);
+            const float base = m == -INFINITY ? 0.0f : -m;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float z[16];
+              uint32_t w[8];
+              tmem_ld16(ts + 16 * c, z);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  v[i] = seen(16 * c + e + i) ? ex2(__fadd_rn(__fmul_rn(z[e + i], f), base)) : 0.0f;
+                  l += v[i];
+                }
+                const __half2 h = __floats2half2_rn(v[0], v[1]);
+                w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              __syncwarp();
+              tmem_st8(tp + 8 * c, w);
+              if (c % (8 / kPSplit) == 8 / kPSplit - 1) p_done(&p_full[c / (8 / kPSplit)][buf]);
+            }
+            continue;
           }
         }
         const float base = m == -INFINITY ? 0.0f : -m;
@@ -395,12 +436,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
           }
           __syncwarp();
           tmem_st16(tp + 16 * c, w);
-          if (c % (4 / kPSplit) == 4 / kPSplit - 1) {
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[c / (4 / kPSplit)][buf]);
-          }
+          if (c % (4 / kPSplit) == 4 / kPSplit - 1) p_done(&p_full[c / (4 / kPSplit)][buf]);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }

@@ -686,3 +686,28 @@ def test_wide_heads_rows_have_all_their_products(new, ctx, hq, hkv):
         differ += (out != o).sum() + (l2 != lse).sum()
     torch.cuda.synchronize()
     assert differ.item() == 0
+
+
+@pytest.mark.parametrize("q_scale", [1e5, 1e10, 1e27])
+@pytest.mark.parametrize("new,d", [(70, 64), (70, 128), (140, 256), (3, 128)])
+def test_attention_scores_far_past_the_exponents_range(new, d, q_scale):
+    """Scores of 1e6 to 1e28: a row takes the value of its largest score, and lse is that score."""
+    c = Case([new], [200], 2, 2, d, 64, "bf16", seed=67, outlier=False)
+    c.q = (c.q.float() * q_scale).bfloat16()
+    c.d_q = c.q.cuda()
+    c.fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+    k, v = quantise(c.k[0], 64)[3], quantise(c.v[0], v_group(d))[3]
+    for i in range(0, new, 7):
+        for h in range(2):
+            qa = c.q[i, h].double()
+            s = (k[:201 + i, h] @ qa) * c.scale
+            top = s.topk(2).values
+            # attention_bound: a score is off by 2^-20 of the sum of its magnitudes, which is under 8 |q|_1; a gap of 2^5
+            # leaves e^-32 of the next value, under the bound's own terms
+            if top[0] - top[1] <= 2 * 2.0 ** -20 * 8 * qa.abs().sum() * c.scale + 32:
+                continue
+            want = v[s.argmax(), h]
+            tol = 2.0 ** -8 * want.abs() + (2 * 2.0 ** -11 + 2.0 ** -19 + new * 2.0 ** -25 + 201 * 2.0 ** -25) * 2 * v.abs().max()
+            assert ((o[i, h].cpu().double() - want).abs() <= tol).all(), (i, h)
