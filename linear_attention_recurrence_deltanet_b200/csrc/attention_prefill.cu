@@ -4,12 +4,13 @@
 //
 // Operands are fp16, with powers of two over them: query rows are brought below 2^8
 // (exactly, but for elements 2^-22 of the row's largest), keys and values below
-// 2^12 by the largest of the block so far.  Keys go as s (c - 8), which is exact in
+// 2^12 by the largest of the piece so far.  Keys go as s (c - 8), which is exact in
 // 11 bits, and the rest, b + 8 s by group, times the sums of the query's groups, as
 // 16 more channels in high and low parts:
 //   q . k_t = sum_g q_g . s_tg (c_tg - 8) + (b_tg + 8 s_tg) sum(q_g),
-// so that scores, and the log of their sum, are those of fp32.  (Keys as s c + b
-// in fp16 put 2^-12 of a score into the log of a short row's sum.)  Values,
+// so that scores, and the log of their sum, are those of fp32 but for 2^-32 of the
+// piece's largest key, half a step below fp16's normal numbers.  (Keys as s c + b in
+// fp16 put 2^-12 of a score into the log of a short row's sum.)  Values,
 // s c + b, and probabilities are off by half a step of fp16, 2^-11, against 2^-8
 // in bf16, at the same rate.  A value group that stands for NaN is expanded as
 // zeros and noted by token, so that it reaches the rows that see it and no other.
@@ -88,7 +89,7 @@ __device__ __forceinline__ uint32_t high_low(float x) {
 // what the expanding warps say of a key tile
 struct alignas(16) Meta {
   float k_unit;          // a key's value = its operand times this
-  float v_unit;          // the same of the values, of this tile and all before
+  float v_unit;          // the same of the values, of this tile and the piece's before
   float v_step;          // v_unit before / after this tile: O is rescaled by it
   uint32_t rare;         // some keys have no page (1), some values are NaN (2); the four are read as one uint4
   uint8_t valid[8];      // 16 keys each: they have a page
@@ -495,8 +496,6 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
     const int w = warp - kSoftWarps, half = lane & 1, tk = lane >> 1;  // 16 keys a warp
     constexpr int kGroup = 32 * kExpandWarps, kBar = 3;
     const int tv = (tk & 8) | ((tk & 3) << 1) | ((tk >> 2) & 1);  // the token of V row tk (v_row's inverse)
-    int k_ref = -100, v_ref = -100;                               // exponents of the largest values so far
-    float k_lim = -1.0f, v_lim = -1.0f, fk = 0.0f, fv = 0.0f;     // what they hold, and their scales
     const Expand expand(a.zero);
     constexpr int kBlock64 = kKeys * 128;  // bytes of 64 channels of a tile, in either layout
     // where this lane's four chunks of 64 channels go, of keys and of values
@@ -510,6 +509,10 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
     do {
       if (!walk.piece(a)) continue;
       const int n = walk.n, h = walk.h;
+      // References: exponents of the piece's largest values so far, what they hold, and their scales.  They begin anew with
+      // every piece, or one request's magnitudes would leave the next one's values no bits.
+      int k_ref = -100, v_ref = -100;
+      float k_lim = -1.0f, v_lim = -1.0f, fk = 0.0f, fv = 0.0f;
       const int all = max(0, min(walk.rw.first + (walk.rt * kRows + walk.rows_here() - 1) / Gq, walk.rw.cap));  // keys anybody sees
       int64_t place = -1;
       // Where this warp's 16 keys of tile t are, -1: nowhere.  Every 32 tiles lane j looks the j-th of them up.

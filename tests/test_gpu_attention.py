@@ -711,3 +711,21 @@ def test_attention_scores_far_past_the_exponents_range(new, d, q_scale):
             want = v[s.argmax(), h]
             tol = 2.0 ** -8 * want.abs() + (2 * 2.0 ** -11 + 2.0 ** -19 + new * 2.0 ** -25 + 201 * 2.0 ** -25) * 2 * v.abs().max()
             assert ((o[i, h].cpu().double() - want).abs() <= tol).all(), (i, h)
+
+
+@pytest.mark.parametrize("big", [1e9, 1e30])
+@pytest.mark.parametrize("by_head", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_long_tiles_large_neighbours_leave_small_ones_alone(d, by_head, big):
+    """Requests, or key/value heads, of one call differ by many powers of two and share blocks (400 groups and more over
+    at most 148): each keeps its own bound."""
+    n, hkv = (50, 8) if by_head else (400, 1)
+    c = Case([70] * n, [60 + i % 3 for i in range(n)], hkv * (1 if d <= 128 else 2), hkv, d, 64, "bf16", seed=71)
+    for i in range(n):
+        if by_head:
+            for t in (c.k[i], c.v[i]):
+                t[:, ::3] = (t[:, ::3].float() * big).bfloat16()
+        elif i % 3 == 0:
+            c.k[i], c.v[i] = ((t.float() * big).bfloat16() for t in (c.k[i], c.v[i]))
+    c.fill()
+    c.check(*c.attention(), skip=[i for i in range(n) if (i % 25 if by_head else i % 23 > 1)])
