@@ -59,9 +59,15 @@ constexpr int kSoftRegs = 128, kExpandRegs = 80, kProductRegs = 56;
 static_assert((8 * kSoftRegs + kExpandWarps * kExpandRegs + 4 * kProductRegs) * 32 <= threads_of(128) * 96, "register split");
 static_assert(kSoftRegs >= 96 && kExpandRegs <= 96 && kProductRegs <= 96, "setmaxnreg.inc must not lower, .dec not raise");
 template <int N>
-__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void more_regs() {
+  __syncwarp();
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 template <int N>
-__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void fewer_regs() {
+  __syncwarp();
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 template <int D>
 using Walk = AttnWalk<rows_of_block(D), kKeys, 3, 3>;  // a group's queries and output cost about three tiles; at least three a block (six: 64 tokens over 500 40 -> 55 us)
 
@@ -141,6 +147,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
+// The TMEM accesses below are .sync.aligned and, unlike those of tc.cuh, do not reconverge the warp themselves, which would
+// cost 3 % of the kernel: what only some lanes do ends with a __syncwarp() before them.
 // 32 columns of this thread's lane, not waited for; ld_wait() ends all loads in flight
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
               make_uint4(side[4 * i], side[4 * i + 1], side[4 * i + 2], side[4 * i + 3]);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
+        mbar_arrive_if(&q_full[x], lane == 0);
       }
       float m = -INFINITY, l = 0.0f, v_unit = 1.0f;
       bool nan[GV] = {};
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full);
+        mbar_arrive_if(full, lane == 0);
       };
       for (int t = walk.t0; t < walk.t1; ++t, ++kt) {
         const int buf = kTwo ? x : kt & 1;
@@ -355,6 +363,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 32; ++e) cur[e] = seen(32 * c + e) ? cur[e] : 0xff800000u;
+            __syncwarp();
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])));
@@ -536,11 +545,17 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
         const int pos = t * kKeys + 16 * w;
         there = at >= 0 || pos >= all;
         const uint32_t* sc = reinterpret_cast<const uint32_t*>(a.cache.pool + at + kv_scale_off(D));
-        const bool see_k = at >= 0 && pos + tk < all, see_v = at >= 0 && pos + tv < all;  // behind the last key they may be anything
+        const bool see_k = pos + tk < all, see_v = pos + tv < all;  // behind the last key they may be anything
 #pragma unroll
-        for (int g = 0; g < GK; ++g) sk[g] = see_k ? sc[g * kKvTile + tk] : 0;
+        for (int g = 0; g < GK; ++g) {
+          const uint32_t v = at >= 0 ? sc[g * kKvTile + tk] : 0;
+          sk[g] = see_k ? v : 0;
+        }
 #pragma unroll
-        for (int g = 0; g < GV; ++g) sv[g] = see_v ? sc[(GK + g) * kKvTile + tv] : 0;
+        for (int g = 0; g < GV; ++g) {
+          const uint32_t v = at >= 0 ? sc[(GK + g) * kKvTile + tv] : 0;
+          sv[g] = see_v ? v : 0;
+        }
       };
       // Brings the references up to a tile's keys and values and fills mt; false: a wait ran out (a warp passes waited =
       // false).  Mostly the tile stays within the references and is finite, and every key has a page: one barrier says
@@ -576,6 +591,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
 #pragma unroll
             for (int g = 0; g < GV; ++g) mt.v_nan[g][w] = (uint16_t)nans[g];
           }
+          __syncwarp();
           if (bar_or(kBar, kGroup, !waited)) return false;
           const bool no_page = bar_or(kBar, kGroup, !ok), any_nan = bar_or(kBar, kGroup, any);
 #pragma unroll
@@ -590,11 +606,15 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
             mt.v_step = v_old == v_ref ? 1.0f : exp2f((float)(v_old - v_ref));
             mt.rare = (no_page ? 1u : 0u) | (any_nan ? 2u : 0u);
           }
+          __syncwarp();
           bar_sync(kBar, kGroup);  // s_top is read
         } else if (w == 0 && lane == 0) {
           mt.v_step = 1.0f, mt.rare = 0;
         }
-        if (w == 0 && lane == 0) mt.k_unit = pow2(k_ref - 11), mt.v_unit = pow2(v_ref - 11);
+        if (w == 0) {
+          if (lane == 0) mt.k_unit = pow2(k_ref - 11), mt.v_unit = pow2(v_ref - 11);
+          __syncwarp();
+        }
         return true;
       };
       auto put_keys = [&](int st, const uint4 (&kc)[CB], const uint32_t (&ks)[GK]) {
@@ -631,7 +651,7 @@ __global__ void __launch_bounds__(threads_of(D), 1) attn_prefill_kernel(const __
       auto full = [&](uint64_t* m) {  // what the warps have written may be read
         fence_async_smem();
         bar_sync(kBar, kGroup);
-        if (w == 0 && lane == 0) mbar_arrive(m);
+        if (w == 0) mbar_arrive_if(m, lane == 0);
       };
       uint4 kc[CB], vc[CB], kn[CB], vnx[CB];
       uint32_t ks[GK], vs[GV], ksn[GK], vsn[GV];

@@ -643,6 +643,8 @@ struct Expand {
   }
 };
 
+// The TMEM accesses below are .sync.aligned and, unlike those of tc.cuh, do not reconverge the warp themselves, which would
+// cost 3 % of the kernel: what only some lanes do ends with a __syncwarp() before them.
 // products with the weights (A) in TMEM; b: as in mma_f16_low
 __device__ __forceinline__ void mma_ts_low(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -844,9 +846,9 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
           fence_before();
         }
         bar_sync(2 + grp, 32 * kStrips);
-        if (polls && lane == 0) {
-          if (here) mbar_arrive(&full[se]);
-          mbar_arrive(&free_c[c]);
+        if (polls) {
+          if (here) mbar_arrive_if(&full[se], lane == 0);
+          mbar_arrive_if(&free_c[c], lane == 0);
         }
         s += min(kBigB, p.k1 - k0);
         if (s >= stages) s -= stages, ++round;
@@ -860,9 +862,10 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
     for (int j = 0; piece(j, p); ++j) {
       const int ab = j % accs, m0 = (p.tile % mt) * a.tn, n = (p.tile / mt) * kTile + row;
       const bool split = p.k1 - p.k0 < a.L.blocks;
-      const float wf = n < a.N ? 1.0f / __ldg(row_inv + n) : 0.0f;
+      const float wf = 1.0f / __ldg(row_inv + n);  // (whole tiles of them are laid out)
       bar_sync(1, 128);  // the last tile's factors are read
       for (int c = tid - 64; c < a.tn; c += 128) s_xf[c] = a.xf[m0 + c];
+      __syncwarp();
       if (!group_wait(1, 128, warp == 2, &acc_full[ab], (j / accs) & 1, nullptr, 0)) {  // the four warps leave together
         bad = true;
         break;
@@ -899,8 +902,8 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
         break;
       }
       __nv_bfloat16* y = a.y + (int64_t)m0 * a.N + n;
+      const bool ragged = n - lane + 32 > a.N;  // some of the warp's rows are past the last
       columns([&](int c, const uint32_t (&v)[16]) {
-        if (n >= a.N) return;
         const int left = a.M - m0 - c;
         auto put = [&](auto all) {
 #pragma unroll
@@ -912,12 +915,18 @@ __global__ void __launch_bounds__(kBigThreads, 1) linear_big_kernel(const __grid
             y += 2 * (int64_t)a.N;
           }
         };
-        if (left >= 16) put(std::true_type{});
-        else put(std::false_type{});
+        if (ragged) {
+          if (n < a.N) put(std::false_type{});
+          __syncwarp();
+        } else if (left >= 16) {
+          put(std::true_type{});
+        } else {
+          put(std::false_type{});
+        }
       });
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      mbar_arrive_if(&acc_empty[ab], lane == 0);
     }
   }
   const bool any_bad = sync_tc_any(bad);

@@ -200,7 +200,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int
   return __all_sync(0xffffffffu, ok);
 }
 
-// A named barrier of n threads: whether any of them passed true.
+// Named barriers of n threads, aligned like the instructions above: whole warps, converged (a branch that only some lanes
+// take is closed by __syncwarp() before them).  bar_or: whether any thread passed true.
 __device__ __forceinline__ bool bar_or(int id, int n, bool v) {
   uint32_t r;
   asm volatile(
@@ -222,6 +223,13 @@ __device__ __forceinline__ bool group_wait(int id, int n, bool polls, uint64_t* 
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
+}
+
+// The arrival of the threads that pass true, without a branch: the warp stays converged for an aligned instruction behind it.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* m, bool v) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(m)),
+               "r"((uint32_t)v)
+               : "memory");
 }
 
 // True in one lane of a converged warp.  Branching on it (rather than on a lane number) lets the compiler keep the
@@ -366,6 +374,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* m, uint32_t parity, 
 }
 // every thread of every CTA of the cluster; also a block barrier
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -2,6 +2,8 @@
 
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -280,3 +282,29 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(gdn.GdnError) as e:
             call()
         assert "CUDA" in str(e.value)
+
+
+@pytest.mark.parametrize("name", ["attention_prefill.cu", "linear_q4.cu", "tc.cuh"])
+def test_aligned_instructions_follow_a_reconvergence(name):
+    """All lanes of a warp execute an aligned instruction together: in the source, what only some lanes do (a branch on the
+    lane, on rows past the last) is closed by a reconvergence before the next one."""
+    path = os.path.join(os.path.dirname(gdn.__file__), "csrc", name)
+    lanes = re.compile(r"\b(if|for) \(.*(\blane\b|\btid\b|threadIdx|\(on\)|\bon &&|!on\b|\bn >= a\.N|\bn < a\.N)")
+    closed = re.compile(r"__syncwarp|_sync\(0xffffffffu|sync_tc|__syncthreads|mbar_wait_warp|elect_one|"
+                        r"tmem_(alloc|dealloc|ld16|ld32|st32)\(")
+    aligned = re.compile(r"\b(ld_wait|tmem_ld16_async|tmem_ld32_async|tmem_st16|tmem_st8|tmem_st_16x8|bar_or|bar_sync|"
+                         r"group_wait|p_done)\(|\.aligned;")
+    since, seen = None, 0
+    for i, line in enumerate(open(path), 1):
+        line = re.sub(r"//.*|mbar_arrive_if\(.*", "", line)  # (the arrival is predicated, not branched around)
+        if "__device__" in line or "__global__" in line:
+            since = None
+            continue
+        if closed.search(line):
+            since = None
+        if aligned.search(line):
+            seen += 1
+            assert since is None, f"{name}:{i}: aligned, behind what only some lanes do in line {since}"
+        if lanes.search(line) and not aligned.search(line) and "static_assert" not in line:
+            since = i
+    assert seen >= 3
