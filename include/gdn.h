@@ -429,8 +429,8 @@ GDN_API gdn_status gdn_project_out(const gdn_config* cfg, const void* o, int32_t
  *   draft to verify, many a prefill chunk; sequences may mix.  Scores are exact
  *   but for fp32 sums; bf16 io rounds probabilities (times the values' scales) to
  *   fp16, 2^-11 (and 2^-28 of the largest value's scale), and, where a sequence
- *   has more than 64 rows (tokens x Hq / Hkv; 128 for D = 256), the values too;
- *   fp32 io keeps 24 bits of everything.
+ *   has more than 64 rows (tokens x Hq / Hkv; 128 for D = 256), the values too,
+ *   whatever the call's other sequences have; fp32 io keeps 24 bits of everything.
  *   Workspace: gdn_attention_workspace_size() bytes for the same (cfg, total
  *   tokens, num_seqs), 256-byte aligned; it needs no initial contents and holds
  *   nothing between calls, so calls that may run at the same time need one each.

@@ -1087,8 +1087,8 @@ gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int64_t ldq,
   int dev = 0;
   if ((s = check_device(&dev)) != GDN_OK) return s;
   if (total == 0) return GDN_OK;
-  const gdn::AttnProblem p{q, o, lse, ldq, cu_seqlens_dev, (int32_t)total, num_seqs, cfg->num_q_heads, cfg->head_dim,
-                           max_len, cfg->softmax_scale, cfg->io_dtype == GDN_BF16};
+  const gdn::AttnProblem p{q, o, lse, ldq, cu_seqlens_dev, cu_seqlens_host, (int32_t)total, num_seqs, cfg->num_q_heads,
+                           cfg->head_dim, cfg->softmax_scale, cfg->io_dtype == GDN_BF16};
   cudaError_t e = gdn::launch_attention(p, c, workspace, g_status_ptr[dev], (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attention launch");
 }

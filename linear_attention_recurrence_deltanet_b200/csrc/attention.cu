@@ -674,13 +674,30 @@ AttnWorkspace ws_at(const WsLayout& w, void* ws) {
   return AttnWorkspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)};
 }
 
-// bf16 io: sequences with more rows a key/value head than this run the long row tiles (16 / 2 heads of 256 over 20000
+// bf16 io: sequences with more rows a key/value head than this take the long row tiles (16 / 2 heads of 256 over 20000
 // tokens: 72 rows 45 us here and 55 there, 136 rows 65 and 56)
 constexpr int prefill_from(int D) { return D <= 128 ? 64 : 128; }
 
+// What a call's sequences ask for: of those with up to `border` rows a key/value head, their rows, how many and the longest;
+// whether there are others.
+struct Split {
+  int64_t rows;
+  int32_t seqs, longest;
+  bool longer;
+};
+Split split_at(const AttnProblem& p, int32_t Hkv, int64_t border) {
+  Split s{};
+  for (int32_t n = 0; n < p.N; ++n) {
+    const int64_t rows = (int64_t)(p.cu_host[n + 1] - p.cu_host[n]) * (p.Hq / Hkv);
+    if (rows > border) s.longer = true;
+    else if (rows > 0) s.rows += rows, ++s.seqs, s.longest = std::max(s.longest, (int32_t)rows);
+  }
+  return s;
+}
+
 template <typename T, int D, int RT>
-cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status, cudaStream_t stream) {
-  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D, RT), 16), ws), grid_of(D, RT), status, 0};
+cudaError_t run(const AttnProblem& p, const KvCache& cache, const Split& s, void* ws, int32_t* status, cudaStream_t stream) {
+  const AttnArgs a{p, cache, ws_at(ws_layout(D, grid_of(D, RT), 16), ws), grid_of(D, RT), 1, s.longest, status, 0};
   constexpr int bytes = smem_bytes(D, RT, sizeof(T) == 4 ? 3 : 1);
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -690,9 +707,8 @@ cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* s
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // as many split groups as there are groups, or blocks; rows of the longest sequence's tile
-  const int Gq = p.Hq / cache.Hkv;
-  const int64_t groups = ((int64_t)p.T * Gq / RT + p.N) * cache.Hkv;
-  const int rows = (int)std::min<int64_t>(RT, (int64_t)p.max_q * Gq);
+  const int64_t groups = (s.rows / RT + s.seqs) * cache.Hkv;
+  const int rows = std::min(RT, s.longest);
   const int64_t x = std::min<int64_t>(groups, a.G);
   // few rows have many parts: the channels go to D / 32 blocks (131072 tokens, 24 rows: 15.6 -> 6.3 us); many rows have
   // few, and the blocks that find no group cost more (64 sequences of 8 heads: 6.6 us against 14.4)
@@ -703,11 +719,11 @@ cudaError_t run(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* s
 }
 
 template <int D>
-cudaError_t run_d(const AttnProblem& p, const KvCache& c, void* ws, int32_t* status, cudaStream_t st) {
-  if (!p.bf16) return run<float, D, 16>(p, c, ws, status, st);
+cudaError_t run_d(const AttnProblem& p, const KvCache& c, const Split& s, void* ws, int32_t* status, cudaStream_t st) {
+  if (!p.bf16) return run<float, D, 16>(p, c, s, ws, status, st);
   // 8-row tiles leave the other half of the products' rows to the low parts of the probabilities
-  if ((int64_t)p.max_q * (p.Hq / c.Hkv) <= 8) return run<__nv_bfloat16, D, 8>(p, c, ws, status, st);
-  return run<__nv_bfloat16, D, 16>(p, c, ws, status, st);
+  if (s.longest <= 8) return run<__nv_bfloat16, D, 8>(p, c, s, ws, status, st);
+  return run<__nv_bfloat16, D, 16>(p, c, s, ws, status, st);
 }
 
 }  // namespace
@@ -720,11 +736,17 @@ size_t attention_ws_bytes(int32_t T, int32_t, int32_t Hq, int32_t Hkv, int32_t D
 
 cudaError_t launch_attention(const AttnProblem& p, const KvCache& cache, void* ws, int32_t* status,
                              cudaStream_t stream) {
-  if (p.bf16 && (int64_t)p.max_q * (p.Hq / cache.Hkv) > prefill_from(p.D))
-    return launch_attention_prefill(AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, prefill_rows(p.D)), ws), kAttnSms, status, 0}, stream);
-  if (p.D == 64) return run_d<64>(p, cache, ws, status, stream);
-  if (p.D == 128) return run_d<128>(p, cache, ws, status, stream);
-  return run_d<256>(p, cache, ws, status, stream);
+  const int32_t border = p.bf16 ? prefill_from(p.D) : 0x7fffffff;
+  const Split s = split_at(p, cache.Hkv, border);
+  // one after the other: both may use the workspace
+  if (s.longer) {
+    const cudaError_t e = launch_attention_prefill(
+        AttnArgs{p, cache, ws_at(ws_layout(p.D, kAttnSms, prefill_rows(p.D)), ws), kAttnSms, border + 1, 0x7fffffff, status, 0}, stream);
+    if (e != cudaSuccess || s.seqs == 0) return e;
+  }
+  if (p.D == 64) return run_d<64>(p, cache, s, ws, status, stream);
+  if (p.D == 128) return run_d<128>(p, cache, s, ws, status, stream);
+  return run_d<256>(p, cache, s, ws, status, stream);
 }
 
 }  // namespace gdn

@@ -8,6 +8,10 @@
 // last row sees.  The units of all groups, end to end, are cut into equal quotas,
 // so that ragged lengths fill the SMs evenly.  A group that crosses blocks leaves
 // unnormalised partial rows in the workspace for a combine kernel.
+//
+// A launch takes the sequences whose rows a key/value head lie in its range and passes
+// over the others, which have no units in it: so a sequence's rounding, and what a short
+// one computes, does not depend on whether the call holds long ones.
 #pragma once
 
 #include "../../include/gdn.h"
@@ -33,6 +37,7 @@ struct AttnArgs {
   KvCache cache;
   AttnWorkspace ws;
   int32_t G;  // blocks
+  int32_t least, most;  // rows a key/value head of the sequences that this launch takes
   int32_t* status;
   uint32_t zero;  // 0, unknown to the compiler
 };
@@ -52,13 +57,14 @@ __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w 
 
 // rows of a sequence's query tiles and the keys they see
 struct AttnRows {
-  int32_t rows;   // new * (Hq / Hkv)
+  int32_t rows;   // new * (Hq / Hkv); 0 where another launch takes the sequence
   int32_t first;  // keys that query token 0 sees: len - new + 1
   int32_t cap;    // positions that the page table's row covers
 };
 __device__ __forceinline__ AttnRows rows_of(const AttnArgs& a, int n) {
   const int nw = a.p.cu[n + 1] - a.p.cu[n];
-  return AttnRows{nw * (a.p.Hq / a.cache.Hkv), a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
+  const int rows = nw * (a.p.Hq / a.cache.Hkv);
+  return AttnRows{rows >= a.least && rows <= a.most ? rows : 0, a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
 }
 
 // inclusive sum over the block's threads
@@ -162,8 +168,7 @@ struct AttnWalk {
     rt = 0;
     if (++h == a.cache.Hkv) {
       h = 0;
-      do ++n; while (a.p.cu[n + 1] == a.p.cu[n]);  // a sequence without queries has no units
-      rw = rows_of(a, n);
+      do rw = rows_of(a, ++n); while (rw.rows == 0);  // a sequence without rows here has no units
     }
     return true;
   }
@@ -192,7 +197,7 @@ __device__ __forceinline__ int split_group(const AttnArgs& a, int x, int* s_coun
   return *s_first;
 }
 
-// attention_prefill.cu: bf16 io, long row tiles
+// attention_prefill.cu: bf16 io, the sequences with more than prefill_from(D) rows
 constexpr int prefill_rows(int D) { return D <= 128 ? 256 : 128; }  // a block's
 cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t stream);
 

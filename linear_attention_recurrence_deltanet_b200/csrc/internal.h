@@ -183,8 +183,8 @@ struct AttnProblem {
   void* o;
   float* lse;         // may be NULL
   int64_t ldq;        // elements between tokens of q
-  const int32_t* cu;  // [N + 1], device
-  int32_t T, N, Hq, D, max_q;
+  const int32_t *cu, *cu_host;  // [N + 1], on the device and here
+  int32_t T, N, Hq, D;
   float scale;
   bool bf16;
 };

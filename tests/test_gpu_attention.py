@@ -729,3 +729,41 @@ def test_long_tiles_large_neighbours_leave_small_ones_alone(d, by_head, big):
             c.k[i], c.v[i] = ((t.float() * big).bfloat16() for t in (c.k[i], c.v[i]))
     c.fill()
     c.check(*c.attention(), skip=[i for i in range(n) if (i % 25 if by_head else i % 23 > 1)])
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 6, 2), (256, 8, 1)])
+@pytest.mark.parametrize("short", [[1, 1, 1, 1, 1], [1, 0, 4, 2, 7]])
+def test_attention_short_sequences_beside_prompts(d, hq, hkv, short):
+    """Each sequence of a call is rounded as it is alone: the ones and the drafts have the bits of a call without the
+    prompts, the prompts those of a call without the others, in any order and captured."""
+    longs, at = [150, 40 if d > 64 else 90], (1, 3)
+    new = list(short)
+    for i, x in zip(at, longs):
+        new.insert(i, x)
+    ctx = [500, 300, 17, 40, 900, 0, 64]
+    c = Case(new, ctx, hq, hkv, d, 32, "bf16", seed=81).fill()
+    o, lse = c.attention()
+    c.check(o, lse)
+
+    def part(keep):
+        cu = np.concatenate(([0], np.cumsum([new[i] for i in keep]))).astype(np.int32)
+        rows = torch.cat([torch.arange(int(c.cu[i]), int(c.cu[i + 1])) for i in keep]).cuda()
+        q, T = c.d_q[rows].contiguous(), int(cu[-1])
+        po = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        pl = torch.full((T, hq), 7.0, device="cuda")
+        ws = torch.empty(max(256, gdn.attention_workspace_size(c.cfg, T, len(keep))), dtype=torch.uint8, device="cuda")
+        gdn.attention(c.cfg, q, torch.from_numpy(cu).cuda(), cu, c.d_lens[keep].contiguous(), c.pool,
+                      c.d_table[keep].contiguous(), po, pl, ws)
+        assert torch.equal(po, o[rows]) and torch.equal(pl, lse[rows])
+
+    part([i for i in range(7) if i not in at])
+    part(list(at))
+    o2, l2, ws = c.outputs()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        gdn.attention(c.cfg, c.d_q, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, o2, l2, ws)
+    for _ in range(3):
+        o2.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, o) and torch.equal(l2, lse)
