@@ -493,7 +493,9 @@ GDN_API gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int6
  * group is 32, 64 or 128; K a positive multiple of 8, M, N >= 0.  X [M, K] and
  * Y [M, N] are dense in io_dtype; sums are fp32.  Products are exact for fp32 io
  * and for up to 16 rows of bf16 (32 for small weights); more rows round the
- * weights to fp16, 2^-11 of each, with powers of two over rows of W and of X.
+ * weights to fp16, 2^-11 of each, with powers of two over rows of W and of X
+ * (a weight under 2^-36 of its row's largest is 0).  Infinities and NaN in X
+ * reach the results of their row as in the formula, in W those of their column.
  *
  * gdn_q4_pack: lays a weight out once for gdn_linear_q4.  codes
  *   [N, G * group / 2] bytes (G = ceil(K / group)): channel 2i in the low half

@@ -249,3 +249,31 @@ def test_linear_q4_weights_that_are_not_finite_stay_in_their_column():
 def test_products_with_one_and_two_accumulators(M, N, K, group):
     """Tiles of up to 128 rows of x and of more; several tiles a block, ragged last rows and weight rows, slices."""
     test_linear_q4_against_float64("bf16", group, M, N, K)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 72), (5, 40, 264), (8, 1000, 128), (12, 257, 1096), (20, 70, 136), (32, 300, 512)])
+def test_linear_q4_infinities_and_the_largest_numbers(io, group, M, N, K):
+    """Few rows: an infinity in x gives the formula's infinity or NaN, and a value near the type's largest its product."""
+    code, scale, bias, w = weight(N, K, group, M + N)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(DT[io])
+    clean = x.clone()
+    x[0, 7] = float("inf")
+    if M > 2:
+        x[1, K - 1] = -float("inf")
+        x[2, 3], x[2, 9] = float("inf"), -float("inf")
+    if M > 4:
+        x[3, 0] = float("nan")
+        x[4, K // 2] = 3.3e38  # weights are below 1: the product is within the type
+    ref, mag_b, mag_f = product(x, code, scale, bias, group)
+    y = run(x.cuda(), w).cpu().double()
+    assert torch.equal(torch.isnan(y), torch.isnan(ref))
+    assert torch.equal(y[torch.isinf(ref)], ref[torch.isinf(ref)])
+    rows = [m for m in range(M) if not (m == 0 or M > 2 and m < 3 or M > 4 and m < 5)]
+    assert torch.equal(run(clean.cuda(), w).cpu().double()[rows], y[rows])
+    if M > 4:
+        # a sum that passes fp32 is formed in fp64 and rounded to fp32 (2^-24 of it) and to the io type; one that does not is
+        # the kernel's own, off by 2^-20 of its magnitudes at most (test_linear_q4_against_float64)
+        tol = (U[io] + 2.0 ** -23) * ref[4].abs() + 2.0 ** -20 * (mag_f if io == "f32" else mag_b)[4]
+        assert ((y[4] - ref[4]).abs() <= tol).all()
