@@ -33,7 +33,9 @@ constexpr int kGroupUnits = 20;  // what a group costs beside its tiles, in tile
 constexpr int kMinUnits = 20;    // the least quota
 
 constexpr int stages(int D) { return D == 64 ? 8 : 4; }
-constexpr int blocks_per_sm(int D, int RT) { return D == 256 ? (RT == 8 ? 3 : 2) : RT == 8 ? 4 : 3; }
+// what registers and shared memory allow (all_fit below; a third block of 256 x 8 rows waited for a place, and every quota
+// was two thirds of one: 64 requests of 16 / 2 heads of 256 68.7 us, two blocks 51.8)
+constexpr int blocks_per_sm(int D, int RT) { return D == 256 ? 2 : RT == 8 ? 4 : 3; }
 // queries in shared memory where a warp's copy would take too many registers
 constexpr bool q_in_smem(int D, int RT, int TQ) { return D * TQ * (RT / 8) > 128; }
 constexpr int smem_bytes(int D, int RT, int TQ) {
@@ -655,6 +657,11 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
 }
 
 int grid_of(int D, int RT) { return kAttnSms * blocks_per_sm(D, RT); }
+// the quotas count on a place for every block: 228 KB an SM, 1 KB of each block the driver's
+constexpr bool all_fit(int D, int RT, int TQ) { return blocks_per_sm(D, RT) * (smem_bytes(D, RT, TQ) + 1024 + 1024) <= 228 * 1024; }
+static_assert(all_fit(64, 8, 1) && all_fit(128, 8, 1) && all_fit(256, 8, 1), "8-row tiles");
+static_assert(all_fit(64, 16, 1) && all_fit(128, 16, 1) && all_fit(256, 16, 1), "16-row tiles");
+static_assert(all_fit(64, 16, 3) && all_fit(128, 16, 3) && all_fit(256, 16, 3), "16-row tiles, fp32");
 static_assert(kAttnSms * blocks_per_sm(64, 8) <= kMaxBlocks, "split_group looks at kSplitPer blocks a thread");
 
 struct WsLayout {
