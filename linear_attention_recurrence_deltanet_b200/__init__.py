@@ -542,7 +542,8 @@ class Q4Weight:
 
 def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     """gdn_q4_pack: codes uint8 [N, ceil(K / group) * group / 2] (channel 2i in the low half of byte i), scales and
-    biases bf16 [N, ceil(K / group)]; a code c stands for scale * c + bias."""
+    biases bf16 [N, ceil(K / group)]; a code c stands for scale * c + bias.  The packed weight is allocated on `stream`, as
+    any tensor made there: another stream waits for it before it reads, and the caller keeps it until it has."""
     import torch
     dev, st = _device(codes, stream)
     N = codes.shape[0]
@@ -551,7 +552,9 @@ def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     G = -(-K // group)
     _need(tuple(codes.shape) == (N, G * group // 2), f"codes must be [{N}, {G * group // 2}], got {list(codes.shape)}")
     _need(tuple(scales.shape) == (N, G) and tuple(biases.shape) == (N, G), f"scales and biases must be [{N}, {G}]")
-    data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
+    # from the memory of the stream that writes it: what the current stream has freed may still be read there
+    with torch.cuda.stream(torch.cuda.ExternalStream(st, dev) if st != _Torch.raw_stream(dev) else None):
+        data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
     _check(lib().gdn_q4_pack(_ptr(codes, dev, "codes", _Torch.u8), _ptr(scales, dev, "scales", _Torch.bf16),
                              _ptr(biases, dev, "biases", _Torch.bf16), N, K, group, data.data_ptr(), st))
     return Q4Weight(data, N, K, group)

@@ -277,3 +277,29 @@ def test_linear_q4_infinities_and_the_largest_numbers(io, group, M, N, K):
         # the kernel's own, off by 2^-20 of its magnitudes at most (test_linear_q4_against_float64)
         tol = (U[io] + 2.0 ** -23) * ref[4].abs() + 2.0 ** -20 * (mag_f if io == "f32" else mag_b)[4]
         assert ((y[4] - ref[4]).abs() <= tol).all()
+
+
+def test_q4_pack_on_another_stream_takes_no_memory_in_use():
+    """What the current stream has freed may still be in use there: a weight packed on another stream does not lie in it."""
+    N, K, group = 2048, 2048, 64
+    g = torch.Generator().manual_seed(5)
+    args = [torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).cuda(),
+            (torch.rand(N, K // group, generator=g) * 0.01).bfloat16().cuda(),
+            torch.randn(N, K // group, generator=g).bfloat16().cuda()]
+    want = gdn.q4_pack(*args, K, group)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = torch.zeros(want.data.numel(), dtype=torch.uint8, device="cuda")
+    at = held.data_ptr()
+    big = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        big.add_(1)
+    held.add_(big[:held.numel()])  # pending: behind the passes over `big`
+    del held
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        w = gdn.q4_pack(*args, K, group, stream=stream)
+        assert not at <= w.data.data_ptr() < at + w.data.numel()
+        torch.cuda.synchronize()
+        assert torch.equal(w.data, want.data)
+    assert torch.equal(gdn.q4_pack(*args, K, group).data, want.data)
