@@ -490,7 +490,7 @@ GDN_API gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int6
  * Projections with 4-bit weights, group scales and biases ("Q4", issue #88,
  * Scope; affine Q4 weights, issue #95, implementation comment):
  *   Y[m, n] = sum_k X[m, k] * w[n, k],  w[n, k] = scale[n, k / group] * code[n, k] + bias[n, k / group]
- * group is 32, 64 or 128; K a positive multiple of 8, M, N >= 0.  X [M, K] and
+ * group is 32, 64 or 128; K a positive multiple of 8, M, N >= 0, each at most 2^30.  X [M, K] and
  * Y [M, N] are dense in io_dtype; sums are fp32.  Products are exact for fp32 io
  * and for up to 16 rows of bf16 (32 for small weights); more rows round the
  * weights to fp16, 2^-11 of each, with powers of two over rows of W and of X

@@ -903,10 +903,19 @@ gdn_status check_plan(const gdn_rope_plan* p, int32_t head_dim) {
   return GDN_OK;
 }
 
+constexpr int32_t kMaxQ4 = 1 << 30;  // of M, N and K: what rounds them up to whole tiles stays within int32
+
 gdn_status check_q4(int32_t N, int32_t K, int32_t group) {
   if (N < 0) return fail(GDN_E_INVAL, "N = %d (must be >= 0)", N);
+  if (N > kMaxQ4 || K > kMaxQ4) return fail(GDN_E_UNSUPPORTED, "N = %d, K = %d (at most %d)", N, K, kMaxQ4);
   if (K <= 0 || K % 8 != 0) return fail(GDN_E_INVAL, "K = %d must be a positive multiple of 8", K);
   if (group != 32 && group != 64 && group != 128) return fail(GDN_E_UNSUPPORTED, "group %d (32, 64 or 128)", group);
+  return GDN_OK;
+}
+
+gdn_status check_q4_rows(int32_t M) {
+  if (M < 0) return fail(GDN_E_INVAL, "M = %d (must be >= 0)", M);
+  if (M > kMaxQ4) return fail(GDN_E_UNSUPPORTED, "M = %d (at most %d)", M, kMaxQ4);
   return GDN_OK;
 }
 
@@ -1120,7 +1129,7 @@ gdn_status gdn_linear_q4_workspace_size(int32_t M, int32_t N, int32_t K, int32_t
                                         size_t* bytes) {
   gdn_status s;
   if ((s = check_q4(N, K, group)) != GDN_OK || (s = check_io_dtype(io_dtype)) != GDN_OK) return s;
-  if (M < 0) return fail(GDN_E_INVAL, "M = %d (must be >= 0)", M);
+  if ((s = check_q4_rows(M)) != GDN_OK) return s;
   if (!bytes) return fail(GDN_E_INVAL, "bytes is NULL");
   *bytes = gdn::linear_q4_ws_bytes(M, N, K, group, io_dtype == GDN_BF16);
   return GDN_OK;
@@ -1130,7 +1139,7 @@ gdn_status gdn_linear_q4(int32_t io_dtype, const void* x, int32_t M, int32_t K, 
                          int32_t group, void* y, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
   gdn_status s;
   if ((s = check_q4(N, K, group)) != GDN_OK || (s = check_io_dtype(io_dtype)) != GDN_OK) return s;
-  if (M < 0) return fail(GDN_E_INVAL, "M = %d (must be >= 0)", M);
+  if ((s = check_q4_rows(M)) != GDN_OK) return s;
   if (M > 0 && N > 0) {
     if ((s = check_ptr(x, "x")) != GDN_OK || (s = check_ptr(packed, "packed")) != GDN_OK) return s;
     if (!y || ((uintptr_t)y & (io_dtype == GDN_BF16 ? 1u : 3u)))

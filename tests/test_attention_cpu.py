@@ -308,3 +308,18 @@ def test_aligned_instructions_follow_a_reconvergence(name):
         if lanes.search(line) and not aligned.search(line) and "static_assert" not in line:
             since = i
     assert seen >= 3
+
+
+def test_linear_sizes_past_the_limit_are_refused():
+    """Sizes whose rounding up to whole tiles would leave int32."""
+    h, L, size = Host(), gdn.lib(), ctypes.c_size_t(7)
+    for N, K in ((2 ** 31 - 1, 8), (16, 2 ** 31 - 8), (2 ** 30 + 1, 8), (16, 2 ** 30 + 8)):
+        refused(L.gdn_q4_packed_bytes(N, K, 32, ctypes.byref(size)), f"N = {N}", -2)
+        refused(L.gdn_q4_pack(h.p, h.p, h.p, N, K, 32, h.p, None), f"N = {N}", -2)
+        refused(L.gdn_linear_q4_workspace_size(4, N, K, 32, 1, ctypes.byref(size)), f"N = {N}", -2)
+        refused(L.gdn_linear_q4(1, h.p, 4, K, h.p, N, 32, h.p, h.p, 1 << 40, None), f"N = {N}", -2)
+    for M in (2 ** 31 - 1, 2 ** 30 + 1):
+        refused(L.gdn_linear_q4_workspace_size(M, 16, 64, 64, 1, ctypes.byref(size)), f"M = {M}", -2)
+        refused(L.gdn_linear_q4(1, h.p, M, 64, h.p, 16, 64, h.p, h.p, 1 << 40, None), f"M = {M}", -2)
+    assert size.value == 7 and h.untouched()
+    assert L.gdn_q4_packed_bytes(2 ** 30, 8, 32, ctypes.byref(size)) == 0 and size.value == 2 ** 30 * (32 + 8 + 4)
