@@ -546,6 +546,7 @@ def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     any tensor made there: another stream waits for it before it reads, and the caller keeps it until it has."""
     import torch
     dev, st = _device(codes, stream)
+    _need(codes.dim() == 2, f"codes must be [N, ceil(K / group) * group / 2], got {list(codes.shape)}")
     N = codes.shape[0]
     size = ctypes.c_size_t()
     _check(lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(size)))

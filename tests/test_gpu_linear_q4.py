@@ -303,3 +303,12 @@ def test_q4_pack_on_another_stream_takes_no_memory_in_use():
         torch.cuda.synchronize()
         assert torch.equal(w.data, want.data)
     assert torch.equal(gdn.q4_pack(*args, K, group).data, want.data)
+
+
+@pytest.mark.parametrize("shape", [(), (64,), (2, 4, 32)])
+def test_q4_pack_refuses_codes_that_are_no_matrix(shape):
+    codes = torch.zeros(shape, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(2, 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.q4_pack(codes, scales, scales, 64, 64)
+    assert e.value.name == "GDN_E_INVAL"
