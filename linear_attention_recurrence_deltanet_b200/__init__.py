@@ -540,6 +540,18 @@ class Q4Weight:
         self.data, self.N, self.K, self.group = data, N, K, group
 
 
+_Q4_BYTES = {}  # gdn_q4_packed_bytes by (N, K, group)
+
+
+def _q4_bytes(N: int, K: int, group: int) -> int:
+    size = _Q4_BYTES.get((N, K, group))
+    if size is None:
+        out = ctypes.c_size_t()
+        _check(lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(out)))
+        size = _Q4_BYTES[N, K, group] = out.value
+    return size
+
+
 def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     """gdn_q4_pack: codes uint8 [N, ceil(K / group) * group / 2] (channel 2i in the low half of byte i), scales and
     biases bf16 [N, ceil(K / group)]; a code c stands for scale * c + bias.  The packed weight is allocated on `stream`, as
@@ -548,14 +560,13 @@ def q4_pack(codes, scales, biases, K: int, group: int, stream=None) -> Q4Weight:
     dev, st = _device(codes, stream)
     _need(codes.dim() == 2, f"codes must be [N, ceil(K / group) * group / 2], got {list(codes.shape)}")
     N = codes.shape[0]
-    size = ctypes.c_size_t()
-    _check(lib().gdn_q4_packed_bytes(N, K, group, ctypes.byref(size)))
+    size = _q4_bytes(N, K, group)
     G = -(-K // group)
     _need(tuple(codes.shape) == (N, G * group // 2), f"codes must be [{N}, {G * group // 2}], got {list(codes.shape)}")
     _need(tuple(scales.shape) == (N, G) and tuple(biases.shape) == (N, G), f"scales and biases must be [{N}, {G}]")
     # from the memory of the stream that writes it: what the current stream has freed may still be read there
     with torch.cuda.stream(torch.cuda.ExternalStream(st, dev) if st != _Torch.raw_stream(dev) else None):
-        data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
+        data = torch.empty(size, dtype=torch.uint8, device=codes.device)
     _check(lib().gdn_q4_pack(_ptr(codes, dev, "codes", _Torch.u8), _ptr(scales, dev, "scales", _Torch.bf16),
                              _ptr(biases, dev, "biases", _Torch.bf16), N, K, group, data.data_ptr(), st))
     return Q4Weight(data, N, K, group)
@@ -577,8 +588,8 @@ def linear_q4(x, w: Q4Weight, y, workspace=None, stream=None):
     if y.shape != (M, N):
         raise GdnError(-1, f"y must be [{M}, {N}], got {list(y.shape)}")
     pw, nw = (None, 0) if workspace is None else (_ptr(workspace, dev, "workspace", _Torch.u8), workspace.numel())
-    _check(lib().gdn_linear_q4(io, _ptr(x, dev, "x", dt), M, K, _ptr(w.data, dev, "w", _Torch.u8), N, w.group,
-                               _ptr(y, dev, "y", dt), pw, nw, st))
+    pd = _ptr(w.data, dev, "w", _Torch.u8, _q4_bytes(N, K, w.group))
+    _check(lib().gdn_linear_q4(io, _ptr(x, dev, "x", dt), M, K, pd, N, w.group, _ptr(y, dev, "y", dt), pw, nw, st))
 
 
 def state_blob_size(cfg) -> int:

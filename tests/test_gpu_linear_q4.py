@@ -312,3 +312,16 @@ def test_q4_pack_refuses_codes_that_are_no_matrix(shape):
     with pytest.raises(gdn.GdnError) as e:
         gdn.q4_pack(codes, scales, scales, 64, 64)
     assert e.value.name == "GDN_E_INVAL"
+
+
+@pytest.mark.parametrize("N,K,group", [(256, 128, 64), (128, 192, 64), (128, 128, 32)])
+def test_linear_q4_refuses_a_weight_with_too_few_bytes(N, K, group):
+    """Packed bytes that a program has kept, under other sizes than they were packed for."""
+    _, _, _, w = weight(128, 128, 64, 10)
+    x = torch.zeros(2, K, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.linear_q4(x, gdn.Q4Weight(w.data, N, K, group), torch.empty(2, N, dtype=torch.bfloat16, device="cuda"))
+    assert e.value.name == "GDN_E_INVAL" and "w has" in str(e.value)
+    kept = gdn.Q4Weight(w.data, 128, 128, 64)
+    x = torch.randn(2, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    assert torch.equal(run(x, kept), run(x, w))
