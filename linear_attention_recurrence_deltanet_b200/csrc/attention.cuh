@@ -64,7 +64,7 @@ struct AttnRows {
 __device__ __forceinline__ AttnRows rows_of(const AttnArgs& a, int n) {
   const int nw = a.p.cu[n + 1] - a.p.cu[n];
   const int rows = nw * (a.p.Hq / a.cache.Hkv);
-  return AttnRows{rows >= a.least && rows <= a.most ? rows : 0, a.cache.lens[n] - nw + 1, a.cache.width * a.cache.page_size};
+  return AttnRows{rows >= a.least && rows <= a.most ? rows : 0, kv_len(a.cache, n) - nw + 1, a.cache.width * a.cache.page_size};
 }
 
 // inclusive sum over the block's threads

@@ -45,6 +45,10 @@ struct KvCache {
   int32_t width, num_pages, page_size, Hkv;
 };
 
+// Tokens of a sequence, the new ones included.  A negative number holds none, as 0 does; positions counted back from it stay
+// within int32.
+__device__ __forceinline__ int kv_len(const KvCache& c, int n) { return max(c.lens[n], -(1 << 30)); }
+
 // Bytes of the pool before the tile of (head h, position p) of sequence n, or
 // -1 when p has no page: past the table's row, or a page id outside the pool.
 __device__ __forceinline__ int64_t kv_tile_at(const KvCache& c, int D, int n, int p, int h) {

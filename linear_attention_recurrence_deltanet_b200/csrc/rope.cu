@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (threadIdx.x < nt) {
     // (a cu_seqlens that leaves a token out is not the host's copy: the token may go wrong, not the address)
     const int n = s_seq[threadIdx.x] = min((uint32_t)s_seq[threadIdx.x], (uint32_t)a.N - 1u);
-    s_at[threadIdx.x] = cache.lens[n] - (a.cu[n + 1] - (t0 + threadIdx.x));  // position in the cache; negative: not stored
+    s_at[threadIdx.x] = kv_len(cache, n) - (a.cu[n + 1] - (t0 + threadIdx.x));  // position in the cache; negative: not stored
   }
   if (!a.pos) __syncthreads();
   make_angles(plan, cs, half, nt, [&](int t, int axis) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
     const int t = (int)(u / upt), h = (int)(u - (int64_t)t * upt) * hpw + sub;
     if (h >= cache.Hkv) continue;
-    const int n = seq_of(cu, N, t), p = cache.lens[n] - (cu[n + 1] - t);
+    const int n = seq_of(cu, N, t), p = kv_len(cache, n) - (cu[n + 1] - t);
     float k[8], v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) k[i] = v[i] = 0.0f;

@@ -767,3 +767,23 @@ def test_attention_short_sequences_beside_prompts(d, hq, hkv, short):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o2, o) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("pad", [-1, -5, -2 ** 31])
+@pytest.mark.parametrize("new", [1, 3, 70])
+def test_negative_lengths_are_padding(pad, new):
+    """A padding row's length may be any number up to 0: nothing is stored, seen or reported."""
+    c = Case([new, 2], [20, 9], 2, 2, 64, 16, "bf16", seed=91).fill()
+    c.d_lens[0] = pad
+    before = c.pool.clone()
+    k, v = (torch.randn(c.T, 2, 64, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in (1, 2))
+    k[new:], v[new:] = c.k[1][-2:].cuda(), c.v[1][-2:].cuda()  # what the other sequence holds already
+    gdn.kv_append(c.cfg, None, None, k, v, None, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, None)
+    assert torch.equal(c.pool, before)
+    ko, vo = torch.full_like(k, 5.0), torch.full_like(v, 5.0)
+    gdn.kv_read(c.cfg, c.d_cu, c.cu, c.d_lens, c.pool, c.d_table, ko, vo)
+    assert (ko[:new] == 0).all() and (vo[:new] == 0).all() and (ko[new:] != 0).any()
+    o, lse = c.attention()
+    assert (o[:new] == 0).all() and (lse[:new] == -math.inf).all()
+    assert gdn.device_status() == 0
+    c.check(o, lse, skip=(0,))
