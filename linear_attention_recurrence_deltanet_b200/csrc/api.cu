@@ -876,7 +876,7 @@ gdn_status check_cache(const gdn_attn_config* cfg, const gdn_kv_cache* c, gdn::K
     return fail(GDN_E_INVAL, "cache.kv_lens is NULL or not 4-byte aligned");
   if (c->num_pages <= 0 || c->pages_per_seq <= 0)
     return fail(GDN_E_INVAL, "num_pages %d and pages_per_seq %d must be positive", c->num_pages, c->pages_per_seq);
-  if ((int64_t)c->pages_per_seq * cfg->page_size > 0x7ffffff0LL)
+  if ((int64_t)c->pages_per_seq * cfg->page_size > 0x7fffff80LL)  // (rounded up to 128 keys it is an int32 still)
     return fail(GDN_E_INVAL, "pages_per_seq %d x page_size %d passes int32", c->pages_per_seq, cfg->page_size);
   *out = gdn::KvCache{(unsigned char*)c->pool, c->page_table, c->kv_lens, (int64_t)kv_page_bytes(cfg),
                       c->pages_per_seq, c->num_pages, cfg->page_size, cfg->num_kv_heads};

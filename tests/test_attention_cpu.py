@@ -323,3 +323,17 @@ def test_linear_sizes_past_the_limit_are_refused():
         refused(L.gdn_linear_q4(1, h.p, M, 64, h.p, 16, 64, h.p, h.p, 1 << 40, None), f"M = {M}", -2)
     assert size.value == 7 and h.untouched()
     assert L.gdn_q4_packed_bytes(2 ** 30, 8, 32, ctypes.byref(size)) == 0 and size.value == 2 ** 30 * (32 + 8 + 4)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the valid call is for a machine without a GPU")
+def test_table_rows_up_to_the_last_whole_tile_of_int32():
+    h, cu = Host(), np.array([0, 1], np.int32)
+    cfg = gdn.make_attn_config(1, 1, 64, page_size=16)
+
+    def read(width):
+        c = gdn.KvCache(h.p, h.p, h.p, 1, width)
+        return gdn.lib().gdn_kv_read(ctypes.byref(cfg), h.p, cu.ctypes.data, 1, ctypes.byref(c), h.p, h.p, None)
+
+    refused(read((2 ** 31 - 16) // 16), "int32")
+    refused(read((2 ** 31 - 112) // 16), "int32")
+    refused(read((2 ** 31 - 128) // 16), status=-9)  # valid, but no device here
