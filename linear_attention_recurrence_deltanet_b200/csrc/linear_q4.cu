@@ -1015,12 +1015,15 @@ cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* bi
                            int32_t group, void* packed, cudaStream_t stream) {
   const Q4Layout L = q4_layout(N, K, group);
   const int64_t blocks = ((int64_t)L.row_off / 4 + 255) / 256;
-  LaunchScope scope(GDN_K_Q4_PACK, stream);
-  q4_pack_kernel<<<(unsigned)(blocks < 148 * 64 ? blocks : 148 * 64), 256, 0, stream>>>(
-      (const unsigned char*)codes, (const unsigned short*)scales, (const unsigned short*)biases, N, K, group,
-      (int64_t)L.groups * group / 2, L, (uint32_t*)packed);
+  {
+    LaunchScope scope(GDN_K_Q4_PACK, stream);
+    q4_pack_kernel<<<(unsigned)(blocks < 148 * 64 ? blocks : 148 * 64), 256, 0, stream>>>(
+        (const unsigned char*)codes, (const unsigned short*)scales, (const unsigned short*)biases, N, K, group,
+        (int64_t)L.groups * group / 2, L, (uint32_t*)packed);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  LaunchScope scope(GDN_K_Q4_PACK, stream);
   q4_rows_kernel<<<(unsigned)(L.tiles * kTile / 8), 256, 0, stream>>>((const unsigned short*)scales, (const unsigned short*)biases, N,
                                                             L, (float*)((unsigned char*)packed + L.row_off));
   return cudaGetLastError();

@@ -325,3 +325,19 @@ def test_linear_q4_refuses_a_weight_with_too_few_bytes(N, K, group):
     kept = gdn.Q4Weight(w.data, 128, 128, 64)
     x = torch.randn(2, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
     assert torch.equal(run(x, kept), run(x, w))
+
+
+def test_launches_are_counted_one_by_one():
+    """The launch counter and the profiler see every kernel of a call."""
+    gdn.profiler_reset()
+    gdn.profiler_enable(True)
+    before = gdn.launch_count()
+    _, _, _, w = weight(300, 256, 64, 11)
+    assert gdn.launch_count() - before == 2  # the codes and scales, the rows' powers of two
+    run(torch.zeros(1, 256, dtype=torch.bfloat16, device="cuda"), w)
+    assert gdn.launch_count() - before == 3
+    run(torch.zeros(300, 256, dtype=torch.bfloat16, device="cuda"), w)
+    assert gdn.launch_count() - before == 5  # x as the products' operand, the products
+    gdn.profiler_enable(False)
+    assert [gdn.profiler_read(k)[0] for k in (gdn.K.Q4_PACK, gdn.K.LINEAR_Q4, gdn.K.X_HALF)] == [2, 2, 1]
+    gdn.profiler_reset()
