@@ -341,3 +341,21 @@ def test_launches_are_counted_one_by_one():
     gdn.profiler_enable(False)
     assert [gdn.profiler_read(k)[0] for k in (gdn.K.Q4_PACK, gdn.K.LINEAR_Q4, gdn.K.X_HALF)] == [2, 2, 1]
     gdn.profiler_reset()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(9, 47, 328), (16, 512, 2048), (17, 130, 264), (24, 257, 1096), (31, 64, 512), (32, 300, 520),
+                                   (32, 3200, 3840), (24, 3100, 3840)])
+def test_linear_q4_exact_rows_keep_their_promise(group, M, N, K):
+    """9 to 16 rows of bf16, and to 32 for small weights (no workspace says that they are): nothing but sums is rounded."""
+    assert gdn.linear_q4_workspace_size(M, N, K, group) == 0
+    code, scale, bias, w = weight(N, K, group, M + N + K)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).bfloat16()
+    ref, mag, _ = product(x, code, scale, bias, group)
+    assert ((run(x.cuda(), w).cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 3200, 3904), (32, 3300, 3840), (33, 3200, 3840)])
+def test_linear_q4_rows_past_the_border_round_weights(M, N, K):
+    assert gdn.linear_q4_workspace_size(M, N, K, 64) > 0
+    test_linear_q4_against_float64("bf16", 64, M, N, K)
