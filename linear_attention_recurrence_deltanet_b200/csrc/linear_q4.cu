@@ -689,7 +689,7 @@ struct Expand {
 
 // The TMEM accesses below are .sync.aligned and, unlike those of tc.cuh, do not reconverge the warp themselves, which would
 // cost 3 % of the kernel: what only some lanes do ends with a __syncwarp() before them.
-// products with the weights (A) in TMEM; b: as in mma_f16_low
+// products with the weights (A) in TMEM; b: the lower half of the descriptor of x
 __device__ __forceinline__ void mma_ts_low(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n.reg .pred p;\n.reg .b64 y;\nmov.b64 y, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"

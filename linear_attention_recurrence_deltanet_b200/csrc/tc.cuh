@@ -73,15 +73,9 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
           d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// The same with descriptors whose upper half is that of a 128-byte swizzle with 1024 bytes between 8-row groups: only
-// the lower halves (address and leading offset) are registers.
+// The upper half of a descriptor with a 128-byte swizzle and 1024 bytes between 8-row groups; address and leading offset are
+// the lower one.
 constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
-__device__ __forceinline__ void mma_f16_low(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 x, y;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHigh));
-}
 __device__ __forceinline__ void mma_commit(uint64_t* mbar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mbar))
                : "memory");
