@@ -175,15 +175,14 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                         int N, T* __restrict__ y, int S, int32_t* status, uint32_t zero) {
   constexpr bool F32 = sizeof(T) == 4;
   const CodePair<F32> code_pair(zero);
-  constexpr int MT = 1;
   constexpr int P = F32 ? 3 : 1;                 // bf16 parts of x
   constexpr int SUB = G == 32 ? 2 : 1;           // groups of a block
   constexpr int LG = G == 32 ? 5 : G == 64 ? 6 : 7;
-  static_assert(kSmallWarps * MT * 8 * kRedLd * 4 <= kSmallSmem, "the join uses the rings");
+  static_assert(kSmallWarps * 8 * kRedLd * 4 <= kSmallSmem, "the join uses the rings");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t s_full[kSmallWarps][kSmallSlots];
-  __shared__ float s_sum[MT * 8 * kTile];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3, m0 = (int)blockIdx.y * MT * 8;
+  __shared__ float s_sum[8 * kTile];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3, m0 = (int)blockIdx.y * 8;
   const int rank = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
   const int step = S * kSmallWarps, first = rank * kSmallWarps + warp;  // this warp's blocks
 
@@ -196,64 +195,54 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     for (int i = 0, b = first; i < kSmallSlots && b < L.blocks; ++i, b += step)
       stream.fetch(ring + i * kSmallSlot, kBlockBytes, b, 1, &s_full[warp][i]);
 
-  float acc[kStrips][MT][4];
+  float acc[kStrips][4];
 #pragma unroll
   for (int i = 0; i < kStrips; ++i)
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.0f;
-  const T* xp[MT];  // this lane's channels of block 0
-  int kmax[MT];     // channels from there on that are there
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + t * 8 + r;
-    kmax[t] = m < M ? K - q * 16 : 0;
-    xp[t] = x + (int64_t)(m < M ? m : 0) * K + q * 16;
-  }
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+  const bool here = m0 + r < M;
+  const int kmax = here ? K - q * 16 : 0;  // channels of this lane from block 0 on
+  const T* xp = x + (int64_t)(here ? m0 + r : 0) * K + q * 16;
 
   int slot_i = 0;
   uint32_t phase = 0;
   for (int b = first; b < L.blocks; b += step) {
     // x as B fragments, and its sums over the groups as the product with ones
-    uint32_t f[MT][P][8];
-    float xs[SUB][MT][4];
+    uint32_t f[P][8];
+    float xs[SUB][4];
+    const T* src = xp + (int64_t)b * kBlock;
+    const int left = kmax - b * kBlock;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const T* src = xp[t] + (int64_t)b * kBlock;
-      const int left = kmax[t] - b * kBlock;
+    for (int h = 0; h < (F32 ? 4 : 2); ++h) {
+      const uint4 v = (F32 ? 4 : 8) * h < left ? ld16(src + (F32 ? 4 : 8) * h) : make_uint4(0, 0, 0, 0);
+      if constexpr (!F32) {
+        f[0][4 * h] = v.x, f[0][4 * h + 1] = v.y, f[0][4 * h + 2] = v.z, f[0][4 * h + 3] = v.w;
+      } else {
+        float e[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
 #pragma unroll
-      for (int h = 0; h < (F32 ? 4 : 2); ++h) {
-        const uint4 v = (F32 ? 4 : 8) * h < left ? ld16(src + (F32 ? 4 : 8) * h) : make_uint4(0, 0, 0, 0);
-        if constexpr (!F32) {
-          f[t][0][4 * h] = v.x, f[t][0][4 * h + 1] = v.y, f[t][0][4 * h + 2] = v.z, f[t][0][4 * h + 3] = v.w;
-        } else {
-          float e[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+        for (int pt = 0; pt < P; ++pt)
 #pragma unroll
-          for (int pt = 0; pt < P; ++pt)
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const uint32_t z = bf16x2(e[2 * d], e[2 * d + 1]);
-              f[t][pt][2 * h + d] = z;
-              e[2 * d] -= lo_bf16(z), e[2 * d + 1] -= hi_bf16(z);
-            }
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < SUB; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xs[g][t][e] = 0.0f;
-#pragma unroll
-      for (int pt = 0; pt < P; ++pt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int g = 0; g < SUB; ++g) {  // groups of 32: lanes q < 2 hold the first, q >= 2 the second
-            const bool on = SUB == 1 || (q >> 1) == g;
-            mma(xs[g][t], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, on ? f[t][pt][2 * j] : 0u,
-                on ? f[t][pt][2 * j + 1] : 0u);
+          for (int d = 0; d < 2; ++d) {
+            const uint32_t z = bf16x2(e[2 * d], e[2 * d + 1]);
+            f[pt][2 * h + d] = z;
+            e[2 * d] -= lo_bf16(z), e[2 * d + 1] -= hi_bf16(z);
           }
+      }
     }
+#pragma unroll
+    for (int g = 0; g < SUB; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xs[g][e] = 0.0f;
+#pragma unroll
+    for (int pt = 0; pt < P; ++pt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int g = 0; g < SUB; ++g) {  // groups of 32: lanes q < 2 hold the first, q >= 2 the second
+          const bool on = SUB == 1 || (q >> 1) == g;
+          mma(xs[g], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, on ? f[pt][2 * j] : 0u,
+              on ? f[pt][2 * j + 1] : 0u);
+        }
     if (!tc::mbar_wait_warp(&s_full[warp][slot_i], phase)) {
       set_status(status, kStatusWaitTimeout | (GDN_K_LINEAR_Q4 << 8));
       break;
@@ -272,27 +261,22 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       }
 #pragma unroll
       for (int g = 0; g < SUB; ++g) {
-        float p[MT][4];
+        float p[4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int pt = 0; pt < P; ++pt)
 #pragma unroll
-          for (int pt = 0; pt < P; ++pt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const bool on = SUB == 1 || (q >> 1) == g;
-              const uint32_t f0 = on ? f[t][pt][2 * j] : 0u, f1 = on ? f[t][pt][2 * j + 1] : 0u;
-              if (pt == 0 && j == 0) mma0(p[t], a[0][0], a[0][1], a[1][0], a[1][1], f0, f1);
-              else mma(p[t], a[2 * j][0], a[2 * j][1], a[2 * j + 1][0], a[2 * j + 1][1], f0, f1);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const bool on = SUB == 1 || (q >> 1) == g;
+            const uint32_t f0 = on ? f[pt][2 * j] : 0u, f1 = on ? f[pt][2 * j + 1] : 0u;
+            if (pt == 0 && j == 0) mma0(p, a[0][0], a[0][1], a[1][0], a[1][1], f0, f1);
+            else mma(p, a[2 * j][0], a[2 * j][1], a[2 * j + 1][0], a[2 * j + 1][1], f0, f1);
+          }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t sw = sc[g * kTile + i * kStrip + 8 * h];
           const float s = lo_bf16(sw), z = fmaf(F32 ? 8.0f : -128.0f, s, hi_bf16(sw));
 #pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              acc[i][t][2 * h + e] = fmaf(s, p[t][2 * h + e], fmaf(z, xs[g][t][e], acc[i][t][2 * h + e]));
+          for (int e = 0; e < 2; ++e) acc[i][2 * h + e] = fmaf(s, p[2 * h + e], fmaf(z, xs[g][e], acc[i][2 * h + e]));
         }
       }
     }
@@ -312,10 +296,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 #pragma unroll
   for (int i = 0; i < kStrips; ++i)
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(warp * MT * 8 + t * 8 + 2 * q + (e & 1)) * kRedLd + i * kStrip + r + 8 * (e >> 1)] = acc[i][t][e];
+    for (int e = 0; e < 4; ++e) red[(warp * 8 + 2 * q + (e & 1)) * kRedLd + i * kStrip + r + 8 * (e >> 1)] = acc[i][e];
   __syncthreads();
   bool odd = false;
   auto put = [&](int i, float v) {
@@ -324,17 +305,17 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     odd |= !isfinite(v);
     y[(int64_t)m * N + n] = from_f<T>(v);
   };
-  for (int i = threadIdx.x; i < MT * 8 * kTile; i += kSmallThreads) {
+  for (int i = threadIdx.x; i < 8 * kTile; i += kSmallThreads) {
     if (m0 + i / kTile >= M) break;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) v += red[(w * MT * 8 + i / kTile) * kRedLd + i % kTile];
+    for (int w = 0; w < kSmallWarps; ++w) v += red[(w * 8 + i / kTile) * kRedLd + i % kTile];
     if (S == 1) put(i, v);
     else s_sum[i] = v;
   }
   auto mend = [&](int first, int step) {
     if (!odd) return;
-    for (int i = first; i < MT * 8 * kTile; i += step) {
+    for (int i = first; i < 8 * kTile; i += step) {
       const int n = tile * kTile + i % kTile, m = m0 + i / kTile;
       if (n < N && m < M && !isfinite(to_f(y[(int64_t)m * N + n])))
         y[(int64_t)m * N + n] = from_f<T>(by_definition(x + (int64_t)m * K, K, packed, L, LG, n));
@@ -343,7 +324,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   if (S == 1) return mend(threadIdx.x, kSmallThreads);
   tc::cluster_sync();
   if (rank == 0)
-    for (int i = threadIdx.x; i < MT * 8 * kTile; i += kSmallThreads) {
+    for (int i = threadIdx.x; i < 8 * kTile; i += kSmallThreads) {
       if (m0 + i / kTile >= M) break;
       float v = s_sum[i];
       for (int o = 1; o < S; ++o) {
@@ -1031,11 +1012,9 @@ cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* bi
 
 namespace {
 
-
 // bf16 io: whether the products go by linear_rows_kernel.  17 to 32 rows do where the weight is small (1024 x 2048: 5.9
 // against 12 us; 5120 x 6144: 27 us against 22).
 bool few_rows(int32_t M, const Q4Layout& L) { return M <= 16 || (M <= 32 && (int64_t)L.tiles * L.blocks <= 1500); }
-  // bf16 io: more rows run linear_big_kernel
 
 // Blocks a tile: a block for each SM, while every warp keeps two blocks of K.  (Twice as many put 320 blocks of 5120 x
 // 6144 in two rounds: one row 11.9 us against 9.3.)
