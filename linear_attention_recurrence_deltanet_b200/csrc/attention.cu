@@ -30,7 +30,9 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroupUnits = 20;  // what a group costs beside its tiles, in tiles
-constexpr int kMinUnits = 20;    // the least quota
+// the least quota: short contexts are spread over more blocks, whose parts have to be joined (one token over 2000 keys, 24 / 2
+// heads of 128: 4 14.1 us, 7 14.6, 10 15.0, 20 16.8; over 8000: 16.8, 16.0, 16.0, 17.4; 16 of them over 300: 16.4, 16.0, 17.2, 18.7)
+constexpr int kMinUnits = 7;
 
 constexpr int stages(int D) { return D == 64 ? 8 : 4; }
 // what registers and shared memory allow (all_fit below; a third block of 256 x 8 rows waited for a place, and every quota
@@ -681,8 +683,12 @@ AttnWorkspace ws_at(const WsLayout& w, void* ws) {
   return AttnWorkspace{(float*)(b + w.o), (float2*)(b + w.ml), (int4*)(b + w.split)};
 }
 
-// bf16 io: sequences with more rows a key/value head than this take the long row tiles (16 / 2 heads of 256 over 20000
-// tokens: 72 rows 45 us here and 55 there, 136 rows 65 and 56)
+// bf16 io: sequences with more rows a key/value head than this take the long row tiles.  One border a head size, since a
+// sequence's rounding goes by it and must not depend on the call's other sequences; which side is faster does.  16 / 2 heads,
+// short | long tiles, us:
+//   D = 128, one sequence over 4000 keys: 56 rows 18 | 27, 96 22 | 28, 192 23 | 38; 16 of them: 40 rows 41 | 40, 56 50 | 41, 72 58 | 41
+//   D = 64, one over 20000: 56 rows 19 | 35, 192 32 | 54; 16 of them: 40 rows 81 | 89, 56 104 | 89, 72 126 | 90
+//   D = 256, one over 20000: 56 rows 36 | 54, 128 57 | 57, 160 58 | 53; 16 of them: 24 rows 143 | 135, 72 328 | 143, 128 514 | 152
 constexpr int prefill_from(int D) { return D <= 128 ? 64 : 128; }
 
 // What a call's sequences ask for: of those with up to `border` rows a key/value head, their rows, how many and the longest;
