@@ -1012,8 +1012,11 @@ cudaError_t launch_q4_pack(const void* codes, const void* scales, const void* bi
 
 namespace {
 
-// bf16 io: whether the products go by linear_rows_kernel.  17 to 32 rows do where the weight is small (1024 x 2048: 5.9
-// against 12 us; 5120 x 6144: 27 us against 22).
+// bf16 io: whether the products go by the kernels for few rows, which round no weight.  17 to 32 rows do where the weight is
+// small; the border is in 128 x 64 blocks.  us, exact | rounded (linear_big_kernel), 17 and 32 rows: 1024 x 2048 (256 blocks)
+// 6.0 | 11.3, 7.0 | 11.3; 2048 x 2048 (512) 10.9 | 12.2, 12.7 | 12.5; 4096 x 2048 (1024) 16.4 | 12.9, 18.8 | 13.5; 2560 x 5120
+// (1600) 17.8 | 14.7, 19.9 | 15.8; 3840 x 3840 (1800) 14.9 | 15.9, 16.9 | 16.7; 5120 x 6144 (3840) 27.7 | 20.4, 30.9 | 20.8.
+// Between 512 and 1500 up to 40 % are paid for exact products.
 bool few_rows(int32_t M, const Q4Layout& L) { return M <= 16 || (M <= 32 && (int64_t)L.tiles * L.blocks <= 1500); }
 
 // Blocks a tile: a block for each SM, while every warp keeps two blocks of K.  (Twice as many put 320 blocks of 5120 x
