@@ -501,7 +501,8 @@ GDN_API gdn_status gdn_attention(const gdn_attn_config* cfg, const void* q, int6
  *   [N, G * group / 2] bytes (G = ceil(K / group)): channel 2i in the low half
  *   of byte i, codes past K ignored; scales, biases [N, G] bf16.  packed:
  *   gdn_q4_packed_bytes() bytes, 16-byte aligned.
- * gdn_linear_q4: workspace gdn_linear_q4_workspace_size() bytes for the same
+ * gdn_linear_q4: Y overlaps neither X nor the workspace;
+ *   workspace gdn_linear_q4_workspace_size() bytes for the same
  *   (M, N, K, group, io_dtype), 256-byte aligned (NULL when that is 0); it needs
  *   no initial contents and holds nothing between calls, so calls that may run
  *   at the same time need one each. */

@@ -337,3 +337,18 @@ def test_table_rows_up_to_the_last_whole_tile_of_int32():
     refused(read((2 ** 31 - 16) // 16), "int32")
     refused(read((2 ** 31 - 112) // 16), "int32")
     refused(read((2 ** 31 - 128) // 16), status=-9)  # valid, but no device here
+
+
+def test_linear_refuses_an_output_over_its_input():
+    h = Host()
+
+    def lin(y, io=1, M=4, N=64, K=64):
+        return gdn.lib().gdn_linear_q4(io, h.p + 4096, M, K, h.p + 32768, N, 64, h.p + y, h.p, 1 << 30, None)
+
+    for y in (4096, 4096 + 4 * 64 * 2 - 2, 4096 - 4 * 64 * 2 + 2):
+        refused(lin(y), "overlaps")
+    refused(lin(4096 + 4 * 64 * 4 - 4, io=0), "overlaps")
+    if not torch.cuda.is_available():
+        for y in (4096 + 4 * 64 * 2, 4096 - 4 * 64 * 2):
+            refused(lin(y), status=-9)  # side by side: valid, but no device here
+    assert h.untouched()
