@@ -1144,13 +1144,15 @@ gdn_status gdn_linear_q4(int32_t io_dtype, const void* x, int32_t M, int32_t K, 
     if ((s = check_ptr(x, "x")) != GDN_OK || (s = check_ptr(packed, "packed")) != GDN_OK) return s;
     if (!y || ((uintptr_t)y & (io_dtype == GDN_BF16 ? 1u : 3u)))
       return fail(GDN_E_INVAL, "y is NULL or not aligned to its element size");
-    const uintptr_t es = io_dtype == GDN_BF16 ? 2 : 4, xb = (uintptr_t)x, yb = (uintptr_t)y;
-    if (xb < yb + (uintptr_t)M * N * es && yb < xb + (uintptr_t)M * K * es)
-      return fail(GDN_E_INVAL, "y overlaps x");  // blocks read all of a row while others write theirs
   }
   if ((s = check_ws(workspace, workspace_bytes, gdn::linear_q4_ws_bytes(M, N, K, group, io_dtype == GDN_BF16))) !=
       GDN_OK)
     return s;
+  if (M > 0 && N > 0) {
+    const uintptr_t es = io_dtype == GDN_BF16 ? 2 : 4, xb = (uintptr_t)x, yb = (uintptr_t)y;
+    if (xb < yb + (uintptr_t)M * N * es && yb < xb + (uintptr_t)M * K * es)
+      return fail(GDN_E_INVAL, "y overlaps x");  // blocks read all of a row while others write theirs
+  }
   int dev = 0;
   if ((s = check_device(&dev)) != GDN_OK) return s;
   if (M == 0 || N == 0) return GDN_OK;
