@@ -432,7 +432,8 @@ GDN_API gdn_status gdn_project_out(const gdn_config* cfg, const void* o, int32_t
  *   has more than 64 rows (tokens x Hq / Hkv; 128 for D = 256), the values too,
  *   whatever the call's other sequences have; fp32 io keeps 24 bits of everything.
  *   Workspace: gdn_attention_workspace_size() bytes for the same (cfg, total
- *   tokens, num_seqs), 256-byte aligned; it needs no initial contents and holds
+ *   tokens, num_seqs), 256-byte aligned (enough for any lengths of the sequences,
+ *   so for a prompt among them); it needs no initial contents and holds
  *   nothing between calls, so calls that may run at the same time need one each.
  *   kv_lens and page_table are read on the device only, so a captured call
  *   follows their contents; cu_seqlens is fixed by the host copy.

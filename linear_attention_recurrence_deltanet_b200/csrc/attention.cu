@@ -9,7 +9,8 @@
 // with the codes less 8 exact in 16 bits.  bf16 io: fp16 operands, query rows brought
 // below 2^8 by a power of two each (exactly, but for elements 2^-22 of the row's
 // largest), and nothing rounded but p_t s_t, to fp16 under a power of two of the
-// warp's largest s_t: 2^-11 of it.  fp32 io: bf16 operands, queries and p_t s_t in
+// warp's largest s_t: 2^-11 of it, or, where it is below 2^-17 of that largest, 2^-28
+// of the largest.  The outputs' bf16 rounds by 2^-8; a second part of p_t s_t cost 8 %.  fp32 io: bf16 operands, queries and p_t s_t in
 // three parts.
 //
 // Keys and values are the A operand (16 keys x 16 channels, 16 channels x 16
@@ -734,7 +735,7 @@ cudaError_t run(const AttnProblem& p, const KvCache& cache, const Split& s, void
 template <int D>
 cudaError_t run_d(const AttnProblem& p, const KvCache& c, const Split& s, void* ws, int32_t* status, cudaStream_t st) {
   if (!p.bf16) return run<float, D, 16>(p, c, s, ws, status, st);
-  // 8-row tiles leave the other half of the products' rows to the low parts of the probabilities
+  // a tile of 8 rows is half the products of one of 16, whose second half would be empty
   if (s.longest <= 8) return run<__nv_bfloat16, D, 8>(p, c, s, ws, status, st);
   return run<__nv_bfloat16, D, 16>(p, c, s, ws, status, st);
 }

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 
 // 9 to 32 rows of bf16 io (8 MT).  A warp takes SPW of the tile's eight strips, so that its sums stay in registers, and
 // every KW-th 64-channel block; the block copies x of KW blocks at a time, in the order of B fragments, some steps ahead
-// (5120 x 6144, 16 rows: 16 us, with x read by each warp 26).
+// (5120 x 6144, 16 rows: 16.8 us, 18 with weights from memory; with x read by each warp 26).
 constexpr int strips_per_warp(int MT) { return MT == 2 ? 8 : 4; }
 constexpr int rows_slots(int MT) { return MT == 2 ? 2 : 4; }
 constexpr int rows_kw(int MT) { return strips_per_warp(MT); }  // eight warps / (8 / SPW)
@@ -561,9 +561,10 @@ __global__ void __launch_bounds__(kSmallThreads, rows_blocks(MT, G))
 // sums go to the workspace, and the block that comes last adds them in the order
 // of the slices.
 //
-// Measured (x_half included): 2048 rows of 5120 -> 8192 150 us, 1150 TFLOP/s (weights in
+// Measured (x_half included): 2048 rows of 5120 -> 8192 148 us, 1160 TFLOP/s (weights in
 // shared memory 167, an output loop of nine instructions a value 175, rounds chosen
-// without the output's cost 164); 64 rows of 6144 -> 5120 23 us (25).  What is left
+// without the output's cost 164); 64 rows of 6144 -> 5120 24 us (25), 26 with weights
+// from memory.  What is left
 // beside the products, which keep the tensor pipe active for 66 %: the output of the
 // single accumulator, start, x_half and the slices' join; for few rows the handshake
 // of a step and 9 us of start, x_half and join.  A pair of

@@ -186,7 +186,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, uint64_t
 // The wait of a whole warp, all lanes together: true for all lanes or for none.  A converged warp is suspended in the
 // instruction until the phase ends (about 110 cycles from the arrival) or something else arrives, 3900 cycles at most; a
 // lane that polls alone is not, and its polls take the issue slots of the warps that work.  For the same reason the limit
-// counts tries, the loop's cheapest measure: 20 to 3900 cycles each, so kWaitTries are 50 ms at least, some seconds at most.
+// counts tries, the loop's cheapest measure: 20 to 3900 cycles each, so kWaitTries are 40 ms at least, some seconds at most.
 constexpr int kWaitTries = 1 << 22;
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* m, uint32_t parity, int tries = kWaitTries) {
   bool ok = mbar_try_wait(m, parity);
