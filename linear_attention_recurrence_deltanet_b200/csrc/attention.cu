@@ -10,8 +10,8 @@
 // below 2^8 by a power of two each (exactly, but for elements 2^-22 of the row's
 // largest), and nothing rounded but p_t s_t, to fp16 under a power of two of the
 // warp's largest s_t: 2^-11 of it, or, where it is below 2^-17 of that largest, 2^-28
-// of the largest.  The outputs' bf16 rounds by 2^-8; a second part of p_t s_t cost 8 %.  fp32 io: bf16 operands, queries and p_t s_t in
-// three parts.
+// of the largest.  The outputs' bf16 rounds by 2^-8; a second part of p_t s_t cost 8 %.
+// fp32 io: bf16 operands, queries and p_t s_t in three parts.
 //
 // Keys and values are the A operand (16 keys x 16 channels, 16 channels x 16
 // keys), eight query rows the B operand: a lane then scales two keys for all rows,

@@ -30,12 +30,13 @@
 // values of t once P V of t - 1 is.
 //
 // Measured, 2048 tokens over 6144, 24 / 2 heads: D = 128 287 us (floor 107, by the
-// products), D = 256 508 us (floor 214; 2310 with attn_kernel), D = 64 246 us.  D = 128: a tile's chain of
-// products, wake-ups, maximum and exponentials is longer than the other tile's work.
+// products), D = 256 508 us (floor 214; 2310 with attn_kernel), D = 64 246 us.
+// D = 128: a tile's chain of products, wake-ups, maximum and exponentials is longer than
+// the other tile's work.
 // D = 256: the chain is a tile's expansion, with shared memory half taken by operands.
-// Tried there, against 487 then: two threads a row 497, the keys in two parts 515, sixteen warps that
-// expand half the channels each 494, eight for keys and eight for values 604 (products
-// and stores then meet in shared memory).
+// Tried there, against 487 then: two threads a row 497, the keys in two parts 515,
+// sixteen warps that expand half the channels each 494, eight for keys and eight for
+// values 604 (products and stores then meet in shared memory).
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
