@@ -673,8 +673,10 @@ gdn_status gdn_prefill_indexed(const gdn_config* cfg, const gdn_params* params, 
   const bool bf16 = cfg->io_dtype == GDN_BF16;
   const size_t base = prefill_ws_bytes(d, prefill_path(d, cfg, chunk_size, flags), total, num_seqs, chunk_size);
   const IndexedLayout L = indexed_layout(d, bf16, base, num_seqs);
-  if (workspace_bytes < L.total || !workspace)
-    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes at %p, need %zu", workspace_bytes, workspace, L.total);
+  // what the query reports, which covers every path: whether a call is refused does not depend on the path it takes
+  const size_t need = indexed_layout(d, bf16, prefill_ws_query(d, cfg, total, num_seqs, chunk_size), num_seqs).total;
+  if (workspace_bytes < need || !workspace)
+    return fail(GDN_E_WORKSPACE, "workspace of %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
   if (((uintptr_t)workspace & 255u) != 0) return fail(GDN_E_WORKSPACE, "workspace is not 256-byte aligned");
   int dev = 0;
   if ((s = check_device(&dev)) != GDN_OK) return s;

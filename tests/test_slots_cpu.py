@@ -118,3 +118,20 @@ def test_indexed_prefill_rejects_before_launch():
         assert e.value.name == status, (kw, e.value)
     for k, v in t.items():
         assert np.array_equal(v.view, snap[k]), k
+
+
+@pytest.mark.parametrize("offset", [0, 16])
+def test_indexed_prefill_asks_for_the_bytes_its_query_reports(offset):
+    """On any path and whatever the workspace's alignment: one byte less is refused for its size."""
+    geo = gi.Geometry()
+    cfg = gdn.make_config(geo)
+    t, params = bufs(geo, 2, 3, T=16)
+    cu_dev, ws = FakeTensor(12), FakeTensor(1 << 12)
+    ws.offset = -ws.view.ctypes.data % 256 + offset
+    for chunk in (16, 64, 128):
+        need = gdn.prefill_indexed_workspace_size(cfg, 16, 2, chunk)
+        for flags in (0, gdn.PREFILL_RECURRENT, gdn.PREFILL_AFFINE):
+            with pytest.raises(gdn.GdnError) as e:
+                gdn.prefill_indexed(cfg, params, t["qkv"], t["z"], t["a"], t["b"], cu_dev, [0, 9, 16], t["idx"], 3, chunk,
+                                    flags, t["conv"], t["state"], t["o"], ws, workspace_bytes=need - 1, stream=0)
+            assert e.value.name == "GDN_E_WORKSPACE" and f"need {need}" in str(e.value)
